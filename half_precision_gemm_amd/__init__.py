@@ -48,6 +48,19 @@ importing this package raises.
         (m, n) float16 whose row j is column j of B; Out is (m, n) float32
         in the same convention.
 
+    linear(X, W, Y, bias=None, act=ACT_NONE, residual=None, Z=None, work=None)
+        Y = act(X·Wᵀ + bias) + residual, the pre-activation saved in Z (16
+        bits, or an 8-bit checkpoint); ACT_NONE, ACT_RELU, ACT_GELU,
+        ACT_GELU_TANH or ACT_SILU; float16 or bfloat16.
+
+    linear_grad(dY, W, X, Z=None, act=ACT_NONE, dX=None, dW=None, dbias=None,
+                accumulate=False, work=None)
+        the gradients of linear; X and Z may be 8-bit checkpoints.
+
+    checkpoint8_write(X, codes, scales), checkpoint8_read(codes, scales, X)
+        an activation as e4m3 codes with one power-of-two scale for every 32
+        columns of a row, and back.
+
     trsm_lower_trans(A, B, Out, alpha=1.0, leaf=256, work=None)
         Out = alpha·A⁻ᵀ·B (the X with Aᵀ·X = alpha·B), A lower triangular,
         same conventions as trmm_lower_trans.  `work` is a device uint8
@@ -511,3 +524,9 @@ def trmm_plan(n: int, leaf: int = 256):
     buf = (_i64 * (4 * cnt))()
     lib.hg_trmm_plan(n, leaf, buf, cnt)
     return [tuple(buf[4 * i:4 * i + 4]) for i in range(cnt)]
+
+
+from .layer import (ACT_GELU, ACT_GELU_TANH, ACT_SILU, E4M3_BLOCK, EXPORTS_LINEAR,  # noqa: E402,F401
+                    checkpoint8_empty, checkpoint8_read, checkpoint8_write, linear, linear_grad,
+                    linear_grad_workspace, linear_grad_workspace_size, linear_workspace,
+                    linear_workspace_size)

@@ -1,0 +1,519 @@
+// Internal interface of the linear layer (include/hgemm_linear.h): the
+// parameters that the host passes to the kernels, and the device code the
+// kernels share.  Not part of the public ABI.
+#pragma once
+
+#include <stdint.h>
+
+#include <type_traits>
+#include <utility>
+
+#include <hip/hip_runtime.h>
+
+namespace hg {
+
+int cu_count();   // compute units of the current device (hg_fast.hip)
+
+namespace lin {
+
+// Activations, numbered as in the public headers.
+enum { kNone = 0, kRelu = 1, kGelu = 2, kGeluTanh = 3, kSilu = 4 };
+// How a matrix is stored next to the 16-bit and fp32 forms.
+enum { kSaveNone = 0, kSave16 = 1, kSave8 = 2 };
+
+constexpr int kBlock8 = 32;       // columns that share a scale in an 8-bit checkpoint
+
+// What is done with a finished fp32 sum of products: bias, save, activation,
+// residual, store.  Every pointer but C may be null.
+struct Finish {
+    void *C;                      // rows×cols row-major, fp32 (out32) or 16 bits
+    const void *R;                // residual, same type as C; may be C itself
+    const float *bias;            // cols values
+    void *Z;                      // pre-activation: 16 bits (kSave16) or codes (kSave8)
+    uint8_t *Zs;                  // kSave8: scale bytes, rows × ceil(cols / 32)
+    int64_t ldc, ldr, ldz, ldzs;
+    int32_t rows, cols;
+    int32_t act, save;
+    int32_t out32;
+    int32_t cvec, rvec, zvec;     // 16-byte accesses allowed (8-byte for codes)
+};
+
+// One product: C[rows×cols] = Σ_k A(i, k)·B(j, k).  An operand is stored
+// either k-contiguous (A[i·lda + k]) or, TA / TB, k-major (A[k·lda + i]).
+struct Product {
+    const uint16_t *A, *B;        // 16-byte aligned, lda and ldb multiples of 8
+    int64_t lda, ldb;
+    int32_t M, N, K;              // rows, cols, length of the sum
+    int32_t splits, per;          // slices of the sum and their length in 64-wide stages
+    float *P;                     // splits > 1: fp32 partial sums, slice s at P + s·M·ldp
+    int64_t ldp;                  // multiple of 4
+    Finish f;
+};
+
+enum class Layout { NN, NT, TT };   // (TA, TB) = (0, 0), (0, 1), (1, 1)
+
+hipError_t launch_ring(const Product &p, Layout l, int tile, bool bf16, hipStream_t s);
+hipError_t launch_reduce(const Product &p, bool bf16, hipStream_t s);
+
+// D (rows×ldd, ldd a multiple of 8) = S (rows×cols) with zeros behind the
+// last column, 16-bit elements.
+hipError_t launch_pad(const void *S, int64_t lds, void *D, int64_t ldd, int64_t rows, int64_t cols,
+                      hipStream_t s);
+
+// 8-bit checkpoint of X (rows×cols) and back; the read writes zeros behind
+// the last column up to `pad` columns.
+hipError_t launch_write8(const void *X, int64_t ldx, uint8_t *C, int64_t ldc, uint8_t *S, int64_t lds,
+                         int64_t rows, int64_t cols, bool bf16, hipStream_t s);
+hipError_t launch_read8(const uint8_t *C, int64_t ldc, const uint8_t *S, int64_t lds, void *X, int64_t ldx,
+                        int64_t rows, int64_t cols, int64_t pad, bool bf16, hipStream_t s);
+
+// dZ = dY·act'(Z) rounded to 16 bits (D: rows×ldd, ldd a multiple of 8, zeros
+// behind the last column; null: not stored) and the column sums of the
+// unrounded dZ in fp32: one row of partial sums for every strip of `strip`
+// rows at Q + s·cols, or, with one strip, the result itself in db.
+struct Slope {
+    const void *dY;
+    const void *Z;                // 16 bits or codes, by `save`
+    const uint8_t *Zs;
+    void *D;
+    float *Q, *db;
+    int64_t lddy, ldz, ldzs, ldd;
+    int64_t rows, cols, strip;
+    int32_t act, save;
+    int32_t accumulate;           // db is added to
+    int32_t yvec, zvec;           // 16-byte (8-byte for codes) loads allowed
+};
+hipError_t launch_slope(const Slope &p, bool bf16, hipStream_t s);
+hipError_t launch_sum_strips(const float *Q, int64_t strips, int64_t cols, float *db, bool accumulate,
+                             hipStream_t s);
+// rows×cols zeros (fp32 or 16 bits).
+hipError_t launch_zero(void *C, int64_t ldc, int64_t rows, int64_t cols, bool wide, hipStream_t s);
+
+#if defined(__HIPCC__)
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef short shortx4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) shortx4 lds_shortx4;
+typedef __attribute__((address_space(3))) uint32_t lds_u32;
+
+// f(std::integral_constant<int, 0>{}) ... f(std::integral_constant<int, N-1>{}).
+template <class F, int... I>
+__device__ __forceinline__ void static_for_impl(F &&f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F &&f)
+{
+    static_for_impl(f, std::make_integer_sequence<int, N>{});
+}
+
+template <bool BF16>
+__device__ __forceinline__ floatx4 mfma_16x16x32(const half8 &a, const half8 &b, const floatx4 &c)
+{
+    if constexpr (BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// s_waitcnt on one counter only.
+template <int n>
+__device__ __forceinline__ void wait_vmcnt()
+{
+    __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+template <int n>
+__device__ __forceinline__ void wait_lgkmcnt()
+{
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | ((n & 15) << 8));
+}
+
+// Raw buffer resource: base address, no stride, `bytes` in range.
+__device__ __forceinline__ i32x4 buffer_of(uint64_t base, uint32_t bytes)
+{
+    i32x4 r;
+    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)base);
+    r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32));
+    r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
+    r[3] = 0x00020000;
+    return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float widen(uint16_t h)
+{
+    if constexpr (BF16)
+        return __builtin_bit_cast(float, (uint32_t)h << 16);
+    else
+        return (float)__builtin_bit_cast(_Float16, h);
+}
+// Rounded to nearest even.
+template <bool BF16>
+__device__ __forceinline__ uint16_t narrow(float v)
+{
+    if constexpr (BF16)
+        return __builtin_bit_cast(uint16_t, (__bf16)v);
+    else
+        return __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
+// Eight 16-bit elements at p[0 .. n-1] (n <= 8, the others 0); vec: p is
+// 16-byte aligned and n = 8 is one load.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void *p, int n, bool vec, float (&v)[8])
+{
+    const uint16_t *h = static_cast<const uint16_t *>(p);
+    if (vec && n >= 8) {
+        const u32x4 w = *reinterpret_cast<const u32x4 *>(h);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = widen<BF16>((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = e < n ? widen<BF16>(h[e]) : 0.0f;
+    }
+}
+template <bool BF16>
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8])
+{
+    u32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        w[e] = (uint32_t)narrow<BF16>(v[2 * e]) | (uint32_t)narrow<BF16>(v[2 * e + 1]) << 16;
+    return w;
+}
+template <bool BF16>
+__device__ __forceinline__ void store8(void *p, int n, bool vec, const float (&v)[8])
+{
+    uint16_t *h = static_cast<uint16_t *>(p);
+    if (vec && n >= 8) {
+        *reinterpret_cast<u32x4 *>(h) = pack8<BF16>(v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n)
+                h[e] = narrow<BF16>(v[e]);
+    }
+}
+
+// ---- Activations, all in fp32.
+//
+// silu(z) = z·s(z) with the logistic s; gelu_tanh(z) = z·s(2u), u =
+// sqrt(2/pi)·(z + 0.044715 z³), since (1 + tanh u)/2 = s(2u).  gelu(z) =
+// z·Phi(z) with the normal distribution function Phi by Abramowitz and
+// Stegun 7.1.26 (absolute error 1.5e-7; the factor exp(-z²/2) it uses is the
+// density that the slope needs).  Where a factor of z is exactly 0 the
+// product is 0 (its limit) also for z = ±inf; NaN passes through.
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+__device__ __forceinline__ float logistic(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x)); }
+__device__ __forceinline__ float times(float z, float w) { return w == 0.0f ? 0.0f : z * w; }
+
+// Phi(z) and the density phi(z).
+__device__ __forceinline__ void normal_cdf(float z, float &cdf, float &pdf)
+{
+    const float x = __builtin_fabsf(z) * 0.70710678f;
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
+    float q = 1.061405429f;
+    q = __builtin_fmaf(q, t, -1.453152027f);
+    q = __builtin_fmaf(q, t, 1.421413741f);
+    q = __builtin_fmaf(q, t, -0.284496736f);
+    q = __builtin_fmaf(q, t, 0.254829592f);
+    const float g = exp_fast(-x * x);
+    const float tail = 0.5f * q * t * g;          // 1 - Phi(|z|)
+    cdf = z < 0.0f ? tail : 1.0f - tail;
+    pdf = 0.39894228f * g;
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z)
+{
+    if constexpr (ACT == kRelu) {
+        return z < 0.0f ? 0.0f : z;
+    } else if constexpr (ACT == kGelu) {
+        float cdf, pdf;
+        normal_cdf(z, cdf, pdf);
+        return times(z, cdf);
+    } else if constexpr (ACT == kGeluTanh) {
+        return times(z, logistic(1.59576912f * __builtin_fmaf(0.044715f * z, z * z, z)));
+    } else if constexpr (ACT == kSilu) {
+        return times(z, logistic(z));
+    } else {
+        return z;
+    }
+}
+
+// dy·act'(z).
+template <int ACT>
+__device__ __forceinline__ float slope(float dy, float z)
+{
+    if constexpr (ACT == kRelu) {
+        return z > 0.0f ? dy : (z <= 0.0f ? 0.0f : z);
+    } else if constexpr (ACT == kGelu) {
+        float cdf, pdf;
+        normal_cdf(z, cdf, pdf);
+        return dy * (cdf + times(z, pdf));
+    } else if constexpr (ACT == kGeluTanh) {
+        const float z2 = z * z;
+        const float s = logistic(1.59576912f * __builtin_fmaf(0.044715f * z, z2, z));
+        return dy * (s + times(z * __builtin_fmaf(0.21406964f, z2, 1.59576912f), s * (1.0f - s)));
+    } else if constexpr (ACT == kSilu) {
+        const float s = logistic(z);
+        return dy * (s + times(z, s * (1.0f - s)));
+    } else {
+        return dy;
+    }
+}
+
+// f(std::integral_constant<int, act>{}), act uniform.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F &&f)
+{
+    switch (act) {
+    case kRelu: f(std::integral_constant<int, kRelu>{}); break;
+    case kGelu: f(std::integral_constant<int, kGelu>{}); break;
+    case kGeluTanh: f(std::integral_constant<int, kGeluTanh>{}); break;
+    case kSilu: f(std::integral_constant<int, kSilu>{}); break;
+    default: f(std::integral_constant<int, kNone>{}); break;
+    }
+}
+
+// ---- 8-bit checkpoints.  A block of 32 columns shares the scale 2^e, e the
+// smallest exponent with amax <= 448·2^e over the block's finite elements
+// (448 is e4m3's largest value), so no element saturates.  A power of two
+// makes x·2^-e exact: the only rounding is the one to e4m3.  e is kept where
+// every code stands for a normal value of the element type (bf16: e >= -117)
+// or an exact one (fp16: -15 <= e <= 8); at the largest e (8, bf16: 120) codes
+// stop at 240, because 256·2^e is past the type's range.
+template <bool BF16>
+__device__ __forceinline__ int scale_exponent(float amax)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, amax);
+    const int e = (int)(b >> 23) - 135 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return BF16 ? max(e, -117) : min(max(e, -15), 8);
+}
+__device__ __forceinline__ float finite_abs(float v)
+{
+    const float a = __builtin_fabsf(v);
+    return a < __builtin_inff() ? a : 0.0f;
+}
+// The codes of eight values that share the exponent e (inf and NaN: NaN).
+template <bool BF16>
+__device__ __forceinline__ u32x2 codes8(const float (&v)[8], int e)
+{
+    const float inv = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
+    const float lim = e == (BF16 ? 120 : 8) ? 240.0f : 448.0f;
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = __builtin_fminf(__builtin_fmaxf(v[i] * inv, -lim), lim);
+        s[i] = __builtin_fabsf(v[i]) < __builtin_inff() ? x : __builtin_nanf("");
+    }
+    u32x2 w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int c = __builtin_amdgcn_cvt_pk_fp8_f32(s[4 * i], s[4 * i + 1], 0, false);
+        w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(s[4 * i + 2], s[4 * i + 3], c, true);
+    }
+    return w;
+}
+// 2^(byte - 127); byte 0 stands for 2^-127 and 255 for NaN.
+__device__ __forceinline__ float scale_of(uint32_t byte)
+{
+    const uint32_t b = byte == 0 ? 0x00400000u : byte == 255 ? 0x7fc00000u : byte << 23;
+    return __builtin_bit_cast(float, b);
+}
+__device__ __forceinline__ void values8(u32x2 w, float scale, float (&v)[8])
+{
+    typedef float floatx2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const floatx2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
+        const floatx2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
+        v[4 * i] = lo[0] * scale;
+        v[4 * i + 1] = lo[1] * scale;
+        v[4 * i + 2] = hi[0] * scale;
+        v[4 * i + 3] = hi[1] * scale;
+    }
+}
+__device__ __forceinline__ u32x2 load_codes(const uint8_t *p, int n, bool vec)
+{
+    if (vec && n >= 8)
+        return *reinterpret_cast<const u32x2 *>(p);
+    u32x2 w = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < n)
+            w[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
+    return w;
+}
+__device__ __forceinline__ void store_codes(uint8_t *p, int n, bool vec, u32x2 w)
+{
+    if (vec && n >= 8) {
+        *reinterpret_cast<u32x2 *>(p) = w;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < n)
+            p[e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+}
+// The largest of four neighbouring lanes' values (lanes 4i .. 4i + 3).
+__device__ __forceinline__ float max_of_4(float v)
+{
+    v = __builtin_fmaxf(v, __shfl_xor(v, 1));
+    return __builtin_fmaxf(v, __shfl_xor(v, 2));
+}
+
+// Finishes eight consecutive columns col .. col + 7 (col a multiple of 8) of
+// one row, `b` their biases.  Called by whole waves in which lanes 4i .. 4i + 3
+// hold the four eighths of one block of 32 columns (an 8-bit save takes their
+// largest); lanes past the last row or column store nothing.
+template <bool BF16>
+__device__ __forceinline__ void finish8(const Finish &f, int row, int col, float (&v)[8], const float (&b)[8])
+{
+    const bool in = row < f.rows;
+    const int n = in ? f.cols - col : 0;          // columns of this lane (may pass 8)
+    if (f.bias) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] += b[e];
+    }
+    if (f.save == kSave16) {
+        if (n > 0)
+            store8<BF16>(static_cast<uint16_t *>(f.Z) + (int64_t)row * f.ldz + col, n, f.zvec, v);
+    } else if (f.save == kSave8) {
+        float a = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            a = __builtin_fmaxf(a, e < n ? finite_abs(v[e]) : 0.0f);
+        const int x = scale_exponent<BF16>(max_of_4(a));
+        if (n > 0) {
+            store_codes(static_cast<uint8_t *>(f.Z) + (int64_t)row * f.ldz + col, n, f.zvec, codes8<BF16>(v, x));
+            if (col % kBlock8 == 0)
+                f.Zs[(int64_t)row * f.ldzs + col / kBlock8] = (uint8_t)(x + 127);
+        }
+    }
+    if (n <= 0)
+        return;
+    with_act(f.act, [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = activate<decltype(a)::value>(v[e]);
+    });
+    if (f.out32) {
+        float *c = static_cast<float *>(f.C) + (int64_t)row * f.ldc + col;
+        const float *r = static_cast<const float *>(f.R) + (int64_t)row * f.ldr + col;
+        if (f.R) {
+            if (f.rvec && n >= 8) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const floatx4 w = *reinterpret_cast<const floatx4 *>(r + 4 * h);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[4 * h + e] += w[e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < n)
+                        v[e] += r[e];
+            }
+        }
+        if (f.cvec && n >= 8) {
+            *reinterpret_cast<floatx4 *>(c) = floatx4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<floatx4 *>(c + 4) = floatx4{v[4], v[5], v[6], v[7]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n)
+                    c[e] = v[e];
+        }
+    } else {
+        if (f.R) {
+            float r[8];
+            load8<BF16>(static_cast<const uint16_t *>(f.R) + (int64_t)row * f.ldr + col, n, f.rvec, r);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] += r[e];
+        }
+        store8<BF16>(static_cast<uint16_t *>(f.C) + (int64_t)row * f.ldc + col, n, f.cvec, v);
+    }
+}
+
+// The biases of columns col .. col + 7 (0 past the last).
+__device__ __forceinline__ void load_bias(const Finish &f, int col, float (&b)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        b[e] = f.bias && col + e < f.cols ? f.bias[col + e] : 0.0f;
+}
+
+// ---- Wave-private staging of a 16×W block of sums (fp32) in LDS, from the
+// matrix cores' layout (a lane holds columns 16j + 4·(lane div 16) .. +3 of
+// row lane mod 16) to eight consecutive columns per lane.  The 16-byte piece
+// index is XORed with the row so that neither side has bank conflicts.
+template <int W>
+__device__ __forceinline__ int stage_at(int row, int piece)
+{
+    constexpr int PIECES = W / 4;                            // per row
+    const int x = W >= 64 ? row & 15 : (row >> 1) & 7;
+    return (row * PIECES + (piece ^ (x & (PIECES - 1)))) * 16;
+}
+template <int W>
+__device__ __forceinline__ void stage_put(unsigned char *s, int lane, const floatx4 (&acc)[W / 16])
+{
+    const int frow = lane & 15, fhi = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < W / 16; ++j)
+        *reinterpret_cast<floatx4 *>(s + stage_at<W>(frow, 4 * j + fhi)) = acc[j];
+}
+template <int W>
+__device__ __forceinline__ void stage_get(const unsigned char *s, int row, int unit, float (&v)[8])
+{
+    const floatx4 lo = *reinterpret_cast<const floatx4 *>(s + stage_at<W>(row, 2 * unit));
+    const floatx4 hi = *reinterpret_cast<const floatx4 *>(s + stage_at<W>(row, 2 * unit + 1));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[e] = lo[e];
+        v[4 + e] = hi[e];
+    }
+}
+
+// Finishes (or, with partial sums, stores as fp32) the staged 16×W block
+// whose first row and column are r0 and c0, `slice` of the sum.
+template <int W, bool BF16>
+__device__ __forceinline__ void drain(const Product &p, const unsigned char *s, int lane, int r0, int c0, int slice,
+                                      const float (&b)[8])
+{
+    constexpr int UNITS = W / 8, ROWS = 64 / UNITS;         // lanes per row, rows per pass
+    const int unit = lane % UNITS, col = c0 + 8 * unit;
+#pragma clang loop unroll(disable)
+    for (int r = lane / UNITS; r < 16; r += ROWS) {
+        float v[8];
+        stage_get<W>(s, r, unit, v);
+        const int row = r0 + r;
+        if (p.splits > 1) {
+            if (row < p.M && col < p.N) {
+                float *d = p.P + ((int64_t)slice * p.M + row) * p.ldp + col;
+                *reinterpret_cast<floatx4 *>(d) = floatx4{v[0], v[1], v[2], v[3]};
+                if (col + 4 < p.ldp)
+                    *reinterpret_cast<floatx4 *>(d + 4) = floatx4{v[4], v[5], v[6], v[7]};
+            }
+        } else {
+            finish8<BF16>(p.f, row, col, v, b);
+        }
+    }
+}
+
+#endif  // __HIPCC__
+
+}  // namespace lin
+}  // namespace hg

@@ -1,0 +1,289 @@
+"""Python binding of include/hgemm_linear.h: the linear layer, its gradient
+and the 8-bit checkpoints between the two.  Argument marshalling only, as in
+the package's other functions; re-exported by the package.
+
+A matrix is a 2-D device tensor with unit stride along its last axis and rows
+that do not overlap.  An 8-bit checkpoint is the pair (codes, scales) of
+checkpoint8_empty: codes (M, N) uint8 or float8_e4m3fn, scales
+(M, ceil(N / 32)) uint8.  All tensors of a call are on one device; the work is
+queued on that device's current stream, and tensors that another stream made
+or will reuse are the caller's to order, as with the package's other calls.
+"""
+import ctypes
+
+import torch
+
+from . import HG_BF16, HG_F16, HG_F32, HgError, _stream_handle, lib
+
+HG_E4M3 = 3
+E4M3_BLOCK = 32
+ACT_GELU = 2
+ACT_GELU_TANH = 3
+ACT_SILU = 4
+
+EXPORTS_LINEAR = ("hg_linear", "hg_linear_workspace_size", "hg_linear_grad", "hg_linear_grad_workspace_size",
+                  "hg_checkpoint8_write", "hg_checkpoint8_read")
+
+
+class Matrix(ctypes.Structure):
+    """struct hg_matrix."""
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("lds", ctypes.c_int64), ("type", ctypes.c_int32)]
+
+
+_i64, _vp, _int, _mp = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(Matrix)
+lib.hg_linear.argtypes = [_int, _i64, _i64, _i64, _mp, _mp, _vp, _mp, _mp, _mp, _vp, _i64, _vp]
+lib.hg_linear.restype = _int
+lib.hg_linear_workspace_size.argtypes = [_i64, _i64, _i64, _mp, _mp]
+lib.hg_linear_workspace_size.restype = _i64
+lib.hg_linear_grad.argtypes = [_int, _i64, _i64, _i64, _mp, _mp, _mp, _mp, _mp, _mp, _vp, _int, _vp, _i64, _vp]
+lib.hg_linear_grad.restype = _int
+lib.hg_linear_grad_workspace_size.argtypes = [_i64, _i64, _i64, _mp, _mp, _mp]
+lib.hg_linear_grad_workspace_size.restype = _i64
+lib.hg_checkpoint8_write.argtypes = [_i64, _i64, _mp, _mp, _vp]
+lib.hg_checkpoint8_write.restype = _int
+lib.hg_checkpoint8_read.argtypes = [_i64, _i64, _mp, _mp, _vp]
+lib.hg_checkpoint8_read.restype = _int
+
+_TYPE = {torch.float16: HG_F16, torch.bfloat16: HG_BF16, torch.float32: HG_F32}
+_HALF = (torch.float16, torch.bfloat16)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _lead(t, name, dtypes):
+    """The leading dimension of a valid matrix; raises for anything else."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    (rows, cols), (ld, unit) = t.shape, t.stride()
+    if rows and cols > 1 and unit != 1:
+        raise ValueError(f"{name} needs unit stride along its last axis")
+    if rows > 1 and cols and ld < cols:
+        raise ValueError(f"{name}'s rows overlap (row stride {ld}, {cols} columns)")
+    return ld if rows > 1 and cols else max(1, cols)
+
+
+def _matrix(t, name, dtypes):
+    ld = _lead(t, name, dtypes)
+    return Matrix(t.data_ptr() or None, ld, None, 0, _TYPE[t.dtype])
+
+
+def _pair(pair, name):
+    if not (isinstance(pair, (tuple, list)) and len(pair) == 2):
+        raise TypeError(f"{name} must be a tensor or a pair (codes, scales)")
+    codes, scales = pair
+    ld, lds = _lead(codes, name + "'s codes", _CODES), _lead(scales, name + "'s scales", (torch.uint8,))
+    want = (codes.shape[0], -(-codes.shape[1] // E4M3_BLOCK))
+    if tuple(scales.shape) != want:
+        raise ValueError(f"{name}'s scales {tuple(scales.shape)} do not match codes {tuple(codes.shape)}: "
+                         f"expected {want}")
+    return Matrix(codes.data_ptr() or None, ld, scales.data_ptr() or None, lds, HG_E4M3)
+
+
+def _saved(m, name, dtype):
+    """(matrix, shape, its tensors) of a 16-bit tensor or an 8-bit checkpoint."""
+    if isinstance(m, torch.Tensor):
+        return _matrix(m, name, (dtype,)), m.shape, (m,)
+    d = _pair(m, name)
+    return d, m[0].shape, tuple(m)
+
+
+def _vector(v, name, n):
+    if not (isinstance(v, torch.Tensor) and v.is_cuda and v.dtype == torch.float32 and v.dim() == 1
+            and v.shape[0] == n and v.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous float32 device vector of length {n}")
+    return v.data_ptr() or None
+
+
+def _work(work, need, like):
+    if work is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
+    if not (isinstance(work, torch.Tensor) and work.is_cuda and work.is_contiguous()):
+        raise ValueError("work must be a contiguous device tensor")
+    return work
+
+
+def _call(fn, name, like, others, *args):
+    """fn(*args, the current stream of `like`'s device), with that device current."""
+    dev = like.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, _stream_handle(like))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream_handle(like))
+    if st != 0:
+        raise HgError(name, st)
+
+
+def _size(fn, name, like, *args):
+    if torch.cuda.current_device() == like.get_device():
+        need = fn(*args)
+    else:
+        with torch.cuda.device(like.get_device()):
+            need = fn(*args)
+    if need < 0:
+        raise HgError(name, int(need))
+    return int(need)
+
+
+def _linear_shapes(X, W):
+    x, w = _matrix(X, "X", _HALF), _matrix(W, "W", (X.dtype,))
+    (M, K), N = X.shape, W.shape[0]
+    if W.shape[1] != K:
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}")
+    return x, w, M, N, K
+
+
+def linear_workspace_size(X, W) -> int:
+    """Bytes of workspace linear needs for these operands (hg_linear_workspace_size)."""
+    x, w, M, N, K = _linear_shapes(X, W)
+    return _size(lib.hg_linear_workspace_size, "hg_linear_workspace_size", X, M, N, K, x, w)
+
+
+def linear_workspace(X, W):
+    """A workspace for linear calls on these operands (None if they need none)."""
+    return _work(None, linear_workspace_size(X, W), X)
+
+
+def linear(X, W, Y, bias=None, act: int = 0, residual=None, Z=None, work=None):
+    """Y = act(X·Wᵀ + bias) + residual on the current stream; returns Y.
+
+    X (M, K) and W (N, K) float16 or bfloat16, Y (M, N) of their type or
+    float32, bias a float32 vector of length N, residual (M, N) of Y's type
+    (Y itself: in place).  The pre-activation X·Wᵀ + bias is saved in Z, an
+    (M, N) tensor of X's type or an 8-bit checkpoint (codes, scales).  `work`:
+    device tensor of at least linear_workspace_size(X, W) bytes (allocated with
+    torch when None and needed)."""
+    x, w, M, N, K = _linear_shapes(X, W)
+    y = _matrix(Y, "Y", (X.dtype, torch.float32))
+    if tuple(Y.shape) != (M, N):
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}, Y {tuple(Y.shape)}")
+    r = z = b = None
+    zt = ()
+    if bias is not None:
+        b = _vector(bias, "bias", N)
+    if residual is not None:
+        r = _matrix(residual, "residual", (Y.dtype,))
+        if residual.shape != Y.shape:
+            raise ValueError(f"residual {tuple(residual.shape)} does not match Y {tuple(Y.shape)}")
+    if Z is not None:
+        z, shape, zt = _saved(Z, "Z", X.dtype)
+        if tuple(shape) != (M, N):
+            raise ValueError(f"Z {tuple(shape)} does not match Y {tuple(Y.shape)}")
+    if work is None:
+        work = _work(None, _size(lib.hg_linear_workspace_size, "hg_linear_workspace_size", X, M, N, K, x, w), X)
+    else:
+        work = _work(work, 0, X)
+    wptr, wbytes = (work.data_ptr(), work.numel() * work.element_size()) if work is not None else (None, 0)
+    _call(lib.hg_linear, "hg_linear", X, (W, Y, bias, residual, work) + zt,
+          int(act), M, N, K, x, w, b, r, y, z, wptr, wbytes)
+    return Y
+
+
+def _grad_shapes(dY, W, X):
+    dy = _matrix(dY, "dY", _HALF)
+    w = x = None
+    xt = ()
+    M, N = dY.shape
+    K = None
+    if W is not None:
+        w = _matrix(W, "W", (dY.dtype,))
+        K = W.shape[1]
+        if W.shape[0] != N:
+            raise ValueError(f"shape mismatch: dY {tuple(dY.shape)}, W {tuple(W.shape)}")
+    if X is not None:
+        x, shape, xt = _saved(X, "X", dY.dtype)
+        if shape[0] != M or K not in (None, shape[1]):
+            raise ValueError(f"shape mismatch: dY {tuple(dY.shape)}, X {tuple(shape)}"
+                             + (f", W {tuple(W.shape)}" if W is not None else ""))
+        K = shape[1]
+    return dy, w, x, xt, M, N, K or 0
+
+
+def linear_grad_workspace_size(dY, W, X) -> int:
+    """Bytes of workspace linear_grad needs for these operands
+    (hg_linear_grad_workspace_size); W or X None: without dX or dW."""
+    dy, w, x, _, M, N, K = _grad_shapes(dY, W, X)
+    return _size(lib.hg_linear_grad_workspace_size, "hg_linear_grad_workspace_size", dY, M, N, K, dy, w, x)
+
+
+def linear_grad_workspace(dY, W, X):
+    """A workspace for linear_grad calls on these operands."""
+    return _work(None, linear_grad_workspace_size(dY, W, X), dY)
+
+
+def linear_grad(dY, W, X, Z=None, act: int = 0, dX=None, dW=None, dbias=None, accumulate: bool = False, work=None):
+    """The gradients of linear on the current stream: dz = dY·act'(Z), dX =
+    dz·W, dW = dzᵀ·X, dbias = the column sums of dz; returns (dX, dW, dbias).
+
+    dY (M, N) float16 or bfloat16, W (N, K) of its type, X (M, K) and Z (M, N)
+    of its type or 8-bit checkpoints (codes, scales).  Only the gradients that
+    are given are computed: dX (M, K) of dY's type, dW (N, K) of dY's type or
+    float32, dbias float32 of length N.  W may be None without dX, X without
+    dW, Z with ACT_NONE.  `accumulate`: dW and dbias are added to.  `work`:
+    device tensor of at least linear_grad_workspace_size(dY, W, X) bytes
+    (allocated with torch when None)."""
+    dy, w, x, xt, M, N, K = _grad_shapes(dY, W, X)
+    z = gx = gw = gb = None
+    zt = ()
+    if dX is not None:
+        if W is None:
+            raise ValueError("dX needs W")
+        gx = _matrix(dX, "dX", (dY.dtype,))
+        if tuple(dX.shape) != (M, K):
+            raise ValueError(f"dX {tuple(dX.shape)} does not match {(M, K)}")
+    if dW is not None:
+        if X is None:
+            raise ValueError("dW needs X")
+        gw = _matrix(dW, "dW", (dY.dtype, torch.float32))
+        if tuple(dW.shape) != (N, K):
+            raise ValueError(f"dW {tuple(dW.shape)} does not match {(N, K)}")
+    if dbias is not None:
+        gb = _vector(dbias, "dbias", N)
+    if Z is not None:
+        z, shape, zt = _saved(Z, "Z", dY.dtype)
+        if tuple(shape) != (M, N):
+            raise ValueError(f"Z {tuple(shape)} does not match dY {tuple(dY.shape)}")
+    elif act != 0:
+        raise ValueError("the activation's gradient needs Z")
+    if work is None:
+        work = _work(None, _size(lib.hg_linear_grad_workspace_size, "hg_linear_grad_workspace_size", dY, M, N, K, dy,
+                                 w, x), dY)
+    else:
+        work = _work(work, 0, dY)
+    wptr, wbytes = (work.data_ptr(), work.numel() * work.element_size()) if work is not None else (None, 0)
+    _call(lib.hg_linear_grad, "hg_linear_grad", dY, (W, dX, dW, dbias, work) + xt + zt,
+          int(act), M, N, K, dy, w, x, z, gx, gw, gb, 1 if accumulate else 0, wptr, wbytes)
+    return dX, dW, dbias
+
+
+def checkpoint8_empty(M: int, N: int, device="cuda"):
+    """Room for the 8-bit checkpoint of an (M, N) matrix: (codes, scales)."""
+    return (torch.empty((M, N), dtype=torch.uint8, device=device),
+            torch.empty((M, -(-N // E4M3_BLOCK)), dtype=torch.uint8, device=device))
+
+
+def checkpoint8_write(X, codes, scales):
+    """X (float16 or bfloat16) as an 8-bit checkpoint; returns (codes, scales)."""
+    x, c = _matrix(X, "X", _HALF), _pair((codes, scales), "the checkpoint")
+    if codes.shape != X.shape:
+        raise ValueError(f"codes {tuple(codes.shape)} do not match X {tuple(X.shape)}")
+    _call(lib.hg_checkpoint8_write, "hg_checkpoint8_write", X, (codes, scales), *X.shape, x, c)
+    return codes, scales
+
+
+def checkpoint8_read(codes, scales, X):
+    """The values of an 8-bit checkpoint, written to X (float16 or bfloat16); returns X."""
+    x, c = _matrix(X, "X", _HALF), _pair((codes, scales), "the checkpoint")
+    if codes.shape != X.shape:
+        raise ValueError(f"codes {tuple(codes.shape)} do not match X {tuple(X.shape)}")
+    _call(lib.hg_checkpoint8_read, "hg_checkpoint8_read", X, (codes, scales), *X.shape, c, x)
+    return X
