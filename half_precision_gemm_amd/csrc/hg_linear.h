@@ -135,6 +135,27 @@ __device__ __forceinline__ void wait_lgkmcnt()
     __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | ((n & 15) << 8));
 }
 
+// Half a fragment of a k-major operand: 16 lanes read a 4 (k) × 16 (rows)
+// block, lane l of them the 8 bytes at p (row k = l div 4, columns 4·(l mod
+// 4) ..), and get the four k of row l.  The parameter's __restrict__ is what
+// keeps the compiler from waiting for every buffer→LDS load in flight before
+// this read, as it does where it knows nothing about the address; the ring's
+// own waits and barriers order the two.
+__device__ __forceinline__ shortx4 read_tr16(const lds_shortx4 *__restrict__ p)
+{
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(const_cast<lds_shortx4 *>(p));
+}
+__device__ __forceinline__ half8 read_tr(const unsigned char *lo, const unsigned char *hi)
+{
+    union {
+        shortx4 h[2];
+        half8 v;
+    } u;
+    u.h[0] = read_tr16((const lds_shortx4 *)lo);
+    u.h[1] = read_tr16((const lds_shortx4 *)hi);
+    return u.v;
+}
+
 // Raw buffer resource: base address, no stride, `bytes` in range.
 __device__ __forceinline__ i32x4 buffer_of(uint64_t base, uint32_t bytes)
 {

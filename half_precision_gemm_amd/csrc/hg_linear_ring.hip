@@ -174,14 +174,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ring_kernel(const Product p
             const int row = 32 * s + 8 * fhi + (frow >> 2);
             const int c = (w * WT + blk * 16) / 8 + ((lane >> 1) & 1);
             const unsigned char *q = slot + row * S::RB + ((c ^ S::swz(row)) * 16) + (lane & 1) * 8;
-            union {
-                shortx4 h[2];
-                half8 v;
-            } u;
-            u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4 *)(uintptr_t)(uint32_t)(uintptr_t)q);
-            u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_shortx4 *)(uintptr_t)(uint32_t)(uintptr_t)(q + 4 * S::RB));
-            return u.v;
+            return read_tr(q, q + 4 * S::RB);
         }
     };
     struct TagA {
