@@ -52,7 +52,8 @@ struct Product {
 
 enum class Layout { NN, NT, TT };   // (TA, TB) = (0, 0), (0, 1), (1, 1)
 
-hipError_t launch_ring(const Product &p, Layout l, int tile, bool bf16, hipStream_t s);
+hipError_t launch_ring(const Product &p, Layout l, int tile, bool bf16, hipStream_t s);    // 64 or 128
+hipError_t launch_tile(const Product &p, Layout l, bool bf16, hipStream_t s);              // 256
 hipError_t launch_reduce(const Product &p, bool bf16, hipStream_t s);
 
 // D (rows×ldd, ldd a multiple of 8) = S (rows×cols) with zeros behind the
@@ -165,6 +166,131 @@ __device__ __forceinline__ i32x4 buffer_of(uint64_t base, uint32_t bytes)
     r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
     r[3] = 0x00020000;
     return r;
+}
+
+// ---- The operands of the tiled product kernels: EDGE rows of A or B in
+// 64-wide stages of the sum, through LDS slots filled by direct buffer→LDS
+// loads of 1 KiB per wave instruction (four waves).
+//
+//  * k-contiguous: an LDS row holds one row's 64 k (128 bytes).  A
+//    matrix-core fragment (lane l: row l mod 16 of a 16-row block, k =
+//    8·(l div 16) .. +7 of a 32-wide step) is one 16-byte read.
+//  * k-major: an LDS row holds one k's EDGE elements; a fragment is two
+//    transposing 8-byte reads.  Both forms give a lane the same k, so either
+//    pairs with either.
+//  * The 16-byte chunks of an LDS row are XOR-swizzled so that the reads are
+//    free of bank conflicts (64 banks of 4 bytes; measured 0 of both forms);
+//    a load realises the swizzle by which chunk each lane fetches.
+//  * Rows and columns past the edge get an offset past the buffer's range, and
+//    stages past the end of the sum an empty range: both load zeros.  A
+//    k-contiguous operand whose K is no multiple of 64 checks every chunk's k
+//    (KCHK), because the bytes behind a row are another row's.
+constexpr int kStage = 64;                          // k per stage
+constexpr uint32_t kOutside = 0x80000000u;          // an offset past every range
+
+template <int EDGE, bool KMAJOR>
+struct Side {
+    static constexpr int RB = KMAJOR ? EDGE * 2 : kStage * 2;     // bytes of an LDS row
+    static constexpr int CH = RB / 16;                            // its 16-byte chunks
+    static constexpr int RPI = 1024 / RB;                         // LDS rows per load instruction
+    static constexpr int L = EDGE / 32;                           // load instructions per wave
+    static constexpr int BYTES = EDGE * kStage * 2;               // of a slot
+    // What the chunk index of LDS row r is XORed with.  k-contiguous: 16 rows
+    // are read at one chunk, two rows to a 256-byte line of banks.  k-major: a
+    // half wave reads the rows r, r+1, r+2, r+3 and the same + 8, 32 bytes
+    // each: pairs of chunks are moved so that they fall on distinct banks.
+    static __device__ __forceinline__ int swz(int r)
+    {
+        if constexpr (!KMAJOR)
+            return (r >> 1) & 7;
+        else if constexpr (EDGE >= 128)
+            return ((r & 3) | ((r >> 1) & 4)) << 1;
+        else
+            return (((r >> 1) & 1) | ((r >> 2) & 2)) << 1;
+    }
+};
+
+// The fragment of k-step s (32 wide) and the 16 rows from `row0` on.
+template <int EDGE, bool KMAJOR>
+__device__ __forceinline__ half8 fragment(const unsigned char *slot, int lane, int row0, int s)
+{
+    using S = Side<EDGE, KMAJOR>;
+    const int frow = lane & 15, fhi = lane >> 4;
+    if constexpr (!KMAJOR) {
+        const unsigned char *q = slot + (row0 + frow) * S::RB;
+        return *reinterpret_cast<const half8 *>(q + (((4 * s + fhi) ^ S::swz(frow)) * 16));
+    } else {
+        const int k = 8 * fhi + (frow >> 2);                      // + 32s and + 4 leave swz() alone
+        const int c = row0 / 8 + ((lane >> 1) & 1);
+        const unsigned char *q = slot + (32 * s + k) * S::RB + ((c ^ S::swz(k)) * 16) + (lane & 1) * 8;
+        return read_tr(q, q + 4 * S::RB);
+    }
+}
+
+// One tile's rows of an operand, as one lane loads them.
+template <int EDGE, bool KMAJOR, bool KCHK>
+struct Panel {
+    using S = Side<EDGE, KMAJOR>;
+    uint64_t base;                  // of the slice's first stage
+    uint32_t step, range, row;      // bytes: per stage; in range at the first stage; per row
+    int left;                       // k from the slice's first stage to the end of the sum
+    uint32_t off[S::L];             // this lane's chunk of each load
+
+    // p, ld: the operand; rows first .. of `edge` in all; the sum has K terms,
+    // the slice begins at stage kt0.
+    __device__ __forceinline__ void set(const uint16_t *p, int64_t ld, int first, int count, int K, int kt0, int wave,
+                                        int lane)
+    {
+        const int edge = min(count - first, EDGE), k0 = kt0 * kStage;
+        const int64_t at = KMAJOR ? (int64_t)k0 * ld + first : (int64_t)first * ld + k0;
+        base = reinterpret_cast<uint64_t>(p) + (uint64_t)at * 2;
+        row = (uint32_t)ld * 2;
+        left = K - k0;
+        step = KMAJOR ? kStage * row : kStage * 2;
+        range = KMAJOR ? (uint32_t)((edge + 7) & ~7) * 2 : (uint32_t)(edge - 1) * row + (uint32_t)((left + 7) & ~7) * 2;
+#pragma unroll
+        for (int i = 0; i < S::L; ++i) {
+            const int r = (wave * S::L + i) * S::RPI + lane / S::CH;
+            const int c = (lane % S::CH) ^ S::swz(r);
+            off[i] = (KMAJOR ? c * 8 < edge : r < edge) ? (uint32_t)r * row + c * 16 : kOutside;
+        }
+    }
+    // Load i of the slice's stage kt (an empty range unless `in`) into `slot`
+    // (an LDS address).
+    template <class LOAD>
+    __device__ __forceinline__ void issue(LOAD load, int kt, bool in, uint32_t slot, int i, int wave, int lane) const
+    {
+        uint32_t o = off[i], bytes;
+        if constexpr (KMAJOR) {
+            bytes = range + (uint32_t)(min(left - kt * kStage, kStage) - 1) * row;
+        } else {
+            bytes = range - (uint32_t)kt * (kStage * 2);
+            if constexpr (KCHK) {
+                const int r = (wave * S::L + i) * S::RPI + lane / S::CH;
+                o = ((lane % S::CH) ^ S::swz(r)) * 8 < left - kt * kStage ? o : kOutside;
+            }
+        }
+        const i32x4 r = buffer_of(base + (uint64_t)kt * step, in ? bytes : 0);
+        load(r, reinterpret_cast<lds_u32 *>((uintptr_t)(slot + (wave * S::L + i) * 1024)), (int)o);
+    }
+};
+
+// Workgroup or work item → (slice, tile row, tile column): ids regrouped per
+// XCD (consecutive ids run on different XCDs, each with its own L2), then
+// bands of 4 tile rows walked column by column, so that tiles on one XCD share
+// panels in its L2.
+__device__ __forceinline__ void place(int id, int total, int tiles_m, int tiles_n, int &slice, int &tm, int &tn)
+{
+    const int per = total >> 3, rem = total & 7, x = id & 7;
+    const int q = x * per + min(x, rem) + (id >> 3);
+    const int tiles = tiles_m * tiles_n;
+    slice = q / tiles;
+    const int l = q - slice * tiles;
+    const int band = l / (4 * tiles_n), first = band * 4;
+    const int gsz = min(tiles_m - first, 4);
+    const int r = l - band * 4 * tiles_n;
+    tm = first + r % gsz;
+    tn = r / gsz;
 }
 
 template <bool BF16>
@@ -475,6 +601,15 @@ __device__ __forceinline__ void load_bias(const Finish &f, int col, float (&b)[8
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         b[e] = f.bias && col + e < f.cols ? f.bias[col + e] : 0.0f;
+}
+
+// Waits for the biases here: otherwise the compiler waits for them inside the
+// epilogue's loop, and with them for every store of the passes before.
+__device__ __forceinline__ void settle(float (&b)[8])
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        __asm__ volatile("" : "+v"(b[e]));
 }
 
 // ---- Wave-private staging of a 16×W block of sums (fp32) in LDS, from the

@@ -106,10 +106,10 @@ struct Cut {
 };
 Cut cut_of(int64_t M, int64_t N, int64_t K)
 {
-    const int64_t t128 = ((M + 127) / 128) * ((N + 127) / 128), t64 = ((M + 63) / 64) * ((N + 63) / 64);
+    auto tiles_of = [&](int64_t edge) { return ((M + edge - 1) / edge) * ((N + edge - 1) / edge); };
     Cut c;
-    c.tile = t128 >= 128 ? 128 : 64;
-    const int64_t tiles = std::max<int64_t>(1, c.tile == 128 ? t128 : t64), stages = (K + kBK - 1) / kBK;
+    c.tile = tiles_of(256) >= hg::cu_count() ? 256 : tiles_of(128) >= 128 ? 128 : 64;
+    const int64_t tiles = std::max<int64_t>(1, tiles_of(c.tile)), stages = (K + kBK - 1) / kBK;
     int64_t s = 1;
     if (tiles < hg::cu_count())
         s = std::min<int64_t>({hg::cu_count() / tiles, stages / 8, (int64_t)32});
@@ -133,7 +133,8 @@ hipError_t run_product(lin::Product &p, const Cut &c, lin::Layout layout, bool b
         p.splits = 0;
         return lin::launch_reduce(p, bf16, s);
     }
-    const hipError_t e = lin::launch_ring(p, layout, c.tile, bf16, s);
+    const hipError_t e =
+        c.tile == 256 ? lin::launch_tile(p, layout, bf16, s) : lin::launch_ring(p, layout, c.tile, bf16, s);
     return e != hipSuccess || p.splits <= 1 ? e : lin::launch_reduce(p, bf16, s);
 }
 

@@ -11,19 +11,9 @@
 //    stages through a ring of LDS slots filled by direct buffer→LDS loads, all
 //    but one of them in flight: with tiles this small a stage is a few hundred
 //    cycles of matrix work, and memory latency is what bounds them.
-//  * A k-contiguous operand's slot holds one 128-byte row per tile row, and a
-//    matrix-core fragment (8 consecutive k of one row) is one 16-byte read.  A
-//    k-major operand's slot holds one row of BM (or BN) elements per k; a
-//    fragment is two transposing 8-byte reads (ds_read_b64_tr_b16), each of
-//    which hands 16 lanes a 4 (k) × 16 (rows) block with the four k of a row
-//    in one lane.  Neither form moves data through registers on its way in,
-//    and nothing is transposed in memory.
-//  * 16-byte chunks are XOR-swizzled within the slot's rows so that the reads
-//    are free of bank conflicts; the loads realise the swizzle by which chunk
-//    each lane fetches.
-//  * Rows, columns and k past the edges load as zeros by the buffer's range
-//    check; a k-contiguous operand whose K is no multiple of 64 is checked
-//    chunk by chunk (KCHK), because the bytes behind a row are another row's.
+//  * No operand is transposed in memory, and none moves through registers on
+//    its way into LDS (hg_linear.h: the slots' layout, the swizzle, the
+//    transposing reads, the edges).
 //  * The sum may be cut into slices (p.splits) for products with few tiles and
 //    a long sum: each slice stores fp32 partial sums, which a second launch
 //    adds in order, so the result does not depend on scheduling.
@@ -37,48 +27,7 @@ namespace hg {
 namespace lin {
 namespace {
 
-constexpr int BK = 64, NWAVES = 4, THREADS = 256;
-constexpr uint32_t OOB = 0x80000000u;          // an offset past every range
-
-// One operand's slot of one stage, EDGE tile rows.
-template <int EDGE, bool KMAJOR>
-struct Side {
-    static constexpr int RB = KMAJOR ? EDGE * 2 : BK * 2;         // bytes of an LDS row
-    static constexpr int CH = RB / 16;                            // its 16-byte chunks
-    static constexpr int RPI = 1024 / RB;                         // LDS rows per load instruction
-    static constexpr int L = EDGE / (8 * NWAVES);                 // load instructions per wave
-    static constexpr int BYTES = EDGE * BK * 2;
-    // What the chunk index of LDS row r is XORed with.  k-contiguous: 16 rows
-    // are read at one chunk, two rows to a 256-byte line of banks.  k-major: a
-    // half wave reads the rows r, r+1, r+2, r+3 and the same + 8, 32 bytes
-    // each: pairs of chunks are moved so that they fall on distinct banks.
-    static __device__ __forceinline__ int swz(int r)
-    {
-        if constexpr (!KMAJOR)
-            return (r >> 1) & 7;
-        else if constexpr (EDGE >= 128)
-            return ((r & 3) | ((r >> 1) & 4)) << 1;
-        else
-            return (((r >> 1) & 1) | ((r >> 2) & 2)) << 1;
-    }
-};
-
-// Workgroup id → (slice, tile row, tile column): ids regrouped per XCD
-// (consecutive ids run on different XCDs), then bands of 4 tile rows walked
-// column by column, so that tiles on one XCD share panels in its L2.
-__device__ __forceinline__ void place(int wg, int total, int tiles_m, int tiles_n, int &slice, int &tm, int &tn)
-{
-    const int per = total >> 3, rem = total & 7, x = wg & 7;
-    const int q = x * per + min(x, rem) + (wg >> 3);
-    const int tiles = tiles_m * tiles_n;
-    slice = q / tiles;
-    const int l = q - slice * tiles;
-    const int band = l / (4 * tiles_n), first = band * 4;
-    const int gsz = min(tiles_m - first, 4);
-    const int r = l - band * 4 * tiles_n;
-    tm = first + r % gsz;
-    tn = r / gsz;
-}
+constexpr int BK = kStage, NWAVES = 4, THREADS = 256;
 
 template <int EDGE, bool TA, bool TB, bool KCHK, bool BF16>
 __global__ void __launch_bounds__(THREADS, 1) linear_ring_kernel(const Product p, int tiles_m, int tiles_n, int total)
@@ -102,47 +51,19 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ring_kernel(const Product p
     const int nk = min((K + BK - 1) / BK - kt0, p.per);
     const uint32_t lds_base = (uint32_t)reinterpret_cast<uintptr_t>(smem);
 
-    // Load i of a wave fills 1 KiB of its operand's slot: LDS rows
-    // (wave·L + i)·RPI .., lane l the chunk at position l.
-    uint32_t off[L];
-    int kchunk[L];
-    auto chunk = [&](int i, int ch, int rpi, int l0) { return (l0 + i) * rpi + lane / ch; };
-#pragma unroll
-    for (int i = 0; i < L; ++i) {
-        const bool isb = i >= LA;
-        const int ch = isb ? SB::CH : SA::CH, rpi = isb ? SB::RPI : SA::RPI;
-        const int row = chunk(isb ? i - LA : i, ch, rpi, wave * (isb ? SB::L : LA));
-        const int c = (lane % ch) ^ (isb ? SB::swz(row) : SA::swz(row));
-        const int64_t ld = isb ? p.ldb : p.lda;
-        const int edge = isb ? p.N - n0 : p.M - m0;
-        const bool ok = (isb ? TB : TA) ? c * 8 < edge : row < edge;
-        off[i] = ok ? (uint32_t)(row * (int)ld * 2 + c * 16) : OOB;
-        kchunk[i] = c * 8;
-    }
+    Panel<EDGE, TA, KCHK> pa;
+    Panel<EDGE, TB, KCHK> pb;
+    pa.set(p.A, p.lda, m0, p.M, K, kt0, wave, lane);
+    pb.set(p.B, p.ldb, n0, p.N, K, kt0, wave, lane);
+    auto load = [](i32x4 r, lds_u32 *dst, int o) __attribute__((always_inline)) {
+        hg_lin_ring_load_lds(r, dst, 16, o, 0, 0, 0);
+    };
     auto issue_one = [&](int kt, int i) __attribute__((always_inline)) {
-        const bool isb = i >= LA, km = isb ? TB : TA;
-        const uint16_t *base = isb ? p.B : p.A;
-        const int64_t ld = isb ? p.ldb : p.lda;
-        const int first = isb ? n0 : m0, edge = min((isb ? p.N : p.M) - first, EDGE);
-        const int k = (kt0 + kt) * BK;
-        uint32_t o = off[i];
-        uint64_t a;
-        uint32_t bytes;
-        if (km) {
-            // rows k .. k+63 of a k-major operand, at most K of them
-            a = reinterpret_cast<uint64_t>(base) + ((uint64_t)k * (uint64_t)ld + (uint64_t)first) * 2;
-            bytes = (uint32_t)(((min(K - k, BK) - 1) * (int)ld + ((edge + 7) & ~7)) * 2);
-        } else {
-            a = reinterpret_cast<uint64_t>(base) + ((uint64_t)first * (uint64_t)ld + (uint64_t)k) * 2;
-            bytes = (uint32_t)(((edge - 1) * (int)ld + ((K + 7) & ~7) - k) * 2);
-            if constexpr (KCHK)
-                o = kchunk[i] < K - k ? o : OOB;
-        }
-        if (kt >= nk)
-            bytes = 0;
-        const uint32_t dst = lds_base + (kt % NS) * SLOT + (isb ? SA::BYTES : 0) +
-                             (wave * (isb ? SB::L : LA) + (isb ? i - LA : i)) * 1024;
-        hg_lin_ring_load_lds(buffer_of(a, bytes), reinterpret_cast<lds_u32 *>((uintptr_t)dst), 16, (int)o, 0, 0, 0);
+        const uint32_t slot = lds_base + (kt % NS) * SLOT;
+        if (i < LA)
+            pa.issue(load, kt, kt < nk, slot, i, wave, lane);
+        else
+            pb.issue(load, kt, kt < nk, slot + SA::BYTES, i - LA, wave, lane);
     };
     auto issue = [&](int kt) __attribute__((always_inline)) {
 #pragma unroll
@@ -160,29 +81,6 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ring_kernel(const Product p
     for (int s = 0; s < NS - 1; ++s)
         issue(s);
 
-    // Fragment of block `blk` and k-step s: lane l holds row l mod 16 of the
-    // block and k = 32s + 8·(l div 16) .. +7, for both operands and both
-    // storage forms, so the matrix core pairs matching k.
-    const int frow = lane & 15, fhi = lane >> 4;
-    auto frag = [&](auto side, const unsigned char *slot, int w, int s, int blk) -> half8 {
-        using S = typename decltype(side)::type;
-        constexpr bool km = std::is_same<S, Side<EDGE, true>>::value;
-        if constexpr (!km) {
-            const int row = w * WT + blk * 16 + frow;
-            return *reinterpret_cast<const half8 *>(slot + row * S::RB + (((4 * s + fhi) ^ S::swz(row)) * 16));
-        } else {
-            const int row = 32 * s + 8 * fhi + (frow >> 2);
-            const int c = (w * WT + blk * 16) / 8 + ((lane >> 1) & 1);
-            const unsigned char *q = slot + row * S::RB + ((c ^ S::swz(row)) * 16) + (lane & 1) * 8;
-            return read_tr(q, q + 4 * S::RB);
-        }
-    };
-    struct TagA {
-        using type = SA;
-    };
-    struct TagB {
-        using type = SB;
-    };
     constexpr int SPS = BK / 32;
     struct Frags {
         half8 a[SPS][T], b[SPS][T];
@@ -193,9 +91,9 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ring_kernel(const Product p
         constexpr int s = r / (2 * T), q = r % (2 * T);
         const unsigned char *slot = smem + (kt % NS) * SLOT;
         if constexpr (q < T)
-            f.a[s][q] = frag(TagA{}, slot, wm, s, q);
+            f.a[s][q] = fragment<EDGE, TA>(slot, lane, wm * WT + q * 16, s);
         else
-            f.b[s][q - T] = frag(TagB{}, slot + SA::BYTES, wn, s, q - T);
+            f.b[s][q - T] = fragment<EDGE, TB>(slot + SA::BYTES, lane, wn * WT + (q - T) * 16, s);
     };
     auto read_stage = [&](int kt, Frags &f) __attribute__((always_inline)) {
         static_for<NR>([&](auto rc) __attribute__((always_inline)) { read_one(kt, f, rc); });
@@ -249,6 +147,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ring_kernel(const Product p
     const int c0 = n0 + wn * WT;
     float bias[8];
     load_bias(p.f, c0 + 8 * (lane % (WT / 8)), bias);
+    settle(bias);
 #pragma unroll
     for (int i = 0; i < T; ++i) {
         stage_put<WT>(stg, lane, acc[i]);
