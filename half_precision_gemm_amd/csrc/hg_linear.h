@@ -10,6 +10,11 @@
 
 #include <hip/hip_runtime.h>
 
+#if defined(__HIPCC__)
+// v_mul_legacy_f32 (an LLVM intrinsic): a product in which 0 times anything is 0.
+extern "C" __device__ float hg_lin_mul_legacy(float a, float b) __asm("llvm.amdgcn.fmul.legacy");
+#endif
+
 namespace hg {
 
 int cu_count();   // compute units of the current device (hg_fast.hip)
@@ -36,6 +41,7 @@ struct Finish {
     int32_t act, save;
     int32_t out32;
     int32_t cvec, rvec, zvec;     // 16-byte accesses allowed (8-byte for codes)
+    int32_t vec;                  // all of them that are used
 };
 
 // One product: C[rows×cols] = Σ_k A(i, k)·B(j, k).  An operand is stored
@@ -358,10 +364,20 @@ __device__ __forceinline__ void store8(void *p, int n, bool vec, const float (&v
 // z·Phi(z) with the normal distribution function Phi by Abramowitz and
 // Stegun 7.1.26 (absolute error 1.5e-7; the factor exp(-z²/2) it uses is the
 // density that the slope needs).  Where a factor of z is exactly 0 the
-// product is 0 (its limit) also for z = ±inf; NaN passes through.
-__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
-__device__ __forceinline__ float logistic(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x)); }
-__device__ __forceinline__ float times(float z, float w) { return w == 0.0f ? 0.0f : z * w; }
+// product is 0 (its limit) also for z = ±inf, which is what the legacy
+// multiply does (0 times anything is 0); NaN passes through.  An activation is
+// 5 to 15 vector operations and two quarter-rate ones per element, which a
+// 256×256 tile pays for outside its matrix work: the constants are folded.
+constexpr float kLog2e = 1.4426950408889634f;
+// s(x) with x given as -x·log2(e).
+__device__ __forceinline__ float logistic2(float x) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x)); }
+__device__ __forceinline__ float times(float z, float w) { return hg_lin_mul_legacy(z, w); }
+// -2u·log2(e) of gelu_tanh.
+__device__ __forceinline__ float tanh_arg(float z, float z2)
+{
+    constexpr float c = -1.5957691216057308f * kLog2e;      // 2·sqrt(2/pi)
+    return z * __builtin_fmaf(0.044715f * c, z2, c);
+}
 
 // Phi(z) and the density phi(z).
 __device__ __forceinline__ void normal_cdf(float z, float &cdf, float &pdf)
@@ -373,7 +389,7 @@ __device__ __forceinline__ void normal_cdf(float z, float &cdf, float &pdf)
     q = __builtin_fmaf(q, t, 1.421413741f);
     q = __builtin_fmaf(q, t, -0.284496736f);
     q = __builtin_fmaf(q, t, 0.254829592f);
-    const float g = exp_fast(-x * x);
+    const float g = __builtin_amdgcn_exp2f(-0.5f * kLog2e * z * z);
     const float tail = 0.5f * q * t * g;          // 1 - Phi(|z|)
     cdf = z < 0.0f ? tail : 1.0f - tail;
     pdf = 0.39894228f * g;
@@ -389,9 +405,9 @@ __device__ __forceinline__ float activate(float z)
         normal_cdf(z, cdf, pdf);
         return times(z, cdf);
     } else if constexpr (ACT == kGeluTanh) {
-        return times(z, logistic(1.59576912f * __builtin_fmaf(0.044715f * z, z * z, z)));
+        return times(z, logistic2(tanh_arg(z, z * z)));
     } else if constexpr (ACT == kSilu) {
-        return times(z, logistic(z));
+        return times(z, logistic2(-kLog2e * z));
     } else {
         return z;
     }
@@ -409,10 +425,10 @@ __device__ __forceinline__ float slope(float dy, float z)
         return dy * (cdf + times(z, pdf));
     } else if constexpr (ACT == kGeluTanh) {
         const float z2 = z * z;
-        const float s = logistic(1.59576912f * __builtin_fmaf(0.044715f * z, z2, z));
+        const float s = logistic2(tanh_arg(z, z2));
         return dy * (s + times(z * __builtin_fmaf(0.21406964f, z2, 1.59576912f), s * (1.0f - s)));
     } else if constexpr (ACT == kSilu) {
-        const float s = logistic(z);
+        const float s = logistic2(-kLog2e * z);
         return dy * (s + times(z, s * (1.0f - s)));
     } else {
         return dy;
@@ -515,8 +531,10 @@ __device__ __forceinline__ void store_codes(uint8_t *p, int n, bool vec, u32x2 w
 // The largest of four neighbouring lanes' values (lanes 4i .. 4i + 3).
 __device__ __forceinline__ float max_of_4(float v)
 {
-    v = __builtin_fmaxf(v, __shfl_xor(v, 1));
-    return __builtin_fmaxf(v, __shfl_xor(v, 2));
+    const int a = __builtin_bit_cast(int, v);
+    v = __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(a, 0xb1, 0xf, 0xf, true)));   // 1 0 3 2
+    const int b = __builtin_bit_cast(int, v);
+    return __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(b, 0x4e, 0xf, 0xf, true)));  // 2 3 0 1
 }
 
 // Finishes eight consecutive columns col .. col + 7 (col a multiple of 8) of
@@ -643,31 +661,155 @@ __device__ __forceinline__ void stage_get(const unsigned char *s, int row, int u
     }
 }
 
-// Finishes (or, with partial sums, stores as fp32) the staged 16×W block
-// whose first row and column are r0 and c0, `slice` of the sum.
+// Finishes (or, with partial sums, stores as fp32) staged 16×W blocks of one
+// wave, one after the other down the tile: `slice` of the sum, columns c0 ..,
+// rows `row0` .. in steps of 16.
+//
+// A block inside the matrix with aligned rows takes its passes together: the
+// reads from LDS, the activation's chains and the stores of PASSES rows per
+// lane overlap, and what depends on the call (save, activation, type) is
+// decided once per block, not per row.  The residual of the next block is
+// requested before this block's stores, because the counter of vector memory
+// operations retires in order: a load issued after them would wait for them.
 template <int W, bool BF16>
-__device__ __forceinline__ void drain(const Product &p, const unsigned char *s, int lane, int r0, int c0, int slice,
-                                      const float (&b)[8])
-{
-    constexpr int UNITS = W / 8, ROWS = 64 / UNITS;         // lanes per row, rows per pass
-    const int unit = lane % UNITS, col = c0 + 8 * unit;
-#pragma clang loop unroll(disable)
-    for (int r = lane / UNITS; r < 16; r += ROWS) {
-        float v[8];
-        stage_get<W>(s, r, unit, v);
-        const int row = r0 + r;
-        if (p.splits > 1) {
-            if (row < p.M && col < p.N) {
-                float *d = p.P + ((int64_t)slice * p.M + row) * p.ldp + col;
-                *reinterpret_cast<floatx4 *>(d) = floatx4{v[0], v[1], v[2], v[3]};
-                if (col + 4 < p.ldp)
-                    *reinterpret_cast<floatx4 *>(d + 4) = floatx4{v[4], v[5], v[6], v[7]};
-            }
-        } else {
-            finish8<BF16>(p.f, row, col, v, b);
+struct Drain {
+    static constexpr int UNITS = W / 8, ROWS = 64 / UNITS;      // lanes per row, rows per pass
+    static constexpr int PASSES = 16 / ROWS;
+    const Product &p;
+    const unsigned char *stg;
+    int lane, slice, c0;
+    float bias[8];
+    u32x4 ahead[PASSES][2];                                     // residual of the next block
+
+    __device__ __forceinline__ Drain(const Product &p_, const unsigned char *stg_, int lane_, int slice_, int c0_)
+        : p(p_), stg(stg_), lane(lane_), slice(slice_), c0(c0_)
+    {
+        load_bias(p.f, c0 + 8 * (lane % UNITS), bias);
+    }
+    __device__ __forceinline__ bool inside(int row0) const
+    {
+        return row0 + 16 <= p.M && c0 + W <= p.N && p.f.vec;
+    }
+    // Requests the residual of the block at row0.
+    __device__ __forceinline__ void request(int row0)
+    {
+        const Finish &f = p.f;
+        if (!f.R || p.splits > 1 || !inside(row0))
+            return;
+        const int64_t at = (int64_t)(row0 + lane / UNITS) * f.ldr + c0 + 8 * (lane % UNITS);
+        const char *r = static_cast<const char *>(f.R) + at * (f.out32 ? 4 : 2);
+        const int64_t step = ROWS * f.ldr * (f.out32 ? 4 : 2);
+#pragma unroll
+        for (int t = 0; t < PASSES; ++t, r += step) {
+            ahead[t][0] = *reinterpret_cast<const u32x4 *>(r);
+            if (f.out32)
+                ahead[t][1] = *reinterpret_cast<const u32x4 *>(r + 16);
         }
     }
-}
+    __device__ __forceinline__ void block(int row0, bool last)
+    {
+        if (inside(row0))
+            whole(row0, last);
+        else
+            edge(row0);
+    }
+    __device__ __forceinline__ void whole(int row0, bool last)
+    {
+        const Finish &f = p.f;
+        const int unit = lane % UNITS, r0 = lane / UNITS, col = c0 + 8 * unit;
+        float v[PASSES][8];
+#pragma unroll
+        for (int t = 0; t < PASSES; ++t)
+            stage_get<W>(stg, r0 + ROWS * t, unit, v[t]);
+        const int64_t row = row0 + r0;
+        if (p.splits > 1) {
+            float *d = p.P + ((int64_t)slice * p.M + row) * p.ldp + col;
+#pragma unroll
+            for (int t = 0; t < PASSES; ++t, d += ROWS * p.ldp) {
+                *reinterpret_cast<floatx4 *>(d) = floatx4{v[t][0], v[t][1], v[t][2], v[t][3]};
+                *reinterpret_cast<floatx4 *>(d + 4) = floatx4{v[t][4], v[t][5], v[t][6], v[t][7]};
+            }
+            return;
+        }
+        if (f.bias) {
+#pragma unroll
+            for (int t = 0; t < PASSES; ++t)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[t][e] += bias[e];
+        }
+        if (f.save == kSave16) {
+            uint16_t *z = static_cast<uint16_t *>(f.Z) + row * f.ldz + col;
+#pragma unroll
+            for (int t = 0; t < PASSES; ++t, z += ROWS * f.ldz)
+                *reinterpret_cast<u32x4 *>(z) = pack8<BF16>(v[t]);
+        } else if (f.save == kSave8) {
+            uint8_t *z = static_cast<uint8_t *>(f.Z) + row * f.ldz + col, *zs = f.Zs + row * f.ldzs + col / kBlock8;
+#pragma unroll
+            for (int t = 0; t < PASSES; ++t, z += ROWS * f.ldz, zs += ROWS * f.ldzs) {
+                float a = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    a = __builtin_fmaxf(a, finite_abs(v[t][e]));
+                const int x = scale_exponent<BF16>(max_of_4(a));
+                *reinterpret_cast<u32x2 *>(z) = codes8<BF16>(v[t], x);
+                if (unit % 4 == 0)
+                    *zs = (uint8_t)(x + 127);
+            }
+        }
+        with_act(f.act, [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+            for (int t = 0; t < PASSES; ++t)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[t][e] = activate<decltype(a)::value>(v[t][e]);
+        });
+        if (f.R) {
+#pragma unroll
+            for (int t = 0; t < PASSES; ++t)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t w32 = ahead[t][e >> 2][e & 3], w16 = ahead[t][0][e >> 1] >> (16 * (e & 1));
+                    v[t][e] += f.out32 ? __builtin_bit_cast(float, w32) : widen<BF16>((uint16_t)w16);
+                }
+            if (!last)
+                request(row0 + 16);
+        }
+        if (f.out32) {
+            float *c = static_cast<float *>(f.C) + row * f.ldc + col;
+#pragma unroll
+            for (int t = 0; t < PASSES; ++t, c += ROWS * f.ldc) {
+                *reinterpret_cast<floatx4 *>(c) = floatx4{v[t][0], v[t][1], v[t][2], v[t][3]};
+                *reinterpret_cast<floatx4 *>(c + 4) = floatx4{v[t][4], v[t][5], v[t][6], v[t][7]};
+            }
+        } else {
+            uint16_t *c = static_cast<uint16_t *>(f.C) + row * f.ldc + col;
+#pragma unroll
+            for (int t = 0; t < PASSES; ++t, c += ROWS * f.ldc)
+                *reinterpret_cast<u32x4 *>(c) = pack8<BF16>(v[t]);
+        }
+    }
+    __device__ __forceinline__ void edge(int row0)
+    {
+        const int unit = lane % UNITS, col = c0 + 8 * unit;
+#pragma clang loop unroll(disable)
+        for (int r = lane / UNITS; r < 16; r += ROWS) {
+            float v[8];
+            stage_get<W>(stg, r, unit, v);
+            const int row = row0 + r;
+            if (p.splits > 1) {
+                if (row < p.M && col < p.N) {
+                    float *d = p.P + ((int64_t)slice * p.M + row) * p.ldp + col;
+                    *reinterpret_cast<floatx4 *>(d) = floatx4{v[0], v[1], v[2], v[3]};
+                    if (col + 4 < p.ldp)
+                        *reinterpret_cast<floatx4 *>(d + 4) = floatx4{v[4], v[5], v[6], v[7]};
+                }
+            } else {
+                finish8<BF16>(p.f, row, col, v, bias);
+            }
+        }
+    }
+};
 
 #endif  // __HIPCC__
 

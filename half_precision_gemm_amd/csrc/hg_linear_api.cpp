@@ -129,6 +129,7 @@ hipError_t run_product(lin::Product &p, const Cut &c, lin::Layout layout, bool b
     p.per = c.per;
     p.P = static_cast<float *>(partials);
     p.ldp = ((int64_t)p.N + 3) / 4 * 4;
+    p.f.vec = p.f.cvec && (p.f.R == nullptr || p.f.rvec) && (p.f.Z == nullptr || p.f.zvec);
     if (p.K == 0) {                              // an empty sum
         p.splits = 0;
         return lin::launch_reduce(p, bf16, s);

@@ -144,17 +144,17 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ring_kernel(const Product p
     __builtin_amdgcn_s_barrier();
 
     unsigned char *stg = smem + wave * (16 * WT * 4);
-    const int c0 = n0 + wn * WT;
-    float bias[8];
-    load_bias(p.f, c0 + 8 * (lane % (WT / 8)), bias);
-    settle(bias);
+    const int row0 = m0 + wm * WT;
+    Drain<WT, BF16> out(p, stg, lane, slice, n0 + wn * WT);
+    out.request(row0);
+    settle(out.bias);
 #pragma unroll
     for (int i = 0; i < T; ++i) {
         stage_put<WT>(stg, lane, acc[i]);
         // a wave's LDS accesses execute in order; the fences keep the compiler
         // from moving them across
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
-        drain<WT, BF16>(p, stg, lane, m0 + wm * WT + 16 * i, c0, slice, bias);
+        out.block(row0 + 16 * i, i == T - 1);
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
     }
 }

@@ -64,13 +64,20 @@ __device__ __forceinline__ constexpr int sched(int q, int k)
     return k % 8 == 2 ? LD + k / 8 : NONE;
 }
 
-// Keeps a row block of accumulators in accumulation registers up to here: the
-// register allocator would otherwise copy all 256 out as the K loop ends.
-__device__ __forceinline__ void pin(floatx4 (&blk)[T])
+// One row block of accumulators into a wave's staging area (an LDS address),
+// straight from the accumulation registers.  As ordinary stores in a loop over
+// the blocks, the compiler copies accumulators to vector registers ahead of
+// the loop and spills; unrolled, the epilogue's code is there eight times.
+// (The stores' completion is not the compiler's to track: a wave's LDS
+// accesses execute in order, and the reads that follow are waited for.)
+__device__ __forceinline__ void put(const floatx4 (&blk)[T], uint32_t stg, int lane)
 {
 #pragma unroll
     for (int j = 0; j < T; ++j)
-        __asm__ volatile("" : "+a"(blk[j]));
+        __asm__ volatile("ds_write_b128 %0, %1"
+                         :
+                         : "v"(stg + stage_at<WT>(lane & 15, 4 * j + (lane >> 4))), "a"(blk[j])
+                         : "memory");
 }
 
 template <bool TA, bool TB, bool KCHK, bool BF16>
@@ -131,9 +138,9 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
     Tile t;
     find(id, t);
     begin(t);
-    // An interior epilogue issues at least one store for each of its 32
-    // passes after the next tile's 4·L first loads, and the counter retires in
-    // order: with 2·L + 32 operations outstanding stage 0 has landed.
+    // An interior epilogue issues at least one store in each of its 32 passes
+    // after the next tile's 4·L first loads, and the counter retires in order:
+    // with 2·L + 32 operations outstanding stage 0 has landed.
     constexpr int AFTER_FIRST = 2 * L, AFTER_EPILOGUE = 2 * L + 32;
     static_assert(AFTER_EPILOGUE <= 63, "");
     int prev = 0;                      // 0: first tile, 1: after an interior epilogue, 2: after an edge one
@@ -208,10 +215,15 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
 
-        const Tile done = t;
-        const int c0 = done.n0 + wn * WT;
-        float bias[8];
-        load_bias(p.f, c0 + 8 * (lane % (WT / 8)), bias);
+        // the matrix core's last results are in their registers (the stores of
+        // put() are not seen by the compiler's check for that)
+        __asm__ volatile("s_nop 15\n\ts_nop 15");
+
+        const int row0 = t.m0 + wm * WT;
+        const int stg = 2 * SLOT + wave * (16 * WT * 4);
+        prev = t.m0 + EDGE <= p.M && t.n0 + EDGE <= p.N ? 1 : 2;
+        Drain<WT, BF16> out(p, smem + stg, lane, t.slice, t.n0 + wn * WT);
+        out.request(row0);
         __builtin_amdgcn_sched_barrier(0);
         id += gridDim.x;
         const bool more = id < total;
@@ -220,19 +232,18 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
             begin(t);
         }
         __builtin_amdgcn_sched_barrier(0);
-        settle(bias);
-        prev = done.m0 + EDGE <= p.M && done.n0 + EDGE <= p.N ? 1 : 2;
-        unsigned char *stg = smem + 2 * SLOT + wave * (16 * WT * 4);
-        static_for<T>([&](auto ic) __attribute__((always_inline)) {
-            constexpr int i = decltype(ic)::value;
-            pin(acc[i]);
-            stage_put<WT>(stg, lane, acc[i]);
-            // a wave's LDS accesses execute in order; the fences keep the
-            // compiler from moving them across
+        settle(out.bias);
+#pragma clang loop unroll(disable)
+        for (int i = 0; i < T; ++i) {
+            static_for<T>([&](auto ic) __attribute__((always_inline)) {
+                constexpr int b = decltype(ic)::value;
+                if (i == b)
+                    put(acc[b], lds_base + stg, lane);
+            });
             __atomic_signal_fence(__ATOMIC_SEQ_CST);
-            drain<WT, BF16>(p, stg, lane, done.m0 + wm * WT + 16 * i, c0, done.slice, bias);
+            out.block(row0 + 16 * i, i == T - 1);
             __atomic_signal_fence(__ATOMIC_SEQ_CST);
-        });
+        }
         if (!more)
             break;
     }
