@@ -47,7 +47,7 @@ struct Finish {
 // One product: C[rows×cols] = Σ_k A(i, k)·B(j, k).  An operand is stored
 // either k-contiguous (A[i·lda + k]) or, TA / TB, k-major (A[k·lda + i]).
 struct Product {
-    const uint16_t *A, *B;        // 16-byte aligned, lda and ldb multiples of 8
+    const uint16_t *A, *B;        // 16-byte aligned, lda and ldb multiples of 8 (not so row-wise)
     int64_t lda, ldb;
     int32_t M, N, K;              // rows, cols, length of the sum
     int32_t splits, per;          // slices of the sum and their length in 64-wide stages
@@ -56,10 +56,13 @@ struct Product {
     Finish f;
 };
 
+constexpr int kFewRows = 64;      // rows that the row-wise product takes
+
 enum class Layout { NN, NT, TT };   // (TA, TB) = (0, 0), (0, 1), (1, 1)
 
 hipError_t launch_ring(const Product &p, Layout l, int tile, bool bf16, hipStream_t s);    // 64 or 128
 hipError_t launch_tile(const Product &p, Layout l, bool bf16, hipStream_t s);              // 256
+hipError_t launch_rowwise(const Product &p, bool bf16, hipStream_t s);                     // M <= kFewRows; NN
 hipError_t launch_reduce(const Product &p, bool bf16, hipStream_t s);
 
 // D (rows×ldd, ldd a multiple of 8) = S (rows×cols) with zeros behind the

@@ -99,7 +99,8 @@ struct Arena {
     }
 };
 
-// How a product is cut: the tile edge and the slices of its sum.
+// How a product is cut: the tile edge (0: the row-wise product) and the
+// slices of its sum.
 struct Cut {
     int tile;
     int splits, per;
@@ -134,6 +135,8 @@ hipError_t run_product(lin::Product &p, const Cut &c, lin::Layout layout, bool b
         p.splits = 0;
         return lin::launch_reduce(p, bf16, s);
     }
+    if (c.tile == 0)
+        return lin::launch_rowwise(p, bf16, s);
     const hipError_t e =
         c.tile == 256 ? lin::launch_tile(p, layout, bf16, s) : lin::launch_ring(p, layout, c.tile, bf16, s);
     return e != hipSuccess || p.splits <= 1 ? e : lin::launch_reduce(p, bf16, s);
@@ -162,16 +165,31 @@ int check_sizes(int64_t M, int64_t N, int64_t K, int first)
 
 bool bad_work(const void *work, int64_t need) { return need > 0 && (work == nullptr || ((uintptr_t)work & 15) != 0); }
 
+// Whether the forward product goes row by row (one launch, W read once, X once
+// per 16 or 32 rows of W) rather than by 64×64 tiles with the sum in slices (a
+// second launch, X read once per 64).  Up to 16 rows it always wins or comes
+// within 3 us; up to 32 or 64 while X is short.  Measured, row-wise against
+// tiles, bf16, us (N × K): M = 32: 4096×4096 14.7 / 16.5, 1024×1024 5.4 / 9.1,
+// 16384×4096 40.6 / 40.3, 4096×16384 52.9 / 39.7; M = 64: 1024×1024 7.3 / 9.1,
+// 4096×4096 22.3 / 16.5.  Operands that the tiles would have to copy first
+// (N·K·4 bytes more) go row by row up to 64.
+bool few_rows(int64_t M, int64_t K, bool direct)
+{
+    return M <= 16 || (M <= 32 && K <= 4096) || (M <= lin::kFewRows && (K <= 1024 || !direct));
+}
+
 struct LinearPlan {
+    bool few;                                     // the row-wise product
     bool copy_x, copy_w;
     Cut cut;
 };
 LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W)
 {
     LinearPlan q;
-    q.copy_x = !direct(X, K);
-    q.copy_w = !direct(W, K);
-    q.cut = cut_of(M, N, K);
+    q.few = few_rows(M, K, direct(X, K) && direct(W, K));
+    q.copy_x = !q.few && !direct(X, K);
+    q.copy_w = !q.few && !direct(W, K);
+    q.cut = q.few ? Cut{0, 1, 0} : cut_of(M, N, K);
     return q;
 }
 struct LinearRoom {

@@ -45,6 +45,9 @@ lib.hg_checkpoint8_write.restype = _int
 lib.hg_checkpoint8_read.argtypes = [_i64, _i64, _mp, _mp, _vp]
 lib.hg_checkpoint8_read.restype = _int
 
+# torch's getter of the current device without the checks of
+# torch.cuda.current_device() (the tensors at hand are on the GPU already).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _TYPE = {torch.float16: HG_F16, torch.bfloat16: HG_BF16, torch.float32: HG_F32}
 _HALF = (torch.float16, torch.bfloat16)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
@@ -69,6 +72,10 @@ def _lead(t, name, dtypes):
 
 
 def _matrix(t, name, dtypes):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == 2:
+        ld, unit = t.stride()                  # the ordinary case, without the checks that raise
+        if unit == 1 and ld >= t.shape[1] > 0:
+            return Matrix(t.data_ptr(), ld, None, 0, _TYPE[t.dtype])
     ld = _lead(t, name, dtypes)
     return Matrix(t.data_ptr() or None, ld, None, 0, _TYPE[t.dtype])
 
@@ -114,24 +121,27 @@ def _call(fn, name, like, others, *args):
     for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError("all tensors must be on one device")
-    if torch.cuda.current_device() == dev:
-        st = fn(*args, _stream_handle(like))
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, _stream_handle(like))
+    st = _on_device(like, fn, *args, _stream_handle(like))
     if st != 0:
         raise HgError(name, st)
 
 
+def _on_device(like, fn, *args):
+    dev = like.get_device()
+    if _current_device() == dev:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
 def _size(fn, name, like, *args):
-    if torch.cuda.current_device() == like.get_device():
-        need = fn(*args)
-    else:
-        with torch.cuda.device(like.get_device()):
-            need = fn(*args)
+    need = _on_device(like, fn, *args)
     if need < 0:
         raise HgError(name, int(need))
     return int(need)
+
+
+_NO_WORK = -11              # hg_linear: a workspace is needed and there is none
 
 
 def _linear_shapes(X, W):
@@ -178,13 +188,18 @@ def linear(X, W, Y, bias=None, act: int = 0, residual=None, Z=None, work=None):
         z, shape, zt = _saved(Z, "Z", X.dtype)
         if tuple(shape) != (M, N):
             raise ValueError(f"Z {tuple(shape)} does not match Y {tuple(Y.shape)}")
-    if work is None:
-        work = _work(None, _size(lib.hg_linear_workspace_size, "hg_linear_workspace_size", X, M, N, K, x, w), X)
-    else:
-        work = _work(work, 0, X)
-    wptr, wbytes = (work.data_ptr(), work.numel() * work.element_size()) if work is not None else (None, 0)
-    _call(lib.hg_linear, "hg_linear", X, (W, Y, bias, residual, work) + zt,
-          int(act), M, N, K, x, w, b, r, y, z, wptr, wbytes)
+    wptr, wbytes = None, 0
+    if work is not None:
+        wptr, wbytes = _work(work, 0, X).data_ptr(), work.numel() * work.element_size()
+    args = (int(act), M, N, K, x, w, b, r, y, z)
+    others = (W, Y, bias, residual, work) + zt
+    try:
+        _call(lib.hg_linear, "hg_linear", X, others, *args, wptr, wbytes)
+    except HgError as e:
+        if work is not None or e.status != _NO_WORK:
+            raise
+        need = _size(lib.hg_linear_workspace_size, "hg_linear_workspace_size", X, M, N, K, x, w)
+        _call(lib.hg_linear, "hg_linear", X, others, *args, _work(None, need, X).data_ptr(), need)
     return Y
 
 

@@ -55,9 +55,9 @@ BIG = 1 << 20
 @pytest.mark.parametrize("kw,code", [
     (dict(act=-1), -1), (dict(act=5), -1), (dict(M=-1), -2), (dict(M=(1 << 30) + 1), -2), (dict(N=-1), -3),
     (dict(N=BIG + 1), -3), (dict(K=-1), -4), (dict(K=BIG + 1), -4), (dict(X=NULL), -5), (dict(W=NULL), -6),
-    (dict(Y=NULL), -9), (dict(work=None, K=17, X=(P[0], 17), W=(P[1], 17)), -11),
-    (dict(work=P[6] + 8, K=17, X=(P[0], 17), W=(P[1], 17)), -11),
-    (dict(work_bytes=0, K=17, X=(P[0], 17), W=(P[1], 17)), -12),
+    (dict(Y=NULL), -9), (dict(work=None, M=100, K=17, X=(P[0], 17), W=(P[1], 17)), -11),
+    (dict(work=P[6] + 8, M=100, K=17, X=(P[0], 17), W=(P[1], 17)), -11),
+    (dict(work_bytes=0, M=100, K=17, X=(P[0], 17), W=(P[1], 17)), -12),
     (dict(X=(None, 16)), -5), (dict(X=(P[0] + 1, 16)), -5), (dict(X=(P[0], 15)), -5), (dict(X=(P[0], (1 << 30) + 1)), -5),
     (dict(X=(P[0], 16, F32)), -5), (dict(X=(P[0], 16, E4M3)), -5), (dict(W=(P[1], 16, BF16)), -6), (dict(W=(P[1], 8)), -6),
     (dict(bias=P[2] + 2), -7), (dict(R=(P[3], 7)), -8), (dict(R=(P[3], 8, F32)), -8), (dict(Y=(P[4], 7)), -9),
@@ -66,7 +66,7 @@ BIG = 1 << 20
     (dict(Y=(P[0] + 16, 8)), -9), (dict(Y=(P[1], 8)), -9), (dict(Y=(P[2], 8)), -9), (dict(R=(P[4] + 16, 8)), -9),
     (dict(R=(P[4], 16)), -9), (dict(Z=(P[4] + 8, 8)), -10), (dict(Z=(P[0], 8)), -10),
     (dict(Z=(P[5], 8, E4M3, P[5] + 8, 1)), -10), (dict(Z=(P[5], 8, E4M3, P[4], 1)), -10),
-    (dict(K=17, X=(P[0], 17), W=(P[1], 17), work=P[4]), -11), (dict(K=17, X=(P[0], 17), W=(P[1], 17), work=P[0]), -11),
+    (dict(M=100, K=17, X=(P[0], 17), W=(P[1], 17), work=P[4]), -11), (dict(M=100, K=17, X=(P[0], 17), W=(P[1], 17), work=P[0]), -11),
 ])
 def test_linear_refusals(api, kw, code):
     kw = {k: mat(api, *v[:2], *(v[2:3] or (F16,)), *v[3:]) if isinstance(v, tuple) else v for k, v in kw.items()}
