@@ -40,8 +40,6 @@ struct Finish {
     int32_t rows, cols;
     int32_t act, save;
     int32_t out32;
-    int32_t cvec, rvec, zvec;     // 16-byte accesses allowed (8-byte for codes)
-    int32_t vec;                  // all of them that are used
 };
 
 // One product: C[rows×cols] = Σ_k A(i, k)·B(j, k).  An operand is stored
@@ -60,27 +58,41 @@ constexpr int kFewRows = 64;      // rows that the row-wise product takes
 
 enum class Layout { NN, NT, TT };   // (TA, TB) = (0, 0), (0, 1), (1, 1)
 
-hipError_t launch_ring(const Product &p, Layout l, int tile, bool bf16, hipStream_t s);    // 64 or 128
-hipError_t launch_tile(const Product &p, Layout l, bool bf16, hipStream_t s);              // 256
-hipError_t launch_rowwise(const Product &p, bool bf16, hipStream_t s);                     // M <= kFewRows; NN
-hipError_t launch_reduce(const Product &p, bool bf16, hipStream_t s);
+// db = (db +) the strips' sums; strips = 0: nothing to do.
+struct Strips {
+    const float *Q;
+    float *db;
+    int64_t strips, cols;
+    int32_t accumulate;
+};
 
-// D (rows×ldd, ldd a multiple of 8) = S (rows×cols) with zeros behind the
-// last column, 16-bit elements.
-hipError_t launch_pad(const void *S, int64_t lds, void *D, int64_t ldd, int64_t rows, int64_t cols,
-                      hipStream_t s);
+hipError_t launch_ring(const Product &p, int tile, bool bf16, hipStream_t s);               // 64 or 128; NN
+// x (NT) and w (TT), either of them null, and the strips' sums in one launch.
+hipError_t launch_ring_pair(const Product *x, const Product *w, const Strips &b, int tile, bool bf16, hipStream_t s);
+hipError_t launch_tile(const Product &p, Layout l, bool bf16, hipStream_t s);               // 256
+hipError_t launch_rowwise(const Product &p, bool bf16, hipStream_t s);                      // M <= kFewRows; NN
+// The slices' partial sums of one or two products (either may be null).
+hipError_t launch_reduce(const Product *p, const Product *q, bool bf16, hipStream_t s);
 
-// 8-bit checkpoint of X (rows×cols) and back; the read writes zeros behind
-// the last column up to `pad` columns.
+// 8-bit checkpoint of X (rows×cols) and back.
 hipError_t launch_write8(const void *X, int64_t ldx, uint8_t *C, int64_t ldc, uint8_t *S, int64_t lds,
                          int64_t rows, int64_t cols, bool bf16, hipStream_t s);
 hipError_t launch_read8(const uint8_t *C, int64_t ldc, const uint8_t *S, int64_t lds, void *X, int64_t ldx,
-                        int64_t rows, int64_t cols, int64_t pad, bool bf16, hipStream_t s);
+                        int64_t rows, int64_t cols, bool bf16, hipStream_t s);
 
+// A matrix copied to rows of ldd 16-bit elements with zeros behind the last
+// column: 16-bit elements as they are, or the values of an 8-bit checkpoint.
+struct Copy {
+    const void *src;
+    const uint8_t *scales;        // null: 16-bit elements
+    void *dst;
+    int64_t lds, ldss, ldd;
+    int64_t rows, cols;           // rows = 0: nothing to copy
+};
 // dZ = dY·act'(Z) rounded to 16 bits (D: rows×ldd, ldd a multiple of 8, zeros
 // behind the last column; null: not stored) and the column sums of the
 // unrounded dZ in fp32: one row of partial sums for every strip of `strip`
-// rows at Q + s·cols, or, with one strip, the result itself in db.
+// rows at Q + s·cols, or, with Q null, the result itself in db.
 struct Slope {
     const void *dY;
     const void *Z;                // 16 bits or codes, by `save`
@@ -88,14 +100,13 @@ struct Slope {
     void *D;
     float *Q, *db;
     int64_t lddy, ldz, ldzs, ldd;
-    int64_t rows, cols, strip;
+    int64_t rows, cols, strip;    // rows = 0: nothing to do
     int32_t act, save;
     int32_t accumulate;           // db is added to
-    int32_t yvec, zvec;           // 16-byte (8-byte for codes) loads allowed
 };
-hipError_t launch_slope(const Slope &p, bool bf16, hipStream_t s);
-hipError_t launch_sum_strips(const float *Q, int64_t strips, int64_t cols, float *db, bool accumulate,
-                             hipStream_t s);
+// What the gradient's products wait for, in one launch.
+hipError_t launch_prepare(const Slope &g, const Copy &x, const Copy &w, bool bf16, hipStream_t s);
+
 // rows×cols zeros (fp32 or 16 bits).
 hipError_t launch_zero(void *C, int64_t ldc, int64_t rows, int64_t cols, bool wide, hipStream_t s);
 
@@ -108,6 +119,11 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef short shortx4 __attribute__((ext_vector_type(4)));
+// The same at any address that suits the elements: global memory takes wide
+// accesses there, so rows of odd length need no slower path.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef float floatx4_any __attribute__((ext_vector_type(4), aligned(4)));
 typedef __attribute__((address_space(3))) shortx4 lds_shortx4;
 typedef __attribute__((address_space(3))) uint32_t lds_u32;
 
@@ -320,14 +336,13 @@ __device__ __forceinline__ uint16_t narrow(float v)
         return __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
-// Eight 16-bit elements at p[0 .. n-1] (n <= 8, the others 0); vec: p is
-// 16-byte aligned and n = 8 is one load.
+// Eight 16-bit elements at p[0 .. n-1] (the others 0; n may pass 8).
 template <bool BF16>
-__device__ __forceinline__ void load8(const void *p, int n, bool vec, float (&v)[8])
+__device__ __forceinline__ void load8(const void *p, int n, float (&v)[8])
 {
     const uint16_t *h = static_cast<const uint16_t *>(p);
-    if (vec && n >= 8) {
-        const u32x4 w = *reinterpret_cast<const u32x4 *>(h);
+    if (n >= 8) {
+        const u32x4 w = *reinterpret_cast<const u32x4_any *>(h);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             v[e] = widen<BF16>((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
@@ -347,11 +362,11 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8])
     return w;
 }
 template <bool BF16>
-__device__ __forceinline__ void store8(void *p, int n, bool vec, const float (&v)[8])
+__device__ __forceinline__ void store8(void *p, int n, const float (&v)[8])
 {
     uint16_t *h = static_cast<uint16_t *>(p);
-    if (vec && n >= 8) {
-        *reinterpret_cast<u32x4 *>(h) = pack8<BF16>(v);
+    if (n >= 8) {
+        *reinterpret_cast<u32x4_any *>(h) = pack8<BF16>(v);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -509,10 +524,10 @@ __device__ __forceinline__ void values8(u32x2 w, float scale, float (&v)[8])
         v[4 * i + 3] = hi[1] * scale;
     }
 }
-__device__ __forceinline__ u32x2 load_codes(const uint8_t *p, int n, bool vec)
+__device__ __forceinline__ u32x2 load_codes(const uint8_t *p, int n)
 {
-    if (vec && n >= 8)
-        return *reinterpret_cast<const u32x2 *>(p);
+    if (n >= 8)
+        return *reinterpret_cast<const u32x2_any *>(p);
     u32x2 w = {0, 0};
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -520,10 +535,10 @@ __device__ __forceinline__ u32x2 load_codes(const uint8_t *p, int n, bool vec)
             w[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
     return w;
 }
-__device__ __forceinline__ void store_codes(uint8_t *p, int n, bool vec, u32x2 w)
+__device__ __forceinline__ void store_codes(uint8_t *p, int n, u32x2 w)
 {
-    if (vec && n >= 8) {
-        *reinterpret_cast<u32x2 *>(p) = w;
+    if (n >= 8) {
+        *reinterpret_cast<u32x2_any *>(p) = w;
         return;
     }
 #pragma unroll
@@ -556,7 +571,7 @@ __device__ __forceinline__ void finish8(const Finish &f, int row, int col, float
     }
     if (f.save == kSave16) {
         if (n > 0)
-            store8<BF16>(static_cast<uint16_t *>(f.Z) + (int64_t)row * f.ldz + col, n, f.zvec, v);
+            store8<BF16>(static_cast<uint16_t *>(f.Z) + (int64_t)row * f.ldz + col, n, v);
     } else if (f.save == kSave8) {
         float a = 0.0f;
 #pragma unroll
@@ -564,7 +579,7 @@ __device__ __forceinline__ void finish8(const Finish &f, int row, int col, float
             a = __builtin_fmaxf(a, e < n ? finite_abs(v[e]) : 0.0f);
         const int x = scale_exponent<BF16>(max_of_4(a));
         if (n > 0) {
-            store_codes(static_cast<uint8_t *>(f.Z) + (int64_t)row * f.ldz + col, n, f.zvec, codes8<BF16>(v, x));
+            store_codes(static_cast<uint8_t *>(f.Z) + (int64_t)row * f.ldz + col, n, codes8<BF16>(v, x));
             if (col % kBlock8 == 0)
                 f.Zs[(int64_t)row * f.ldzs + col / kBlock8] = (uint8_t)(x + 127);
         }
@@ -580,10 +595,10 @@ __device__ __forceinline__ void finish8(const Finish &f, int row, int col, float
         float *c = static_cast<float *>(f.C) + (int64_t)row * f.ldc + col;
         const float *r = static_cast<const float *>(f.R) + (int64_t)row * f.ldr + col;
         if (f.R) {
-            if (f.rvec && n >= 8) {
+            if (n >= 8) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const floatx4 w = *reinterpret_cast<const floatx4 *>(r + 4 * h);
+                    const floatx4 w = *reinterpret_cast<const floatx4_any *>(r + 4 * h);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         v[4 * h + e] += w[e];
@@ -595,9 +610,9 @@ __device__ __forceinline__ void finish8(const Finish &f, int row, int col, float
                         v[e] += r[e];
             }
         }
-        if (f.cvec && n >= 8) {
-            *reinterpret_cast<floatx4 *>(c) = floatx4{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<floatx4 *>(c + 4) = floatx4{v[4], v[5], v[6], v[7]};
+        if (n >= 8) {
+            *reinterpret_cast<floatx4_any *>(c) = floatx4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<floatx4_any *>(c + 4) = floatx4{v[4], v[5], v[6], v[7]};
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -607,12 +622,12 @@ __device__ __forceinline__ void finish8(const Finish &f, int row, int col, float
     } else {
         if (f.R) {
             float r[8];
-            load8<BF16>(static_cast<const uint16_t *>(f.R) + (int64_t)row * f.ldr + col, n, f.rvec, r);
+            load8<BF16>(static_cast<const uint16_t *>(f.R) + (int64_t)row * f.ldr + col, n, r);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 v[e] += r[e];
         }
-        store8<BF16>(static_cast<uint16_t *>(f.C) + (int64_t)row * f.ldc + col, n, f.cvec, v);
+        store8<BF16>(static_cast<uint16_t *>(f.C) + (int64_t)row * f.ldc + col, n, v);
     }
 }
 
@@ -668,7 +683,7 @@ __device__ __forceinline__ void stage_get(const unsigned char *s, int row, int u
 // wave, one after the other down the tile: `slice` of the sum, columns c0 ..,
 // rows `row0` .. in steps of 16.
 //
-// A block inside the matrix with aligned rows takes its passes together: the
+// A block inside the matrix takes its passes together: the
 // reads from LDS, the activation's chains and the stores of PASSES rows per
 // lane overlap, and what depends on the call (save, activation, type) is
 // decided once per block, not per row.  The residual of the next block is
@@ -691,7 +706,7 @@ struct Drain {
     }
     __device__ __forceinline__ bool inside(int row0) const
     {
-        return row0 + 16 <= p.M && c0 + W <= p.N && p.f.vec;
+        return row0 + 16 <= p.M && c0 + W <= p.N;
     }
     // Requests the residual of the block at row0.
     __device__ __forceinline__ void request(int row0)
@@ -704,9 +719,9 @@ struct Drain {
         const int64_t step = ROWS * f.ldr * (f.out32 ? 4 : 2);
 #pragma unroll
         for (int t = 0; t < PASSES; ++t, r += step) {
-            ahead[t][0] = *reinterpret_cast<const u32x4 *>(r);
+            ahead[t][0] = *reinterpret_cast<const u32x4_any *>(r);
             if (f.out32)
-                ahead[t][1] = *reinterpret_cast<const u32x4 *>(r + 16);
+                ahead[t][1] = *reinterpret_cast<const u32x4_any *>(r + 16);
         }
     }
     __device__ __forceinline__ void block(int row0, bool last)
@@ -745,7 +760,7 @@ struct Drain {
             uint16_t *z = static_cast<uint16_t *>(f.Z) + row * f.ldz + col;
 #pragma unroll
             for (int t = 0; t < PASSES; ++t, z += ROWS * f.ldz)
-                *reinterpret_cast<u32x4 *>(z) = pack8<BF16>(v[t]);
+                *reinterpret_cast<u32x4_any *>(z) = pack8<BF16>(v[t]);
         } else if (f.save == kSave8) {
             uint8_t *z = static_cast<uint8_t *>(f.Z) + row * f.ldz + col, *zs = f.Zs + row * f.ldzs + col / kBlock8;
 #pragma unroll
@@ -755,7 +770,7 @@ struct Drain {
                 for (int e = 0; e < 8; ++e)
                     a = __builtin_fmaxf(a, finite_abs(v[t][e]));
                 const int x = scale_exponent<BF16>(max_of_4(a));
-                *reinterpret_cast<u32x2 *>(z) = codes8<BF16>(v[t], x);
+                *reinterpret_cast<u32x2_any *>(z) = codes8<BF16>(v[t], x);
                 if (unit % 4 == 0)
                     *zs = (uint8_t)(x + 127);
             }
@@ -782,14 +797,14 @@ struct Drain {
             float *c = static_cast<float *>(f.C) + row * f.ldc + col;
 #pragma unroll
             for (int t = 0; t < PASSES; ++t, c += ROWS * f.ldc) {
-                *reinterpret_cast<floatx4 *>(c) = floatx4{v[t][0], v[t][1], v[t][2], v[t][3]};
-                *reinterpret_cast<floatx4 *>(c + 4) = floatx4{v[t][4], v[t][5], v[t][6], v[t][7]};
+                *reinterpret_cast<floatx4_any *>(c) = floatx4{v[t][0], v[t][1], v[t][2], v[t][3]};
+                *reinterpret_cast<floatx4_any *>(c + 4) = floatx4{v[t][4], v[t][5], v[t][6], v[t][7]};
             }
         } else {
             uint16_t *c = static_cast<uint16_t *>(f.C) + row * f.ldc + col;
 #pragma unroll
             for (int t = 0; t < PASSES; ++t, c += ROWS * f.ldc)
-                *reinterpret_cast<u32x4 *>(c) = pack8<BF16>(v[t]);
+                *reinterpret_cast<u32x4_any *>(c) = pack8<BF16>(v[t]);
         }
     }
     __device__ __forceinline__ void edge(int row0)

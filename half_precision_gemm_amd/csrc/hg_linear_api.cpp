@@ -73,11 +73,6 @@ bool valid(const hg_matrix *m, int64_t rows, int64_t cols)
     return true;
 }
 
-bool vec_ok(const void *p, int64_t ld, int64_t each, int64_t bytes)
-{
-    return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0 && ld * each % bytes == 0;
-}
-
 // Whether the product kernels can load this 16-bit operand as it is: 16-byte
 // pieces of rows whose length is a multiple of 8 (a piece never holds
 // elements of the next row or behind the last one), 32-bit offsets in a tile.
@@ -105,41 +100,85 @@ struct Cut {
     int tile;
     int splits, per;
 };
-Cut cut_of(int64_t M, int64_t N, int64_t K)
+
+// The expected time of a product, in us, from what its kernels measured on a
+// 256-CU MI355X (graph replays, bf16; both operands in the last-level cache).
+// A work item (a tile's slice of the sum) takes `fix` + `stage` per 64 of the
+// sum, as many at once as the GPU has room for:
+//
+//    edge   alone on its CUs          GPU full                  items per CU
+//     64    1.0 + 0.265 / stage       3.2 + 0.45 / stage        2
+//    128    5.0 + 0.55                the same                  1
+//    256    7.0 + 1.05                13.0 + 1.4 (power, stores) 1
+//
+// and slices cost a second launch and their partial sums' way through memory:
+// 3 us + bytes at 5 TB/s.  Both sides of the choices this makes, measured (M ×
+// N × K, us): 1000×1000×1000 64×64 tiles 9.0, in two slices 15.4, 128×128 15.3;
+// 128×1024×8192 one slice 33.9, eight 13.8; 2048×4096×4096 128×128 80.3,
+// 256×256 in two slices 72.9; 2000×6000×4000 128×128 125, 256×256 91.8;
+// 512×4096×4096 64×64 28.3, 128×128 in two slices 30.7.
+double cost_us(int64_t M, int64_t N, int64_t K, int tile, int64_t s)
 {
-    auto tiles_of = [&](int64_t edge) { return ((M + edge - 1) / edge) * ((N + edge - 1) / edge); };
+    const int64_t cus = hg::cu_count(), stages = (K + kBK - 1) / kBK;
+    const int64_t items = ((M + tile - 1) / tile) * ((N + tile - 1) / tile) * s;
+    const double fill = std::min(1.0, (double)items / (double)cus);
+    const int64_t slots = tile == 64 && items > cus ? 2 * cus : cus;
+    const double fix = tile == 64 ? (items > cus ? 3.2 : 1.0) : tile == 128 ? 5.0 : 7.0 + 6.0 * fill;
+    const double stage = tile == 64 ? (items > cus ? 0.45 : 0.265) : tile == 128 ? 0.55 : 1.05 + 0.35 * fill;
+    const double rounds = (double)((items + slots - 1) / slots);
+    const double reduce = s > 1 ? 3.0 + (double)s * (double)M * (double)N * 8.0 / 5e6 : 0.0;
+    return 2.0 + rounds * (fix + stage * (double)((stages + s - 1) / s)) + reduce;
+}
+// The best number of slices (at least four stages each) on this tile.
+Cut cut_as(int64_t M, int64_t N, int64_t K, int tile, double *us = nullptr)
+{
+    static const int counts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+    const int64_t stages = (K + kBK - 1) / kBK;
+    int best = 1;
+    double least = cost_us(M, N, K, tile, 1);
+    for (int s : counts) {
+        if (s == 1 || stages < 4 * s)
+            continue;
+        const double c = cost_us(M, N, K, tile, s);
+        if (c < least) {
+            least = c;
+            best = s;
+        }
+    }
+    if (us != nullptr)
+        *us = least;
     Cut c;
-    c.tile = tiles_of(256) >= hg::cu_count() ? 256 : tiles_of(128) >= 128 ? 128 : 64;
-    const int64_t tiles = std::max<int64_t>(1, tiles_of(c.tile)), stages = (K + kBK - 1) / kBK;
-    int64_t s = 1;
-    if (tiles < hg::cu_count())
-        s = std::min<int64_t>({hg::cu_count() / tiles, stages / 8, (int64_t)32});
-    s = std::max<int64_t>(s, 1);
-    c.per = (int)((stages + s - 1) / s);
+    c.tile = tile;
+    c.per = (int)((stages + best - 1) / best);
     c.splits = c.per > 0 ? (int)((stages + c.per - 1) / c.per) : 1;
     return c;
+}
+Cut cut_of(int64_t M, int64_t N, int64_t K, double *us = nullptr)
+{
+    Cut best{};
+    double least = 0.0;
+    for (int tile : {64, 128, 256}) {
+        double c;
+        const Cut cut = cut_as(M, N, K, tile, &c);
+        if (tile == 64 || c < least) {
+            least = c;
+            best = cut;
+        }
+    }
+    if (us != nullptr)
+        *us = least;
+    return best;
 }
 int64_t partial_bytes(const Cut &c, int64_t M, int64_t N)
 {
     return c.splits > 1 ? (int64_t)c.splits * M * ((N + 3) / 4 * 4) * 4 : 0;
 }
-
-hipError_t run_product(lin::Product &p, const Cut &c, lin::Layout layout, bool bf16, void *partials, hipStream_t s)
+void set_cut(lin::Product &p, const Cut &c, void *partials)
 {
     p.splits = c.splits;
     p.per = c.per;
     p.P = static_cast<float *>(partials);
     p.ldp = ((int64_t)p.N + 3) / 4 * 4;
-    p.f.vec = p.f.cvec && (p.f.R == nullptr || p.f.rvec) && (p.f.Z == nullptr || p.f.zvec);
-    if (p.K == 0) {                              // an empty sum
-        p.splits = 0;
-        return lin::launch_reduce(p, bf16, s);
-    }
-    if (c.tile == 0)
-        return lin::launch_rowwise(p, bf16, s);
-    const hipError_t e =
-        c.tile == 256 ? lin::launch_tile(p, layout, bf16, s) : lin::launch_ring(p, layout, c.tile, bf16, s);
-    return e != hipSuccess || p.splits <= 1 ? e : lin::launch_reduce(p, bf16, s);
 }
 
 void set_output(lin::Finish &f, const hg_matrix *Y, int64_t rows, int64_t cols)
@@ -147,7 +186,6 @@ void set_output(lin::Finish &f, const hg_matrix *Y, int64_t rows, int64_t cols)
     f.C = Y->data;
     f.ldc = Y->ld;
     f.out32 = Y->type == HG_F32;
-    f.cvec = vec_ok(Y->data, Y->ld, esize(Y->type), 16);
     f.rows = (int32_t)rows;
     f.cols = (int32_t)cols;
 }
@@ -165,33 +203,53 @@ int check_sizes(int64_t M, int64_t N, int64_t K, int first)
 
 bool bad_work(const void *work, int64_t need) { return need > 0 && (work == nullptr || ((uintptr_t)work & 15) != 0); }
 
-// Whether the forward product goes row by row (one launch, W read once, X once
-// per 16 or 32 rows of W) rather than by 64×64 tiles with the sum in slices (a
-// second launch, X read once per 64).  Up to 16 rows it always wins or comes
-// within 3 us; up to 32 or 64 while X is short.  Measured, row-wise against
-// tiles, bf16, us (N × K): M = 32: 4096×4096 14.7 / 16.5, 1024×1024 5.4 / 9.1,
-// 16384×4096 40.6 / 40.3, 4096×16384 52.9 / 39.7; M = 64: 1024×1024 7.3 / 9.1,
-// 4096×4096 22.3 / 16.5.  Operands that the tiles would have to copy first
-// (N·K·4 bytes more) go row by row up to 64.
-bool few_rows(int64_t M, int64_t K, bool direct)
+// Whether the forward product of M <= kFewRows rows goes row by row: one
+// launch that reads W once, but X once for every 16 rows of W.  Its time is
+// that of the CU with the most rows of W: per 16 rows and element of the sum
+// 1.2 ns, and 0.05 for every row of X (rounded up to 16 from 17 on).  Measured
+// against 64×64 tiles in their best slices, bf16, us (M × N × K): 1×4096×4096
+// 7.3 / 10.9, 16×4096×4096 9.8 / 11.5, 16×1024×1024 4.2 / 6.9, 16×4096×16384
+// 33.6 / 25.5, 16×16384×4096 26.7 / 21.8, 64×4096×4096 22.3 / 12.6.  Those are
+// weights out of the last-level cache; out of HBM, as a model's weights are,
+// tiles take 3 us more and reach 4.6 TB/s (1×512×8192 11.3 / 15.0,
+// 8×4096×16384 35.6 / 37.5, 16×16384×4096 33.8 / 33.4).
+// Operands that the tiles would have to copy first (twice their bytes at 5 TB/s, a
+// launch) count that.
+bool row_by_row(int64_t M, int64_t N, int64_t K, bool copy_x, bool copy_w, double tiles_us)
 {
-    return M <= 16 || (M <= 32 && K <= 4096) || (M <= lin::kFewRows && (K <= 1024 || !direct));
+    if (M > lin::kFewRows)
+        return false;
+    const int64_t blocks = (N + 15) / 16, cus = hg::cu_count();
+    const double rows = M > 16 ? (double)((M + 15) / 16 * 16) : (double)M;
+    const double us = 2.2 + (double)((blocks + cus - 1) / cus) * (double)K * (1.2 + 0.05 * rows) * 1e-3;
+    tiles_us = std::max(tiles_us + 3.0, 4.0 + (double)N * (double)K * 2.0 / 4.6e6);
+    double copies = copy_x || copy_w ? 3.0 : 0.0;
+    copies += (copy_x ? (double)M * (double)K * 4.0 / 5e6 : 0.0) + (copy_w ? (double)N * (double)K * 4.0 / 5e6 : 0.0);
+    return us < tiles_us + copies;
 }
 
 struct LinearPlan {
-    bool few;                                     // the row-wise product
     bool copy_x, copy_w;
     Cut cut;
 };
 LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W)
 {
     LinearPlan q;
-    q.few = few_rows(M, K, direct(X, K) && direct(W, K));
-    q.copy_x = !q.few && !direct(X, K);
-    q.copy_w = !q.few && !direct(W, K);
-    q.cut = q.few ? Cut{0, 1, 0} : cut_of(M, N, K);
+    double us;
+    q.copy_x = !direct(X, K);
+    q.copy_w = !direct(W, K);
+    q.cut = cut_of(M, N, K, &us);
+    if (row_by_row(M, N, K, q.copy_x, q.copy_w, us)) {
+        q.copy_x = q.copy_w = false;
+        q.cut = {0, 1, 0};
+    }
     return q;
 }
+lin::Copy copy_of(const hg_matrix *m, int64_t rows, int64_t cols, void *to)
+{
+    return {m->data, m->type == HG_E4M3 ? m->scales : nullptr, to, m->ld, m->lds, up8(cols), rows, cols};
+}
+
 struct LinearRoom {
     void *x, *w, *p;
 };
@@ -217,15 +275,25 @@ int64_t strip_of(int64_t M, int64_t N)
 }
 
 struct GradRoom {
-    void *dz, *x, *w, *q, *p;
+    void *dz, *x, *w, *q, *px, *pw;
     Cut cx, cw;
     bool copy_w, copy_x;
 };
 GradRoom room_grad(Arena &a, int64_t M, int64_t N, int64_t K, const hg_matrix *W, const hg_matrix *X)
 {
     GradRoom r;
-    r.cx = cut_of(M, K, N);
-    r.cw = cut_of(N, K, M);
+    // Products on smaller tiles than 256×256 share a launch, and so an edge.
+    const Cut none{64, 1, 0};
+    double x64 = 0, x128 = 0, w64 = 0, w128 = 0;
+    r.cx = W != nullptr ? cut_of(M, K, N) : none;
+    r.cw = X != nullptr ? cut_of(N, K, M) : none;
+    if (W != nullptr && X != nullptr && r.cx.tile != 256 && r.cw.tile != 256 && r.cx.tile != r.cw.tile) {
+        const Cut cx64 = cut_as(M, K, N, 64, &x64), cx128 = cut_as(M, K, N, 128, &x128);
+        const Cut cw64 = cut_as(N, K, M, 64, &w64), cw128 = cut_as(N, K, M, 128, &w128);
+        const bool small = x64 + w64 < x128 + w128;
+        r.cx = small ? cx64 : cx128;
+        r.cw = small ? cw64 : cw128;
+    }
     r.copy_w = W != nullptr && !direct(W, K);
     r.copy_x = X != nullptr && (X->type == HG_E4M3 || !direct(X, K));
     const int64_t strips = M > 0 ? (M + strip_of(M, N) - 1) / strip_of(M, N) : 0;
@@ -233,7 +301,8 @@ GradRoom room_grad(Arena &a, int64_t M, int64_t N, int64_t K, const hg_matrix *W
     r.x = a.take(r.copy_x ? M * up8(K) * 2 : 0);
     r.w = a.take(r.copy_w ? N * up8(K) * 2 : 0);
     r.q = a.take(strips > 1 ? strips * N * 4 : 0);
-    r.p = a.take(std::max(W != nullptr ? partial_bytes(r.cx, M, K) : 0, X != nullptr ? partial_bytes(r.cw, N, K) : 0));
+    r.px = a.take(W != nullptr ? partial_bytes(r.cx, M, K) : 0);
+    r.pw = a.take(X != nullptr ? partial_bytes(r.cw, N, K) : 0);
     return r;
 }
 
@@ -312,7 +381,6 @@ int hg_linear(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
     if (R != nullptr) {
         p.f.R = R->data;
         p.f.ldr = R->ld;
-        p.f.rvec = vec_ok(R->data, R->ld, esize(R->type), 16);
     }
     if (Z != nullptr) {
         p.f.Z = Z->data;
@@ -320,21 +388,30 @@ int hg_linear(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
         p.f.save = Z->type == HG_E4M3 ? lin::kSave8 : lin::kSave16;
         p.f.Zs = Z->scales;
         p.f.ldzs = Z->lds;
-        p.f.zvec = Z->type == HG_E4M3 ? vec_ok(Z->data, Z->ld, 1, 8) : vec_ok(Z->data, Z->ld, 2, 16);
     }
-    if (K > 0 && q.copy_x) {
-        if (const hipError_t e = lin::launch_pad(X->data, X->ld, room.x, up8(K), M, K, s))
-            return status_of(e);
+    if (K == 0) {                                 // an empty sum
+        return status_of(lin::launch_reduce(&p, nullptr, bf16, s));
+    }
+    set_cut(p, q.cut, room.p);
+    lin::Copy cx{}, cw{};
+    if (q.copy_x) {
+        cx = copy_of(X, M, K, room.x);
         p.A = static_cast<const uint16_t *>(room.x);
         p.lda = up8(K);
     }
-    if (K > 0 && q.copy_w) {
-        if (const hipError_t e = lin::launch_pad(W->data, W->ld, room.w, up8(K), N, K, s))
-            return status_of(e);
+    if (q.copy_w) {
+        cw = copy_of(W, N, K, room.w);
         p.B = static_cast<const uint16_t *>(room.w);
         p.ldb = up8(K);
     }
-    return status_of(run_product(p, q.cut, lin::Layout::NN, bf16, room.p, s));
+    if (const hipError_t e = lin::launch_prepare(lin::Slope{}, cx, cw, bf16, s))
+        return status_of(e);
+    const hipError_t e = q.cut.tile == 0     ? lin::launch_rowwise(p, bf16, s)
+                         : q.cut.tile == 256 ? lin::launch_tile(p, lin::Layout::NN, bf16, s)
+                                             : lin::launch_ring(p, q.cut.tile, bf16, s);
+    if (e != hipSuccess || p.splits <= 1)
+        return status_of(e);
+    return status_of(lin::launch_reduce(&p, nullptr, bf16, s));
 }
 
 int64_t hg_linear_grad_workspace_size(int64_t M, int64_t N, int64_t K, const hg_matrix *dY, const hg_matrix *W,
@@ -414,15 +491,16 @@ int hg_linear_grad(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *dY
     Arena arena{static_cast<char *>(work)};
     const GradRoom room = room_grad(arena, M, N, K, Wr, Xr);
 
-    // dZ and the bias's gradient.  Without an activation dZ is dY, which the
-    // products read themselves if it is aligned.
-    const bool products = (want_x || want_w) && K > 0;
-    const bool own_dz = products && (need_z || !direct(dY, N));
+    // dZ, its column sums, and the operands that the products cannot load as
+    // they are.  Without an activation dZ is dY, which the products read
+    // themselves if it is aligned.
+    const bool products = K > 0;
+    const bool own_dz = products && (want_x || want_w) && (need_z || !direct(dY, N));
+    lin::Slope g{};
+    lin::Strips b{};
     if (own_dz || dbias != nullptr) {
-        lin::Slope g{};
         g.dY = dY->data;
         g.lddy = dY->ld;
-        g.yvec = vec_ok(dY->data, dY->ld, 2, 16);
         g.act = act;
         if (need_z) {
             g.Z = Z->data;
@@ -430,78 +508,70 @@ int hg_linear_grad(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *dY
             g.Zs = Z->scales;
             g.ldzs = Z->lds;
             g.save = Z->type == HG_E4M3 ? lin::kSave8 : lin::kSave16;
-            g.zvec = Z->type == HG_E4M3 ? vec_ok(Z->data, Z->ld, 1, 8) : vec_ok(Z->data, Z->ld, 2, 16);
         }
         g.D = own_dz ? room.dz : nullptr;
         g.ldd = up8(N);
         g.rows = M;
         g.cols = N;
         g.strip = strip_of(M, N);
-        const int64_t strips = (M + g.strip - 1) / g.strip;
-        if (dbias != nullptr) {
-            g.Q = strips > 1 ? static_cast<float *>(room.q) : nullptr;
-            g.db = dbias;
-        }
         g.accumulate = accumulate;
-        if (const hipError_t e = lin::launch_slope(g, bf16, s))
-            return status_of(e);
-        if (dbias != nullptr && strips > 1)
-            if (const hipError_t e = lin::launch_sum_strips(g.Q, strips, N, dbias, accumulate != 0, s))
-                return status_of(e);
+        if (dbias != nullptr) {
+            const int64_t strips = (M + g.strip - 1) / g.strip;
+            if (strips > 1) {
+                g.Q = static_cast<float *>(room.q);
+                b = {g.Q, dbias, strips, N, accumulate};
+            } else {
+                g.db = dbias;
+            }
+        }
     }
-    if (!products)
-        return HG_OK;
-    const uint16_t *dz = static_cast<const uint16_t *>(own_dz ? room.dz : dY->data);
-    const int64_t lddz = own_dz ? up8(N) : dY->ld;
+    lin::Copy cx{}, cw{};
+    if (products && room.copy_x)
+        cx = copy_of(X, M, K, room.x);
+    if (products && room.copy_w)
+        cw = copy_of(W, N, K, room.w);
+    if (const hipError_t e = lin::launch_prepare(g, cx, cw, bf16, s))
+        return status_of(e);
 
-    if (want_x) {                                 // dX (M×K) = dZ (M×N) · W (N×K, summed over its rows)
-        lin::Product p{};
-        p.A = dz;
-        p.lda = lddz;
-        p.B = static_cast<const uint16_t *>(W->data);
-        p.ldb = W->ld;
-        if (room.copy_w) {
-            if (const hipError_t e = lin::launch_pad(W->data, W->ld, room.w, up8(K), N, K, s))
-                return status_of(e);
-            p.B = static_cast<const uint16_t *>(room.w);
-            p.ldb = up8(K);
-        }
-        p.M = (int32_t)M;
-        p.N = (int32_t)K;
-        p.K = (int32_t)N;
-        set_output(p.f, dX, M, K);
-        if (const hipError_t e = run_product(p, room.cx, lin::Layout::NT, bf16, room.p, s))
-            return status_of(e);
+    lin::Product px{}, pw{};
+    px.A = pw.A = static_cast<const uint16_t *>(own_dz ? room.dz : dY->data);
+    px.lda = pw.lda = own_dz ? up8(N) : dY->ld;
+    const bool do_x = want_x && products, do_w = want_w && products;
+    if (do_x) {                                   // dX (M×K) = dZ (M×N) · W (N×K, summed over its rows)
+        px.B = static_cast<const uint16_t *>(room.copy_w ? room.w : W->data);
+        px.ldb = room.copy_w ? up8(K) : W->ld;
+        px.M = (int32_t)M;
+        px.N = (int32_t)K;
+        px.K = (int32_t)N;
+        set_output(px.f, dX, M, K);
+        set_cut(px, room.cx, room.px);
     }
-    if (want_w) {                                 // dW (N×K) = dZᵀ · X, both summed over their rows
-        lin::Product p{};
-        p.A = dz;
-        p.lda = lddz;
-        p.B = static_cast<const uint16_t *>(X->data);
-        p.ldb = X->ld;
-        if (room.copy_x) {
-            const hipError_t e =
-                X->type == HG_E4M3
-                    ? lin::launch_read8(static_cast<const uint8_t *>(X->data), X->ld, X->scales, X->lds, room.x, up8(K),
-                                        M, K, up8(K), bf16, s)
-                    : lin::launch_pad(X->data, X->ld, room.x, up8(K), M, K, s);
-            if (e != hipSuccess)
-                return status_of(e);
-            p.B = static_cast<const uint16_t *>(room.x);
-            p.ldb = up8(K);
-        }
-        p.M = (int32_t)N;
-        p.N = (int32_t)K;
-        p.K = (int32_t)M;
-        set_output(p.f, dW, N, K);
+    if (do_w) {                                   // dW (N×K) = dZᵀ · X, both summed over their rows
+        pw.B = static_cast<const uint16_t *>(room.copy_x ? room.x : X->data);
+        pw.ldb = room.copy_x ? up8(K) : X->ld;
+        pw.M = (int32_t)N;
+        pw.N = (int32_t)K;
+        pw.K = (int32_t)M;
+        set_output(pw.f, dW, N, K);
         if (accumulate) {
-            p.f.R = dW->data;
-            p.f.ldr = dW->ld;
-            p.f.rvec = p.f.cvec;
+            pw.f.R = dW->data;
+            pw.f.ldr = dW->ld;
         }
-        return status_of(run_product(p, room.cw, lin::Layout::TT, bf16, room.p, s));
+        set_cut(pw, room.cw, room.pw);
     }
-    return HG_OK;
+    const bool big_x = do_x && room.cx.tile == 256, big_w = do_w && room.cw.tile == 256;
+    const int edge = do_x && !big_x ? room.cx.tile : do_w && !big_w ? room.cw.tile : 64;
+    if (const hipError_t e = lin::launch_ring_pair(do_x && !big_x ? &px : nullptr, do_w && !big_w ? &pw : nullptr, b,
+                                                   edge, bf16, s))
+        return status_of(e);
+    if (big_x)
+        if (const hipError_t e = lin::launch_tile(px, lin::Layout::NT, bf16, s))
+            return status_of(e);
+    if (big_w)
+        if (const hipError_t e = lin::launch_tile(pw, lin::Layout::TT, bf16, s))
+            return status_of(e);
+    return status_of(lin::launch_reduce(do_x && px.splits > 1 ? &px : nullptr, do_w && pw.splits > 1 ? &pw : nullptr,
+                                        bf16, s));
 }
 
 int hg_checkpoint8_write(int64_t M, int64_t N, const hg_matrix *X, const hg_matrix *C, void *stream)
@@ -534,7 +604,7 @@ int hg_checkpoint8_read(int64_t M, int64_t N, const hg_matrix *C, const hg_matri
     if (M == 0 || N == 0)
         return HG_OK;
     return status_of(lin::launch_read8(static_cast<const uint8_t *>(C->data), C->ld, C->scales, C->lds, X->data, X->ld,
-                                       M, N, N, X->type == HG_BF16, static_cast<hipStream_t>(stream)));
+                                       M, N, X->type == HG_BF16, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -29,20 +29,31 @@ namespace {
 
 constexpr int BK = kStage, NWAVES = 4, THREADS = 256;
 
+// Ring depth: 64×64 tiles take 80 KiB, so that two workgroups share a CU (one
+// multiplies while the other waits for memory or finishes its tile).
+template <int EDGE>
+constexpr int kSlots = EDGE == 64 ? 5 : 4;
+template <int EDGE>
+constexpr int kLds = kSlots<EDGE> * 2 * EDGE * kStage * 2;
+
+// How a product is spread over workgroups.
+struct Spread {
+    int tiles_m, tiles_n, total;      // total: tiles × slices
+};
+
 template <int EDGE, bool TA, bool TB, bool KCHK, bool BF16>
-__global__ void __launch_bounds__(THREADS, 1) linear_ring_kernel(const Product p, int tiles_m, int tiles_n, int total)
+__device__ __forceinline__ void ring_tile(const Product &p, const Spread &w, int id, unsigned char *smem)
 {
     using SA = Side<EDGE, TA>;
     using SB = Side<EDGE, TB>;
     constexpr int SLOT = SA::BYTES + SB::BYTES;
-    constexpr int NS = (128 * 1024) / SLOT < 8 ? (128 * 1024) / SLOT : 8;     // ring depth
+    constexpr int NS = kSlots<EDGE>;
     constexpr int WT = EDGE / 2, T = WT / 16;                                // wave sub-tile, its 16×16 blocks
     constexpr int LA = SA::L, L = SA::L + SB::L;
-    static_assert(NS >= 4 && LA >= 1 && (NS - 2) * L <= 63 && NS * SLOT >= NWAVES * 16 * WT * 4, "");
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[NS * SLOT];
+    static_assert(NS >= 4 && (NS - 2) * L <= 63 && NS * SLOT == kLds<EDGE> && kLds<EDGE> >= NWAVES * 16 * WT * 4, "");
 
     int slice, tm, tn;
-    place(blockIdx.x, total, tiles_m, tiles_n, slice, tm, tn);
+    place(id, w.total, w.tiles_m, w.tiles_n, slice, tm, tn);
     const int m0 = tm * EDGE, n0 = tn * EDGE, K = p.K;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -159,40 +170,112 @@ __global__ void __launch_bounds__(THREADS, 1) linear_ring_kernel(const Product p
     }
 }
 
-template <int EDGE, bool TA, bool TB, bool BF16>
+template <int EDGE, bool KCHK, bool BF16>
+__global__ void __launch_bounds__(THREADS, 1) linear_ring_kernel(const Product p, const Spread w)
+{
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[kLds<EDGE>];
+    ring_tile<EDGE, false, false, KCHK, BF16>(p, w, blockIdx.x, smem);
+}
+
+// db = (db +) the strips' sums of 32 columns: eight threads to a column, each
+// every eighth strip.
+__device__ __forceinline__ void sum_strips(const Strips &b, int block, unsigned char *smem)
+{
+    constexpr int CW = 32, G = THREADS / CW;
+    float(*part)[CW] = reinterpret_cast<float(*)[CW]>(smem);
+    const int tc = threadIdx.x % CW, g = threadIdx.x / CW;
+    const int64_t col = (int64_t)block * CW + tc;
+    float t = 0.0f;
+    if (col < b.cols) {
+#pragma unroll 4
+        for (int64_t s = g; s < b.strips; s += G)
+            t += b.Q[s * b.cols + col];
+    }
+    part[g][tc] = t;
+    __syncthreads();
+    if (g != 0 || col >= b.cols)
+        return;
+#pragma unroll
+    for (int k = 1; k < G; ++k)
+        t += part[k][tc];
+    b.db[col] = b.accumulate ? b.db[col] + t : t;
+}
+
+// The two products of a gradient and the end of its column sums, which do not
+// depend on each other, in one launch: their tiles fill the GPU together.
+template <int EDGE, bool KCHK, bool BF16>
+__global__ void __launch_bounds__(THREADS, 1)
+linear_ring_pair_kernel(const Product x, const Product y, const Strips b, const Spread wx, const Spread wy)
+{
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[kLds<EDGE>];
+    const int id = blockIdx.x;
+    if (id < wx.total)
+        ring_tile<EDGE, false, true, KCHK, BF16>(x, wx, id, smem);
+    else if (id < wx.total + wy.total)
+        ring_tile<EDGE, true, true, false, BF16>(y, wy, id - wx.total, smem);
+    else
+        sum_strips(b, id - wx.total - wy.total, smem);
+}
+
+Spread spread(const Product &p, int edge, int64_t &total)
+{
+    const int64_t tm = ((int64_t)p.M + edge - 1) / edge, tn = ((int64_t)p.N + edge - 1) / edge;
+    total = tm * tn * p.splits;
+    return {(int)tm, (int)tn, total > 0x7fffffff ? 0 : (int)total};
+}
+
+template <int EDGE, bool BF16>
 hipError_t launch(const Product &p, hipStream_t s)
 {
-    const int tiles_m = (int)(((int64_t)p.M + EDGE - 1) / EDGE), tiles_n = (p.N + EDGE - 1) / EDGE;
-    const int64_t total = (int64_t)tiles_m * tiles_n * p.splits;
+    int64_t total;
+    const Spread w = spread(p, EDGE, total);
     if (total <= 0)
         return hipSuccess;
     if (total > 0x7fffffff)
         return hipErrorInvalidConfiguration;
-    // both k-major: the buffer's range ends the sum
-    if (!(TA && TB) && p.K % BK != 0)
-        hipLaunchKernelGGL((linear_ring_kernel<EDGE, TA, TB, !(TA && TB), BF16>), dim3((unsigned)total), dim3(THREADS),
-                           0, s, p, tiles_m, tiles_n, (int)total);
+    if (p.K % BK != 0)
+        hipLaunchKernelGGL((linear_ring_kernel<EDGE, true, BF16>), dim3((unsigned)total), dim3(THREADS), 0, s, p, w);
     else
-        hipLaunchKernelGGL((linear_ring_kernel<EDGE, TA, TB, false, BF16>), dim3((unsigned)total), dim3(THREADS), 0,
-                           s, p, tiles_m, tiles_n, (int)total);
+        hipLaunchKernelGGL((linear_ring_kernel<EDGE, false, BF16>), dim3((unsigned)total), dim3(THREADS), 0, s, p, w);
     return hipGetLastError();
 }
 
-template <int EDGE>
-hipError_t launch_layout(const Product &p, Layout l, bool bf16, hipStream_t s)
+template <int EDGE, bool BF16>
+hipError_t launch_pair(const Product *x, const Product *y, const Strips &b, hipStream_t s)
 {
-    switch (l) {
-    case Layout::NN: return bf16 ? launch<EDGE, false, false, true>(p, s) : launch<EDGE, false, false, false>(p, s);
-    case Layout::NT: return bf16 ? launch<EDGE, false, true, true>(p, s) : launch<EDGE, false, true, false>(p, s);
-    default: return bf16 ? launch<EDGE, true, true, true>(p, s) : launch<EDGE, true, true, false>(p, s);
-    }
+    const Product none{};
+    const Product &px = x ? *x : none, &py = y ? *y : none;
+    int64_t tx, ty;
+    const Spread wx = spread(px, EDGE, tx), wy = spread(py, EDGE, ty);
+    const int64_t total = tx + ty + (b.strips > 0 ? (b.cols + 31) / 32 : 0);
+    if (total <= 0)
+        return hipSuccess;
+    if (total > 0x7fffffff)
+        return hipErrorInvalidConfiguration;
+    // (both k-major: the buffer's range ends the sum)
+    if (px.K % BK != 0)
+        hipLaunchKernelGGL((linear_ring_pair_kernel<EDGE, true, BF16>), dim3((unsigned)total), dim3(THREADS), 0, s, px,
+                           py, b, wx, wy);
+    else
+        hipLaunchKernelGGL((linear_ring_pair_kernel<EDGE, false, BF16>), dim3((unsigned)total), dim3(THREADS), 0, s, px,
+                           py, b, wx, wy);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_ring(const Product &p, Layout l, int tile, bool bf16, hipStream_t s)
+hipError_t launch_ring(const Product &p, int tile, bool bf16, hipStream_t s)
 {
-    return tile >= 128 ? launch_layout<128>(p, l, bf16, s) : launch_layout<64>(p, l, bf16, s);
+    if (tile >= 128)
+        return bf16 ? launch<128, true>(p, s) : launch<128, false>(p, s);
+    return bf16 ? launch<64, true>(p, s) : launch<64, false>(p, s);
+}
+
+hipError_t launch_ring_pair(const Product *x, const Product *w, const Strips &b, int tile, bool bf16, hipStream_t s)
+{
+    if (tile >= 128)
+        return bf16 ? launch_pair<128, true>(x, w, b, s) : launch_pair<128, false>(x, w, b, s);
+    return bf16 ? launch_pair<64, true>(x, w, b, s) : launch_pair<64, false>(x, w, b, s);
 }
 
 }  // namespace lin

@@ -1,6 +1,7 @@
 // hg_linear_rows.hip — the passes of the linear layer that go over a matrix
-// once: 8-bit checkpoints written and read, dZ = dY·act'(Z) with its column
-// sums, partial sums added up, operands copied to aligned rows.
+// once: 8-bit checkpoints written and read, what the gradient's products wait
+// for (dZ = dY·act'(Z) with its column sums, operands brought into rows that
+// the tiles can load), partial sums added up.
 //
 // All of them are bound by memory: a thread takes eight consecutive columns
 // (16 bytes of 16-bit elements), so a wave moves whole 128-byte lines, and
@@ -13,27 +14,11 @@ namespace {
 
 constexpr int THREADS = 256;
 
-// Blocks of a grid-stride launch over `units` threads' work.
-unsigned blocks_for(int64_t units)
+// Blocks of a grid-stride pass over `units` threads' work.
+int blocks_for(int64_t units)
 {
     const int64_t b = (units + THREADS - 1) / THREADS, most = (int64_t)cu_count() * 32;
-    return (unsigned)(b < most ? b : most);
-}
-
-__global__ void __launch_bounds__(THREADS) pad_kernel(const uint16_t *__restrict__ S, int64_t lds,
-                                                      uint16_t *__restrict__ D, int64_t ldd, int64_t rows, int64_t cols)
-{
-    const int64_t units = ldd / 8, total = rows * units;
-    for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < total; i += (int64_t)gridDim.x * THREADS) {
-        const int64_t r = i / units, c = (i - r * units) * 8;
-        const uint16_t *s = S + r * lds + c;
-        u32x4 w = {0, 0, 0, 0};
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (c + e < cols)
-                w[e >> 1] |= (uint32_t)s[e] << (16 * (e & 1));
-        *reinterpret_cast<u32x4 *>(D + r * ldd + c) = w;
-    }
+    return (int)(b < most ? b : most);
 }
 
 template <bool WIDE>
@@ -50,88 +35,133 @@ __global__ void __launch_bounds__(THREADS) zero_kernel(void *C, int64_t ldc, int
 }
 
 // Four neighbouring lanes hold one block of 32 columns; units past the last
-// column or row take part in the block's largest value with zeros.
+// column take part in the block's largest value with zeros.  (total is a
+// multiple of four, so the four are in the loop together.)
 template <bool BF16>
 __global__ void __launch_bounds__(THREADS) write8_kernel(const uint16_t *__restrict__ X, int64_t ldx,
                                                          uint8_t *__restrict__ C, int64_t ldc, uint8_t *__restrict__ S,
-                                                         int64_t lds, int64_t rows, int64_t cols, int xvec, int cvec)
+                                                         int64_t lds, int64_t rows, int64_t cols)
 {
     const int64_t units = (cols + kBlock8 - 1) / kBlock8 * 4, total = rows * units;
-    const int64_t end = (total + 3) & ~(int64_t)3;
-    for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < end; i += (int64_t)gridDim.x * THREADS) {
+    for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < total; i += (int64_t)gridDim.x * THREADS) {
         const int64_t r = i / units, c = (i - r * units) * 8;
         const int n = (int)(cols - c < 8 ? cols - c : 8);       // may be <= 0 in a short last block
         float v[8];
-        load8<BF16>(X + r * ldx + c, n, xvec, v);
+        load8<BF16>(X + r * ldx + c, n, v);
         float a = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             a = __builtin_fmaxf(a, finite_abs(v[e]));
         const int x = scale_exponent<BF16>(max_of_4(a));
         if (n > 0)
-            store_codes(C + r * ldc + c, n, cvec, codes8<BF16>(v, x));
+            store_codes(C + r * ldc + c, n, codes8<BF16>(v, x));
         if (c % kBlock8 == 0)
             S[r * lds + c / kBlock8] = (uint8_t)(x + 127);
     }
+}
+
+// The values of n codes from column c of a row on (the others 0).
+__device__ __forceinline__ void restore8(const uint8_t *codes, const uint8_t *scales, int64_t c, int n, float (&v)[8])
+{
+    values8(load_codes(codes + c, n), scale_of(scales[c / kBlock8]), v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] = e < n ? v[e] : 0.0f;
 }
 
 template <bool BF16>
 __global__ void __launch_bounds__(THREADS) read8_kernel(const uint8_t *__restrict__ C, int64_t ldc,
                                                         const uint8_t *__restrict__ S, int64_t lds,
                                                         uint16_t *__restrict__ X, int64_t ldx, int64_t rows,
-                                                        int64_t cols, int64_t pad, int xvec, int cvec)
+                                                        int64_t cols)
 {
-    const int64_t units = (pad + 7) / 8, total = rows * units;
+    const int64_t units = (cols + 7) / 8, total = rows * units;
     for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < total; i += (int64_t)gridDim.x * THREADS) {
         const int64_t r = i / units, c = (i - r * units) * 8;
         const int n = (int)(cols - c < 8 ? cols - c : 8);
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (n > 0) {
-            const float s = scale_of(S[r * lds + c / kBlock8]);
-            values8(load_codes(C + r * ldc + c, n, cvec), s, v);
+        float v[8];
+        restore8(C + r * ldc, S + r * lds, c, n, v);
+        store8<BF16>(X + r * ldx + c, n, v);
+    }
+}
+
+// One matrix into aligned rows with zeros behind its last column, by blocks
+// block, block + blocks, ..
+template <bool BF16>
+__device__ __forceinline__ void copy_rows(const Copy &q, int block, int blocks)
+{
+    const int64_t units = q.ldd / 8, total = q.rows * units;
+    for (int64_t i = (int64_t)block * THREADS + threadIdx.x; i < total; i += (int64_t)blocks * THREADS) {
+        const int64_t r = i / units, c = (i - r * units) * 8;
+        const int n = (int)(q.cols - c < 8 ? q.cols - c : 8);   // at least 1: ldd is cols rounded up to 8
+        u32x4 w;
+        if (q.scales) {
+            float v[8];
+            restore8(static_cast<const uint8_t *>(q.src) + r * q.lds, q.scales + r * q.ldss, c, n, v);
+            w = pack8<BF16>(v);
+        } else {
+            const uint16_t *s = static_cast<const uint16_t *>(q.src) + r * q.lds + c;
+            if (n == 8) {
+                w = *reinterpret_cast<const u32x4_any *>(s);
+            } else {
+                w = u32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = e < n ? v[e] : 0.0f;
+                for (int e = 0; e < 8; ++e)
+                    if (e < n)
+                        w[e >> 1] |= (uint32_t)s[e] << (16 * (e & 1));
+            }
         }
-        store8<BF16>(X + r * ldx + c, (int)(pad - c < 8 ? pad - c : 8), xvec, v);
+        *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(q.dst) + r * q.ldd + c) = w;
     }
 }
 
 // dZ and its column sums.  A workgroup takes 256 columns (32 threads of eight)
-// of one strip of rows, eight rows at a time; each thread keeps its columns'
-// sums in fp32 registers, the eight rows' threads are added in a fixed order
-// through LDS, and the strips by a second launch: no atomics.
-constexpr int SC = 32, SR = THREADS / SC;
+// of one strip of rows, eight rows at a time and four of those in flight; each
+// thread keeps its columns' sums in fp32 registers, the eight rows' threads
+// are added in a fixed order through LDS, and the strips by a later launch: no
+// atomics.  A product's operand is rounded to 16 bits here; the sums take the
+// unrounded values.
+constexpr int SC = 32, SR = THREADS / SC, SU = 4;
 template <bool BF16, int ACT, int SAVE>
-__global__ void __launch_bounds__(THREADS) slope_kernel(const Slope p)
+__device__ __forceinline__ void slope_strip(const Slope &p, int tile, int strip)
 {
     __shared__ float part[SR][SC * 8 + 8];
     const int tc = threadIdx.x % SC, tr = threadIdx.x / SC;
-    const int64_t c = (int64_t)blockIdx.x * (SC * 8) + tc * 8;
-    const int64_t r0 = (int64_t)blockIdx.y * p.strip, r1 = r0 + p.strip < p.rows ? r0 + p.strip : p.rows;
+    const int64_t c = (int64_t)tile * (SC * 8) + tc * 8;
+    const int64_t r0 = strip * p.strip, r1 = r0 + p.strip < p.rows ? r0 + p.strip : p.rows;
     const int n = (int)(p.cols - c < 8 ? p.cols - c : 8);
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (n > 0) {
-        const uint16_t *dy = static_cast<const uint16_t *>(p.dY) + c;
-#pragma unroll 4
-        for (int64_t r = r0 + tr; r < r1; r += SR) {
-            float y[8], z[8];
-            load8<BF16>(dy + r * p.lddy, n, p.yvec, y);
-            if constexpr (ACT != kNone) {
-                if constexpr (SAVE == kSave8)
-                    values8(load_codes(static_cast<const uint8_t *>(p.Z) + r * p.ldz + c, n, p.zvec),
-                            scale_of(p.Zs[r * p.ldzs + c / kBlock8]), z);
-                else
-                    load8<BF16>(static_cast<const uint16_t *>(p.Z) + r * p.ldz + c, n, p.zvec, z);
+        for (int64_t r = r0 + tr; r < r1; r += SR * SU) {
+            float y[SU][8], z[SU][8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    y[e] = e < n ? slope<ACT>(y[e], z[e]) : 0.0f;
+            for (int u = 0; u < SU; ++u) {
+                // past the strip: its last row again, dropped below
+                const int64_t q = r + u * SR < r1 ? r + u * SR : r1 - 1;
+                load8<BF16>(static_cast<const uint16_t *>(p.dY) + q * p.lddy + c, n, y[u]);
+                if constexpr (ACT != kNone) {
+                    if constexpr (SAVE == kSave8)
+                        restore8(static_cast<const uint8_t *>(p.Z) + q * p.ldz, p.Zs + q * p.ldzs, c, n, z[u]);
+                    else
+                        load8<BF16>(static_cast<const uint16_t *>(p.Z) + q * p.ldz + c, n, z[u]);
+                }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                sum[e] += y[e];
-            if (p.D)
-                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.D) + r * p.ldd + c) = pack8<BF16>(y);
+            for (int u = 0; u < SU; ++u) {
+                const int64_t q = r + u * SR;
+                if (q >= r1)
+                    break;
+                if constexpr (ACT != kNone) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[u][e] = e < n ? slope<ACT>(y[u][e], z[u][e]) : 0.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sum[e] += y[u][e];
+                if (p.D)
+                    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.D) + q * p.ldd + c) = pack8<BF16>(y[u]);
+            }
         }
     }
     if (!p.Q && !p.db)
@@ -140,7 +170,7 @@ __global__ void __launch_bounds__(THREADS) slope_kernel(const Slope p)
     for (int e = 0; e < 8; ++e)
         part[tr][tc * 8 + e] = sum[e];
     __syncthreads();
-    const int64_t col = (int64_t)blockIdx.x * (SC * 8) + threadIdx.x;
+    const int64_t col = (int64_t)tile * (SC * 8) + threadIdx.x;
     if (col >= p.cols)
         return;
     float t = 0.0f;
@@ -148,42 +178,30 @@ __global__ void __launch_bounds__(THREADS) slope_kernel(const Slope p)
     for (int g = 0; g < SR; ++g)
         t += part[g][threadIdx.x];
     if (p.Q)
-        p.Q[blockIdx.y * p.cols + col] = t;
+        p.Q[strip * p.cols + col] = t;
     else
         p.db[col] = p.accumulate ? p.db[col] + t : t;
 }
 
-// db = (db +) the strips' sums: 32 columns per workgroup, eight threads to a
-// column, each every eighth strip.
-__global__ void __launch_bounds__(THREADS) sum_strips_kernel(const float *__restrict__ Q, int64_t strips, int64_t cols,
-                                                             float *__restrict__ db, int accumulate)
+template <bool BF16, int ACT, int SAVE>
+__global__ void __launch_bounds__(THREADS) prepare_kernel(const Slope g, const Copy x, const Copy w, int tiles,
+                                                          int slopes, int xblocks, int wblocks)
 {
-    constexpr int CW = 32, G = THREADS / CW;
-    __shared__ float part[G][CW];
-    const int tc = threadIdx.x % CW, g = threadIdx.x / CW;
-    const int64_t col = (int64_t)blockIdx.x * CW + tc;
-    float t = 0.0f;
-    if (col < cols) {
-#pragma unroll 4
-        for (int64_t s = g; s < strips; s += G)
-            t += Q[s * cols + col];
-    }
-    part[g][tc] = t;
-    __syncthreads();
-    if (g != 0 || col >= cols)
-        return;
-#pragma unroll
-    for (int k = 1; k < G; ++k)
-        t += part[k][tc];
-    db[col] = accumulate ? db[col] + t : t;
+    const int b = blockIdx.x;
+    if (b < slopes)
+        slope_strip<BF16, ACT, SAVE>(g, b % tiles, b / tiles);
+    else if (b < slopes + xblocks)
+        copy_rows<BF16>(x, b - slopes, xblocks);
+    else
+        copy_rows<BF16>(w, b - slopes - xblocks, wblocks);
 }
 
-// The slices' partial sums added in order, then what a product's epilogue does.
+// One product's slices added in order, then what its epilogue does.
 template <bool BF16>
-__global__ void __launch_bounds__(THREADS) reduce_kernel(const Product p)
+__device__ __forceinline__ void reduce_rows(const Product &p, int block, int blocks)
 {
     const int64_t units = ((int64_t)p.N + kBlock8 - 1) / kBlock8 * 4, total = (int64_t)p.M * units;
-    for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < total; i += (int64_t)gridDim.x * THREADS) {
+    for (int64_t i = (int64_t)block * THREADS + threadIdx.x; i < total; i += (int64_t)blocks * THREADS) {
         const int row = (int)(i / units), col = (int)(i - row * units) * 8;
         float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, b[8];
         if (col < p.N) {
@@ -205,103 +223,97 @@ __global__ void __launch_bounds__(THREADS) reduce_kernel(const Product p)
         finish8<BF16>(p.f, row, col, v, b);
     }
 }
-
-bool aligned(const void *p, int64_t ld, int64_t bytes, int64_t each)
-{
-    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * each % bytes == 0;
-}
-
-template <bool BF16, int ACT>
-void slope_save(const Slope &p, dim3 grid, hipStream_t s)
-{
-    if (p.save == kSave8)
-        hipLaunchKernelGGL((slope_kernel<BF16, ACT, kSave8>), grid, dim3(THREADS), 0, s, p);
-    else
-        hipLaunchKernelGGL((slope_kernel<BF16, ACT, kSave16>), grid, dim3(THREADS), 0, s, p);
-}
 template <bool BF16>
-void slope_act(const Slope &p, dim3 grid, hipStream_t s)
+__global__ void __launch_bounds__(THREADS) reduce_kernel(const Product p, const Product q, int pblocks, int qblocks)
 {
-    switch (p.act) {
-    case kRelu: slope_save<BF16, kRelu>(p, grid, s); break;
-    case kGelu: slope_save<BF16, kGelu>(p, grid, s); break;
-    case kGeluTanh: slope_save<BF16, kGeluTanh>(p, grid, s); break;
-    case kSilu: slope_save<BF16, kSilu>(p, grid, s); break;
-    default: hipLaunchKernelGGL((slope_kernel<BF16, kNone, kSave16>), grid, dim3(THREADS), 0, s, p); break;
+    if ((int)blockIdx.x < pblocks)
+        reduce_rows<BF16>(p, blockIdx.x, pblocks);
+    else
+        reduce_rows<BF16>(q, blockIdx.x - pblocks, qblocks);
+}
+
+template <bool BF16>
+hipError_t prepare(const Slope &g, const Copy &x, const Copy &w, hipStream_t s)
+{
+    const int64_t tiles = g.rows > 0 ? (g.cols + SC * 8 - 1) / (SC * 8) : 0;
+    const int64_t slopes = g.rows > 0 ? tiles * ((g.rows + g.strip - 1) / g.strip) : 0;
+    const int xb = x.rows > 0 ? blocks_for(x.rows * (x.ldd / 8)) : 0, wb = w.rows > 0 ? blocks_for(w.rows * (w.ldd / 8)) : 0;
+    const int64_t total = slopes + xb + wb;
+    if (total == 0)
+        return hipSuccess;
+    if (total > 0x7fffffff)
+        return hipErrorInvalidConfiguration;
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)total), dim3(THREADS), 0, s, g, x, w, (int)(tiles > 0 ? tiles : 1),
+                           (int)slopes, xb, wb);
+    };
+    const bool e = g.save == kSave8;
+    switch (g.act) {
+    case kRelu: e ? go(prepare_kernel<BF16, kRelu, kSave8>) : go(prepare_kernel<BF16, kRelu, kSave16>); break;
+    case kGelu: e ? go(prepare_kernel<BF16, kGelu, kSave8>) : go(prepare_kernel<BF16, kGelu, kSave16>); break;
+    case kGeluTanh: e ? go(prepare_kernel<BF16, kGeluTanh, kSave8>) : go(prepare_kernel<BF16, kGeluTanh, kSave16>); break;
+    case kSilu: e ? go(prepare_kernel<BF16, kSilu, kSave8>) : go(prepare_kernel<BF16, kSilu, kSave16>); break;
+    default: go(prepare_kernel<BF16, kNone, kSave16>); break;
     }
+    return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_pad(const void *S, int64_t lds, void *D, int64_t ldd, int64_t rows, int64_t cols, hipStream_t s)
-{
-    hipLaunchKernelGGL(pad_kernel, dim3(blocks_for(rows * (ldd / 8))), dim3(THREADS), 0, s,
-                       static_cast<const uint16_t *>(S), lds, static_cast<uint16_t *>(D), ldd, rows, cols);
-    return hipGetLastError();
-}
-
 hipError_t launch_zero(void *C, int64_t ldc, int64_t rows, int64_t cols, bool wide, hipStream_t s)
 {
+    const dim3 grid((unsigned)blocks_for(rows * cols));
     if (wide)
-        hipLaunchKernelGGL((zero_kernel<true>), dim3(blocks_for(rows * cols)), dim3(THREADS), 0, s, C, ldc, rows, cols);
+        hipLaunchKernelGGL((zero_kernel<true>), grid, dim3(THREADS), 0, s, C, ldc, rows, cols);
     else
-        hipLaunchKernelGGL((zero_kernel<false>), dim3(blocks_for(rows * cols)), dim3(THREADS), 0, s, C, ldc, rows, cols);
+        hipLaunchKernelGGL((zero_kernel<false>), grid, dim3(THREADS), 0, s, C, ldc, rows, cols);
     return hipGetLastError();
 }
 
 hipError_t launch_write8(const void *X, int64_t ldx, uint8_t *C, int64_t ldc, uint8_t *S, int64_t lds, int64_t rows,
                          int64_t cols, bool bf16, hipStream_t s)
 {
-    const unsigned b = blocks_for(rows * ((cols + kBlock8 - 1) / kBlock8 * 4));
-    const int xv = aligned(X, ldx, 16, 2), cv = aligned(C, ldc, 8, 1);
+    const dim3 grid((unsigned)blocks_for(rows * ((cols + kBlock8 - 1) / kBlock8 * 4)));
     const uint16_t *x = static_cast<const uint16_t *>(X);
     if (bf16)
-        hipLaunchKernelGGL((write8_kernel<true>), dim3(b), dim3(THREADS), 0, s, x, ldx, C, ldc, S, lds, rows, cols, xv, cv);
+        hipLaunchKernelGGL((write8_kernel<true>), grid, dim3(THREADS), 0, s, x, ldx, C, ldc, S, lds, rows, cols);
     else
-        hipLaunchKernelGGL((write8_kernel<false>), dim3(b), dim3(THREADS), 0, s, x, ldx, C, ldc, S, lds, rows, cols, xv, cv);
+        hipLaunchKernelGGL((write8_kernel<false>), grid, dim3(THREADS), 0, s, x, ldx, C, ldc, S, lds, rows, cols);
     return hipGetLastError();
 }
 
 hipError_t launch_read8(const uint8_t *C, int64_t ldc, const uint8_t *S, int64_t lds, void *X, int64_t ldx, int64_t rows,
-                        int64_t cols, int64_t pad, bool bf16, hipStream_t s)
+                        int64_t cols, bool bf16, hipStream_t s)
 {
-    const unsigned b = blocks_for(rows * ((pad + 7) / 8));
-    const int xv = aligned(X, ldx, 16, 2), cv = aligned(C, ldc, 8, 1);
+    const dim3 grid((unsigned)blocks_for(rows * ((cols + 7) / 8)));
     uint16_t *x = static_cast<uint16_t *>(X);
     if (bf16)
-        hipLaunchKernelGGL((read8_kernel<true>), dim3(b), dim3(THREADS), 0, s, C, ldc, S, lds, x, ldx, rows, cols, pad, xv, cv);
+        hipLaunchKernelGGL((read8_kernel<true>), grid, dim3(THREADS), 0, s, C, ldc, S, lds, x, ldx, rows, cols);
     else
-        hipLaunchKernelGGL((read8_kernel<false>), dim3(b), dim3(THREADS), 0, s, C, ldc, S, lds, x, ldx, rows, cols, pad, xv, cv);
+        hipLaunchKernelGGL((read8_kernel<false>), grid, dim3(THREADS), 0, s, C, ldc, S, lds, x, ldx, rows, cols);
     return hipGetLastError();
 }
 
-hipError_t launch_slope(const Slope &p, bool bf16, hipStream_t s)
+hipError_t launch_prepare(const Slope &g, const Copy &x, const Copy &w, bool bf16, hipStream_t s)
 {
-    const int64_t strips = (p.rows + p.strip - 1) / p.strip, tiles = (p.cols + SC * 8 - 1) / (SC * 8);
-    if (strips > 65535 || tiles > 0x7fffffff)
-        return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)tiles, (unsigned)strips);
+    return bf16 ? prepare<true>(g, x, w, s) : prepare<false>(g, x, w, s);
+}
+
+hipError_t launch_reduce(const Product *p, const Product *q, bool bf16, hipStream_t s)
+{
+    auto blocks = [](const Product *x) {
+        return x ? blocks_for((int64_t)x->M * (((int64_t)x->N + kBlock8 - 1) / kBlock8 * 4)) : 0;
+    };
+    const int pb = blocks(p), qb = blocks(q);
+    const Product none{};
+    if (pb + qb == 0)
+        return hipSuccess;
     if (bf16)
-        slope_act<true>(p, grid, s);
+        hipLaunchKernelGGL((reduce_kernel<true>), dim3((unsigned)(pb + qb)), dim3(THREADS), 0, s, p ? *p : none,
+                           q ? *q : none, pb, qb);
     else
-        slope_act<false>(p, grid, s);
-    return hipGetLastError();
-}
-
-hipError_t launch_sum_strips(const float *Q, int64_t strips, int64_t cols, float *db, bool accumulate, hipStream_t s)
-{
-    hipLaunchKernelGGL(sum_strips_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(THREADS), 0, s, Q, strips, cols, db,
-                       accumulate ? 1 : 0);
-    return hipGetLastError();
-}
-
-hipError_t launch_reduce(const Product &p, bool bf16, hipStream_t s)
-{
-    const unsigned b = blocks_for((int64_t)p.M * (((int64_t)p.N + kBlock8 - 1) / kBlock8 * 4));
-    if (bf16)
-        hipLaunchKernelGGL((reduce_kernel<true>), dim3(b), dim3(THREADS), 0, s, p);
-    else
-        hipLaunchKernelGGL((reduce_kernel<false>), dim3(b), dim3(THREADS), 0, s, p);
+        hipLaunchKernelGGL((reduce_kernel<false>), dim3((unsigned)(pb + qb)), dim3(THREADS), 0, s, p ? *p : none,
+                           q ? *q : none, pb, qb);
     return hipGetLastError();
 }
 

@@ -26,7 +26,6 @@ namespace lin {
 namespace {
 
 constexpr int WAVES = 8, THREADS = WAVES * 64, PIECE = 64;
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
 // k .. k+7 of a row, zero from K on.
 __device__ __forceinline__ half8 tail8(const uint16_t *row, int k, int K)
