@@ -480,30 +480,64 @@ __device__ __forceinline__ int scale_exponent(float amax)
     const int e = (int)(b >> 23) - 135 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
     return BF16 ? max(e, -117) : min(max(e, -15), 8);
 }
-__device__ __forceinline__ float finite_abs(float v)
+// The largest of four neighbouring lanes' values (lanes 4i .. 4i + 3).
+__device__ __forceinline__ float max_of_4(float v)
 {
-    const float a = __builtin_fabsf(v);
-    return a < __builtin_inff() ? a : 0.0f;
+    const int a = __builtin_bit_cast(int, v);
+    v = __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(a, 0xb1, 0xf, 0xf, true)));   // 1 0 3 2
+    const int b = __builtin_bit_cast(int, v);
+    return __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(b, 0x4e, 0xf, 0xf, true)));  // 2 3 0 1
 }
-// The codes of eight values that share the exponent e (inf and NaN: NaN).
-template <bool BF16>
-__device__ __forceinline__ u32x2 codes8(const float (&v)[8], int e)
+
+__device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float d)
 {
-    const float inv = __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
-    const float lim = e == (BF16 ? 120 : 8) ? 240.0f : 448.0f;
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+// One eighth of a block per lane, four neighbouring lanes to a block: the
+// codes of the first n values and the block's exponent (returned).
+//
+// Ordinarily an element costs a multiplication, half a conversion and half of
+// a three-way maximum: the maximum skips NaN, the conversion turns NaN into a
+// NaN code, and nothing can pass 448 (see scale_exponent).  Blocks with an
+// infinity or at the largest exponent go the long way.
+template <bool BF16>
+__device__ __forceinline__ int encode8(const float (&v)[8], int n, u32x2 &w)
+{
+    // the largest magnitude whose exponent is below the largest, 448·2^(emax - 1)
+    constexpr float ordinary = BF16 ? 448.0f * 0x1p119f : 448.0f * 0x1p7f;
+    float a = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        a = __builtin_fmaxf(a, e < n ? __builtin_fabsf(v[e]) : 0.0f);
+    a = max_of_4(a);
+    if (__builtin_expect(a <= ordinary, 1)) {
+        const int x = scale_exponent<BF16>(a);
+        const float inv = __builtin_bit_cast(float, (uint32_t)(127 - x) << 23);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = pack_codes(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+        return x;
+    }
+    a = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float m = __builtin_fabsf(v[e]);
+        a = e < n && m < __builtin_inff() ? __builtin_fmaxf(a, m) : a;
+    }
+    const int x = scale_exponent<BF16>(max_of_4(a));
+    const float inv = __builtin_bit_cast(float, (uint32_t)(127 - x) << 23);
+    const float lim = x == (BF16 ? 120 : 8) ? 240.0f : 448.0f;
     float s[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float x = __builtin_fminf(__builtin_fmaxf(v[i] * inv, -lim), lim);
-        s[i] = __builtin_fabsf(v[i]) < __builtin_inff() ? x : __builtin_nanf("");
+        const float c = __builtin_fminf(__builtin_fmaxf(v[i] * inv, -lim), lim);
+        s[i] = __builtin_fabsf(v[i]) < __builtin_inff() ? c : __builtin_nanf("");
     }
-    u32x2 w;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        int c = __builtin_amdgcn_cvt_pk_fp8_f32(s[4 * i], s[4 * i + 1], 0, false);
-        w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(s[4 * i + 2], s[4 * i + 3], c, true);
-    }
-    return w;
+    for (int i = 0; i < 2; ++i)
+        w[i] = pack_codes(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+    return x;
 }
 // 2^(byte - 127); byte 0 stands for 2^-127 and 255 for NaN.
 __device__ __forceinline__ float scale_of(uint32_t byte)
@@ -546,15 +580,6 @@ __device__ __forceinline__ void store_codes(uint8_t *p, int n, u32x2 w)
         if (e < n)
             p[e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
 }
-// The largest of four neighbouring lanes' values (lanes 4i .. 4i + 3).
-__device__ __forceinline__ float max_of_4(float v)
-{
-    const int a = __builtin_bit_cast(int, v);
-    v = __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(a, 0xb1, 0xf, 0xf, true)));   // 1 0 3 2
-    const int b = __builtin_bit_cast(int, v);
-    return __builtin_fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(b, 0x4e, 0xf, 0xf, true)));  // 2 3 0 1
-}
-
 // Finishes eight consecutive columns col .. col + 7 (col a multiple of 8) of
 // one row, `b` their biases.  Called by whole waves in which lanes 4i .. 4i + 3
 // hold the four eighths of one block of 32 columns (an 8-bit save takes their
@@ -573,13 +598,10 @@ __device__ __forceinline__ void finish8(const Finish &f, int row, int col, float
         if (n > 0)
             store8<BF16>(static_cast<uint16_t *>(f.Z) + (int64_t)row * f.ldz + col, n, v);
     } else if (f.save == kSave8) {
-        float a = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            a = __builtin_fmaxf(a, e < n ? finite_abs(v[e]) : 0.0f);
-        const int x = scale_exponent<BF16>(max_of_4(a));
+        u32x2 w;
+        const int x = encode8<BF16>(v, n, w);
         if (n > 0) {
-            store_codes(static_cast<uint8_t *>(f.Z) + (int64_t)row * f.ldz + col, n, codes8<BF16>(v, x));
+            store_codes(static_cast<uint8_t *>(f.Z) + (int64_t)row * f.ldz + col, n, w);
             if (col % kBlock8 == 0)
                 f.Zs[(int64_t)row * f.ldzs + col / kBlock8] = (uint8_t)(x + 127);
         }
@@ -765,12 +787,9 @@ struct Drain {
             uint8_t *z = static_cast<uint8_t *>(f.Z) + row * f.ldz + col, *zs = f.Zs + row * f.ldzs + col / kBlock8;
 #pragma unroll
             for (int t = 0; t < PASSES; ++t, z += ROWS * f.ldz, zs += ROWS * f.ldzs) {
-                float a = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    a = __builtin_fmaxf(a, finite_abs(v[t][e]));
-                const int x = scale_exponent<BF16>(max_of_4(a));
-                *reinterpret_cast<u32x2_any *>(z) = codes8<BF16>(v[t], x);
+                u32x2 w;
+                const int x = encode8<BF16>(v[t], 8, w);
+                *reinterpret_cast<u32x2_any *>(z) = w;
                 if (unit % 4 == 0)
                     *zs = (uint8_t)(x + 127);
             }

@@ -263,15 +263,15 @@ LinearRoom room_linear(Arena &a, const LinearPlan &q, int64_t M, int64_t N, int6
 }
 
 // Rows per strip of the column sums: enough strips to fill the GPU, at least
-// 64 rows each; up to 128 rows are one strip (no second launch).
+// 64 rows each; up to 128 rows are one strip, which ends the sums itself.
 int64_t strip_of(int64_t M, int64_t N)
 {
-    const int64_t tiles = std::max<int64_t>(1, (N + 255) / 256);
+    const int64_t tiles = std::max<int64_t>(1, (N + 127) / 128);
     if (M <= 128)
         return std::max<int64_t>(M, 1);
-    const int64_t want = std::max<int64_t>(1, 8 * (int64_t)hg::cu_count() / tiles);
+    const int64_t want = std::max<int64_t>(1, 16 * (int64_t)hg::cu_count() / tiles);
     const int64_t rows = std::max<int64_t>((M + want - 1) / want, 64);
-    return std::max((rows + 7) / 8 * 8, (M + 65534) / 65535);
+    return (rows + 63) / 64 * 64;
 }
 
 struct GradRoom {

@@ -48,13 +48,10 @@ __global__ void __launch_bounds__(THREADS) write8_kernel(const uint16_t *__restr
         const int n = (int)(cols - c < 8 ? cols - c : 8);       // may be <= 0 in a short last block
         float v[8];
         load8<BF16>(X + r * ldx + c, n, v);
-        float a = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            a = __builtin_fmaxf(a, finite_abs(v[e]));
-        const int x = scale_exponent<BF16>(max_of_4(a));
+        u32x2 w;
+        const int x = encode8<BF16>(v, n, w);
         if (n > 0)
-            store_codes(C + r * ldc + c, n, codes8<BF16>(v, x));
+            store_codes(C + r * ldc + c, n, w);
         if (c % kBlock8 == 0)
             S[r * lds + c / kBlock8] = (uint8_t)(x + 127);
     }
@@ -115,13 +112,13 @@ __device__ __forceinline__ void copy_rows(const Copy &q, int block, int blocks)
     }
 }
 
-// dZ and its column sums.  A workgroup takes 256 columns (32 threads of eight)
-// of one strip of rows, eight rows at a time and four of those in flight; each
-// thread keeps its columns' sums in fp32 registers, the eight rows' threads
-// are added in a fixed order through LDS, and the strips by a later launch: no
+// dZ and its column sums.  A workgroup takes 128 columns (16 threads of eight)
+// of one strip of rows, 16 rows at a time and four of those in flight; each
+// thread keeps its columns' sums in fp32 registers, the 16 rows' threads are
+// added in a fixed order through LDS, and the strips by a later launch: no
 // atomics.  A product's operand is rounded to 16 bits here; the sums take the
 // unrounded values.
-constexpr int SC = 32, SR = THREADS / SC, SU = 4;
+constexpr int SC = 16, SR = THREADS / SC, SU = 4;
 template <bool BF16, int ACT, int SAVE>
 __device__ __forceinline__ void slope_strip(const Slope &p, int tile, int strip)
 {
@@ -171,7 +168,7 @@ __device__ __forceinline__ void slope_strip(const Slope &p, int tile, int strip)
         part[tr][tc * 8 + e] = sum[e];
     __syncthreads();
     const int64_t col = (int64_t)tile * (SC * 8) + threadIdx.x;
-    if (col >= p.cols)
+    if (threadIdx.x >= SC * 8 || col >= p.cols)
         return;
     float t = 0.0f;
 #pragma unroll

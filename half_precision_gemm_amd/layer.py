@@ -48,21 +48,27 @@ lib.hg_checkpoint8_read.restype = _int
 # torch's getter of the current device without the checks of
 # torch.cuda.current_device() (the tensors at hand are on the GPU already).
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_TYPE = {torch.float16: HG_F16, torch.bfloat16: HG_BF16, torch.float32: HG_F32}
-_HALF = (torch.float16, torch.bfloat16)
-_CODES = (torch.uint8, torch.float8_e4m3fn)
+_HALF = {torch.float16: HG_F16, torch.bfloat16: HG_BF16}
+_ONLY = {torch.float16: {torch.float16: HG_F16}, torch.bfloat16: {torch.bfloat16: HG_BF16},
+         torch.float32: {torch.float32: HG_F32}}
+_WIDE = {t: {t: c, torch.float32: HG_F32} for t, c in _HALF.items()}       # a type or float32
+_CODES = {torch.uint8: HG_E4M3, torch.float8_e4m3fn: HG_E4M3}
+_BYTES = {torch.uint8: HG_E4M3}
 
 
-def _lead(t, name, dtypes):
-    """The leading dimension of a valid matrix; raises for anything else."""
+def _lead(t, name, types, dev):
+    """The leading dimension of a valid matrix on device `dev` (None: on any);
+    raises for anything else."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dtype not in types:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(types)}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError("all tensors must be on one device")
     (rows, cols), (ld, unit) = t.shape, t.stride()
     if rows and cols > 1 and unit != 1:
         raise ValueError(f"{name} needs unit stride along its last axis")
@@ -71,56 +77,64 @@ def _lead(t, name, dtypes):
     return ld if rows > 1 and cols else max(1, cols)
 
 
-def _matrix(t, name, dtypes):
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == 2:
-        ld, unit = t.stride()                  # the ordinary case, without the checks that raise
-        if unit == 1 and ld >= t.shape[1] > 0:
-            return Matrix(t.data_ptr(), ld, None, 0, _TYPE[t.dtype])
-    ld = _lead(t, name, dtypes)
-    return Matrix(t.data_ptr() or None, ld, None, 0, _TYPE[t.dtype])
+def _matrix(t, name, types, dev):
+    try:                                 # an ordinary matrix, without the checks that name what is wrong
+        ld, unit = t.stride()
+        if unit == 1 and ld >= t.shape[1] > 0 and t.get_device() == dev:
+            return Matrix(t.data_ptr(), ld, None, 0, types[t.dtype])
+    except (AttributeError, KeyError, TypeError, ValueError):
+        pass
+    ld = _lead(t, name, types, dev)
+    return Matrix(t.data_ptr(), ld, None, 0, types[t.dtype])
 
 
-def _pair(pair, name):
+def _pair(pair, name, dev):
     if not (isinstance(pair, (tuple, list)) and len(pair) == 2):
         raise TypeError(f"{name} must be a tensor or a pair (codes, scales)")
     codes, scales = pair
-    ld, lds = _lead(codes, name + "'s codes", _CODES), _lead(scales, name + "'s scales", (torch.uint8,))
-    want = (codes.shape[0], -(-codes.shape[1] // E4M3_BLOCK))
-    if tuple(scales.shape) != want:
-        raise ValueError(f"{name}'s scales {tuple(scales.shape)} do not match codes {tuple(codes.shape)}: "
-                         f"expected {want}")
-    return Matrix(codes.data_ptr() or None, ld, scales.data_ptr() or None, lds, HG_E4M3)
+    c, s = _matrix(codes, name + "'s codes", _CODES, dev), _matrix(scales, name + "'s scales", _BYTES, dev)
+    (rows, cols), have = codes.shape, scales.shape
+    if have[0] != rows or have[1] != -(-cols // E4M3_BLOCK):
+        raise ValueError(f"{name}'s scales {tuple(have)} do not match codes {tuple(codes.shape)}: "
+                         f"expected {(rows, -(-cols // E4M3_BLOCK))}")
+    c.scales, c.lds = s.data, s.ld
+    return c
 
 
-def _saved(m, name, dtype):
-    """(matrix, shape, its tensors) of a 16-bit tensor or an 8-bit checkpoint."""
+def _saved(m, name, dtype, dev):
+    """(matrix, shape) of a 16-bit tensor or an 8-bit checkpoint."""
     if isinstance(m, torch.Tensor):
-        return _matrix(m, name, (dtype,)), m.shape, (m,)
-    d = _pair(m, name)
-    return d, m[0].shape, tuple(m)
+        return _matrix(m, name, _ONLY[dtype], dev), m.shape
+    d = _pair(m, name, dev)
+    return d, m[0].shape
 
 
-def _vector(v, name, n):
-    if not (isinstance(v, torch.Tensor) and v.is_cuda and v.dtype == torch.float32 and v.dim() == 1
-            and v.shape[0] == n and v.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous float32 device vector of length {n}")
-    return v.data_ptr() or None
+def _device(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t.get_device() if t.is_cuda else None
 
 
-def _work(work, need, like):
-    if work is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
-    if not (isinstance(work, torch.Tensor) and work.is_cuda and work.is_contiguous()):
-        raise ValueError("work must be a contiguous device tensor")
-    return work
+def _vector(v, name, n, dev):
+    if not (isinstance(v, torch.Tensor) and v.dtype == torch.float32 and v.dim() == 1 and v.shape[0] == n
+            and v.is_contiguous() and v.get_device() == dev):
+        raise ValueError(f"{name} must be a contiguous float32 vector of length {n} on the same device")
+    return v.data_ptr()
 
 
-def _call(fn, name, like, others, *args):
+def _room(work, dev):
+    """(address, bytes) of a caller's workspace."""
+    if not (isinstance(work, torch.Tensor) and work.is_contiguous() and work.get_device() == dev):
+        raise ValueError("work must be a contiguous tensor on the same device")
+    return work.data_ptr(), work.numel() * work.element_size()
+
+
+def _new_room(need, like):
+    return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
+
+
+def _call(fn, name, like, *args):
     """fn(*args, the current stream of `like`'s device), with that device current."""
-    dev = like.get_device()
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("all tensors must be on one device")
     st = _on_device(like, fn, *args, _stream_handle(like))
     if st != 0:
         raise HgError(name, st)
@@ -144,23 +158,25 @@ def _size(fn, name, like, *args):
 _NO_WORK = -11              # hg_linear: a workspace is needed and there is none
 
 
-def _linear_shapes(X, W):
-    x, w = _matrix(X, "X", _HALF), _matrix(W, "W", (X.dtype,))
-    (M, K), N = X.shape, W.shape[0]
-    if W.shape[1] != K:
+def _linear_operands(X, W):
+    dev = _device(X, "X")
+    x = _matrix(X, "X", _HALF, dev)
+    w = _matrix(W, "W", _ONLY[X.dtype], dev)
+    (M, K), (N, k) = X.shape, W.shape
+    if k != K:
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}")
-    return x, w, M, N, K
+    return x, w, M, N, K, dev
 
 
 def linear_workspace_size(X, W) -> int:
     """Bytes of workspace linear needs for these operands (hg_linear_workspace_size)."""
-    x, w, M, N, K = _linear_shapes(X, W)
+    x, w, M, N, K, _ = _linear_operands(X, W)
     return _size(lib.hg_linear_workspace_size, "hg_linear_workspace_size", X, M, N, K, x, w)
 
 
 def linear_workspace(X, W):
     """A workspace for linear calls on these operands (None if they need none)."""
-    return _work(None, linear_workspace_size(X, W), X)
+    return _new_room(linear_workspace_size(X, W), X)
 
 
 def linear(X, W, Y, bias=None, act: int = 0, residual=None, Z=None, work=None):
@@ -172,67 +188,65 @@ def linear(X, W, Y, bias=None, act: int = 0, residual=None, Z=None, work=None):
     (M, N) tensor of X's type or an 8-bit checkpoint (codes, scales).  `work`:
     device tensor of at least linear_workspace_size(X, W) bytes (allocated with
     torch when None and needed)."""
-    x, w, M, N, K = _linear_shapes(X, W)
-    y = _matrix(Y, "Y", (X.dtype, torch.float32))
-    if tuple(Y.shape) != (M, N):
-        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}, Y {tuple(Y.shape)}")
-    r = z = b = None
-    zt = ()
+    x, w, M, N, K, dev = _linear_operands(X, W)
+    y = _matrix(Y, "Y", _WIDE[X.dtype], dev)
+    shape = Y.shape
+    if shape[0] != M or shape[1] != N:
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}, Y {tuple(shape)}")
+    r = z = b = wptr = None
+    wbytes = 0
     if bias is not None:
-        b = _vector(bias, "bias", N)
+        b = _vector(bias, "bias", N, dev)
     if residual is not None:
-        r = _matrix(residual, "residual", (Y.dtype,))
-        if residual.shape != Y.shape:
-            raise ValueError(f"residual {tuple(residual.shape)} does not match Y {tuple(Y.shape)}")
+        r = _matrix(residual, "residual", _ONLY[Y.dtype], dev)
+        if residual.shape != shape:
+            raise ValueError(f"residual {tuple(residual.shape)} does not match Y {tuple(shape)}")
     if Z is not None:
-        z, shape, zt = _saved(Z, "Z", X.dtype)
-        if tuple(shape) != (M, N):
-            raise ValueError(f"Z {tuple(shape)} does not match Y {tuple(Y.shape)}")
-    wptr, wbytes = None, 0
+        z, zshape = _saved(Z, "Z", X.dtype, dev)
+        if zshape != shape:
+            raise ValueError(f"Z {tuple(zshape)} does not match Y {tuple(shape)}")
     if work is not None:
-        wptr, wbytes = _work(work, 0, X).data_ptr(), work.numel() * work.element_size()
+        wptr, wbytes = _room(work, dev)
     args = (int(act), M, N, K, x, w, b, r, y, z)
-    others = (W, Y, bias, residual, work) + zt
     try:
-        _call(lib.hg_linear, "hg_linear", X, others, *args, wptr, wbytes)
+        _call(lib.hg_linear, "hg_linear", X, *args, wptr, wbytes)
     except HgError as e:
         if work is not None or e.status != _NO_WORK:
             raise
         need = _size(lib.hg_linear_workspace_size, "hg_linear_workspace_size", X, M, N, K, x, w)
-        _call(lib.hg_linear, "hg_linear", X, others, *args, _work(None, need, X).data_ptr(), need)
+        _call(lib.hg_linear, "hg_linear", X, *args, _new_room(need, X).data_ptr(), need)
     return Y
 
 
-def _grad_shapes(dY, W, X):
-    dy = _matrix(dY, "dY", _HALF)
-    w = x = None
-    xt = ()
+def _grad_operands(dY, W, X):
+    dev = _device(dY, "dY")
+    dy = _matrix(dY, "dY", _HALF, dev)
+    w = x = K = None
     M, N = dY.shape
-    K = None
     if W is not None:
-        w = _matrix(W, "W", (dY.dtype,))
-        K = W.shape[1]
-        if W.shape[0] != N:
+        w = _matrix(W, "W", _ONLY[dY.dtype], dev)
+        n, K = W.shape
+        if n != N:
             raise ValueError(f"shape mismatch: dY {tuple(dY.shape)}, W {tuple(W.shape)}")
     if X is not None:
-        x, shape, xt = _saved(X, "X", dY.dtype)
+        x, shape = _saved(X, "X", dY.dtype, dev)
         if shape[0] != M or K not in (None, shape[1]):
             raise ValueError(f"shape mismatch: dY {tuple(dY.shape)}, X {tuple(shape)}"
                              + (f", W {tuple(W.shape)}" if W is not None else ""))
         K = shape[1]
-    return dy, w, x, xt, M, N, K or 0
+    return dy, w, x, M, N, K or 0, dev
 
 
 def linear_grad_workspace_size(dY, W, X) -> int:
     """Bytes of workspace linear_grad needs for these operands
     (hg_linear_grad_workspace_size); W or X None: without dX or dW."""
-    dy, w, x, _, M, N, K = _grad_shapes(dY, W, X)
+    dy, w, x, M, N, K, _ = _grad_operands(dY, W, X)
     return _size(lib.hg_linear_grad_workspace_size, "hg_linear_grad_workspace_size", dY, M, N, K, dy, w, x)
 
 
 def linear_grad_workspace(dY, W, X):
     """A workspace for linear_grad calls on these operands."""
-    return _work(None, linear_grad_workspace_size(dY, W, X), dY)
+    return _new_room(linear_grad_workspace_size(dY, W, X), dY)
 
 
 def linear_grad(dY, W, X, Z=None, act: int = 0, dX=None, dW=None, dbias=None, accumulate: bool = False, work=None):
@@ -246,37 +260,36 @@ def linear_grad(dY, W, X, Z=None, act: int = 0, dX=None, dW=None, dbias=None, ac
     dW, Z with ACT_NONE.  `accumulate`: dW and dbias are added to.  `work`:
     device tensor of at least linear_grad_workspace_size(dY, W, X) bytes
     (allocated with torch when None)."""
-    dy, w, x, xt, M, N, K = _grad_shapes(dY, W, X)
-    z = gx = gw = gb = None
-    zt = ()
+    dy, w, x, M, N, K, dev = _grad_operands(dY, W, X)
+    z = gx = gw = gb = wptr = None
+    wbytes = 0
     if dX is not None:
         if W is None:
             raise ValueError("dX needs W")
-        gx = _matrix(dX, "dX", (dY.dtype,))
-        if tuple(dX.shape) != (M, K):
+        gx = _matrix(dX, "dX", _ONLY[dY.dtype], dev)
+        if dX.shape[0] != M or dX.shape[1] != K:
             raise ValueError(f"dX {tuple(dX.shape)} does not match {(M, K)}")
     if dW is not None:
         if X is None:
             raise ValueError("dW needs X")
-        gw = _matrix(dW, "dW", (dY.dtype, torch.float32))
-        if tuple(dW.shape) != (N, K):
+        gw = _matrix(dW, "dW", _WIDE[dY.dtype], dev)
+        if dW.shape[0] != N or dW.shape[1] != K:
             raise ValueError(f"dW {tuple(dW.shape)} does not match {(N, K)}")
     if dbias is not None:
-        gb = _vector(dbias, "dbias", N)
+        gb = _vector(dbias, "dbias", N, dev)
     if Z is not None:
-        z, shape, zt = _saved(Z, "Z", dY.dtype)
-        if tuple(shape) != (M, N):
+        z, shape = _saved(Z, "Z", dY.dtype, dev)
+        if shape != dY.shape:
             raise ValueError(f"Z {tuple(shape)} does not match dY {tuple(dY.shape)}")
     elif act != 0:
         raise ValueError("the activation's gradient needs Z")
     if work is None:
-        work = _work(None, _size(lib.hg_linear_grad_workspace_size, "hg_linear_grad_workspace_size", dY, M, N, K, dy,
-                                 w, x), dY)
-    else:
-        work = _work(work, 0, dY)
-    wptr, wbytes = (work.data_ptr(), work.numel() * work.element_size()) if work is not None else (None, 0)
-    _call(lib.hg_linear_grad, "hg_linear_grad", dY, (W, dX, dW, dbias, work) + xt + zt,
-          int(act), M, N, K, dy, w, x, z, gx, gw, gb, 1 if accumulate else 0, wptr, wbytes)
+        work = _new_room(_size(lib.hg_linear_grad_workspace_size, "hg_linear_grad_workspace_size", dY, M, N, K, dy, w,
+                               x), dY)
+    if work is not None:
+        wptr, wbytes = _room(work, dev)
+    _call(lib.hg_linear_grad, "hg_linear_grad", dY, int(act), M, N, K, dy, w, x, z, gx, gw, gb,
+          1 if accumulate else 0, wptr, wbytes)
     return dX, dW, dbias
 
 
@@ -286,19 +299,23 @@ def checkpoint8_empty(M: int, N: int, device="cuda"):
             torch.empty((M, -(-N // E4M3_BLOCK)), dtype=torch.uint8, device=device))
 
 
-def checkpoint8_write(X, codes, scales):
-    """X (float16 or bfloat16) as an 8-bit checkpoint; returns (codes, scales)."""
-    x, c = _matrix(X, "X", _HALF), _pair((codes, scales), "the checkpoint")
+def _checkpoint(X, codes, scales):
+    dev = _device(X, "X")
+    x, c = _matrix(X, "X", _HALF, dev), _pair((codes, scales), "the checkpoint", dev)
     if codes.shape != X.shape:
         raise ValueError(f"codes {tuple(codes.shape)} do not match X {tuple(X.shape)}")
-    _call(lib.hg_checkpoint8_write, "hg_checkpoint8_write", X, (codes, scales), *X.shape, x, c)
+    return x, c, X.shape[0], X.shape[1]
+
+
+def checkpoint8_write(X, codes, scales):
+    """X (float16 or bfloat16) as an 8-bit checkpoint; returns (codes, scales)."""
+    x, c, M, N = _checkpoint(X, codes, scales)
+    _call(lib.hg_checkpoint8_write, "hg_checkpoint8_write", X, M, N, x, c)
     return codes, scales
 
 
 def checkpoint8_read(codes, scales, X):
     """The values of an 8-bit checkpoint, written to X (float16 or bfloat16); returns X."""
-    x, c = _matrix(X, "X", _HALF), _pair((codes, scales), "the checkpoint")
-    if codes.shape != X.shape:
-        raise ValueError(f"codes {tuple(codes.shape)} do not match X {tuple(X.shape)}")
-    _call(lib.hg_checkpoint8_read, "hg_checkpoint8_read", X, (codes, scales), *X.shape, c, x)
+    x, c, M, N = _checkpoint(X, codes, scales)
+    _call(lib.hg_checkpoint8_read, "hg_checkpoint8_read", X, M, N, c, x)
     return X
