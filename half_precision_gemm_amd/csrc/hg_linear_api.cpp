@@ -101,10 +101,10 @@ struct Cut {
     int splits, per;
 };
 
-// The expected time of a product, in us, from what its kernels measured on a
-// 256-CU MI355X (graph replays, bf16; both operands in the last-level cache).
-// A work item (a tile's slice of the sum) takes `fix` + `stage` per 64 of the
-// sum, as many at once as the GPU has room for:
+// The expected time of one or two products that share a launch, in us, from
+// what the kernels measured on a 256-CU MI355X (graph replays, bf16, operands
+// in the last-level cache).  A work item (a tile's slice of the sum) takes
+// `fix` + `stage` per 64 of the sum, as many at once as the GPU has room for:
 //
 //    edge   alone on its CUs          GPU full                  items per CU
 //     64    1.0 + 0.265 / stage       3.2 + 0.45 / stage        2
@@ -117,57 +117,91 @@ struct Cut {
 // 128×1024×8192 one slice 33.9, eight 13.8; 2048×4096×4096 128×128 80.3,
 // 256×256 in two slices 72.9; 2000×6000×4000 128×128 125, 256×256 91.8;
 // 512×4096×4096 64×64 28.3, 128×128 in two slices 30.7.
-double cost_us(int64_t M, int64_t N, int64_t K, int tile, int64_t s)
+struct Shape {
+    int64_t M, N, K;
+    int64_t stages() const { return (K + kBK - 1) / kBK; }
+};
+double expected_us(int64_t cus, int tile, const Shape &a, int sa, const Shape *b = nullptr, int sb = 1)
 {
-    const int64_t cus = hg::cu_count(), stages = (K + kBK - 1) / kBK;
-    const int64_t items = ((M + tile - 1) / tile) * ((N + tile - 1) / tile) * s;
+    auto tiles = [&](const Shape &p) { return ((p.M + tile - 1) / tile) * ((p.N + tile - 1) / tile); };
+    const int64_t na = tiles(a) * sa, nb = b != nullptr ? tiles(*b) * sb : 0, items = na + nb;
     const double fill = std::min(1.0, (double)items / (double)cus);
-    const int64_t slots = tile == 64 && items > cus ? 2 * cus : cus;
-    const double fix = tile == 64 ? (items > cus ? 3.2 : 1.0) : tile == 128 ? 5.0 : 7.0 + 6.0 * fill;
-    const double stage = tile == 64 ? (items > cus ? 0.45 : 0.265) : tile == 128 ? 0.55 : 1.05 + 0.35 * fill;
+    const bool shared = tile == 64 && items > cus;
+    const int64_t slots = shared ? 2 * cus : cus;
+    const double fix = tile == 64 ? (shared ? 3.2 : 1.0) : tile == 128 ? 5.0 : 7.0 + 6.0 * fill;
+    const double stage = tile == 64 ? (shared ? 0.45 : 0.265) : tile == 128 ? 0.55 : 1.05 + 0.35 * fill;
+    const double ta = fix + stage * (double)((a.stages() + sa - 1) / sa);
+    const double tb = b != nullptr ? fix + stage * (double)((b->stages() + sb - 1) / sb) : 0.0;
     const double rounds = (double)((items + slots - 1) / slots);
-    const double reduce = s > 1 ? 3.0 + (double)s * (double)M * (double)N * 8.0 / 5e6 : 0.0;
-    return 2.0 + rounds * (fix + stage * (double)((stages + s - 1) / s)) + reduce;
+    const double mean = items > 0 ? ((double)na * ta + (double)nb * tb) / (double)items : 0.0;
+    double us = 2.0 + std::max(rounds * mean, std::max(ta, tb));
+    if (sa > 1 || sb > 1)
+        us += 3.0 + ((sa > 1 ? (double)sa * (double)a.M * (double)a.N : 0.0) +
+                     (b != nullptr && sb > 1 ? (double)sb * (double)b->M * (double)b->N : 0.0)) * 8.0 / 5e6;
+    return us;
 }
-// The best number of slices (at least four stages each) on this tile.
-Cut cut_as(int64_t M, int64_t N, int64_t K, int tile, double *us = nullptr)
+Cut slices(int tile, const Shape &p, int s)
 {
-    static const int counts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
-    const int64_t stages = (K + kBK - 1) / kBK;
-    int best = 1;
-    double least = cost_us(M, N, K, tile, 1);
-    for (int s : counts) {
-        if (s == 1 || stages < 4 * s)
-            continue;
-        const double c = cost_us(M, N, K, tile, s);
-        if (c < least) {
-            least = c;
-            best = s;
-        }
-    }
-    if (us != nullptr)
-        *us = least;
     Cut c;
     c.tile = tile;
-    c.per = (int)((stages + best - 1) / best);
-    c.splits = c.per > 0 ? (int)((stages + c.per - 1) / c.per) : 1;
+    c.per = (int)((p.stages() + s - 1) / s);
+    c.splits = c.per > 0 ? (int)((p.stages() + c.per - 1) / c.per) : 1;
     return c;
 }
-Cut cut_of(int64_t M, int64_t N, int64_t K, double *us = nullptr)
+// Numbers of slices that are tried, as long as a slice has at least four stages
+// and the work items are no more than the GPU holds twice.
+constexpr int kSlices[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+bool may_slice(int64_t cus, int tile, const Shape &p, int s)
 {
-    Cut best{};
+    return s == 1 || (p.stages() >= 4 * s &&
+                      ((p.M + tile - 1) / tile) * ((p.N + tile - 1) / tile) * s <= 2 * cus);
+}
+
+Cut best_cut(const Shape &p, double *us = nullptr)
+{
+    const int64_t cus = hg::cu_count();
+    Cut best{64, 1, 0};
     double least = 0.0;
-    for (int tile : {64, 128, 256}) {
-        double c;
-        const Cut cut = cut_as(M, N, K, tile, &c);
-        if (tile == 64 || c < least) {
-            least = c;
-            best = cut;
+    bool first = true;
+    for (int tile : {64, 128, 256})
+        for (int s : kSlices) {
+            if (!may_slice(cus, tile, p, s))
+                break;
+            const double c = expected_us(cus, tile, p, s);
+            if (first || c < least) {
+                least = c;
+                best = slices(tile, p, s);
+                first = false;
+            }
         }
-    }
     if (us != nullptr)
         *us = least;
     return best;
+}
+// Two products: each on its own if either is best on 256×256 tiles, else
+// together on one smaller edge.
+void best_cuts(const Shape &a, const Shape &b, Cut &ca, Cut &cb)
+{
+    const int64_t cus = hg::cu_count();
+    double ua, ub;
+    ca = best_cut(a, &ua);
+    cb = best_cut(b, &ub);
+    double least = ca.tile == 256 || cb.tile == 256 ? ua + ub : -1.0;
+    for (int tile : {64, 128})
+        for (int sa : kSlices) {
+            if (!may_slice(cus, tile, a, sa))
+                break;
+            for (int sb : kSlices) {
+                if (!may_slice(cus, tile, b, sb))
+                    break;
+                const double c = expected_us(cus, tile, a, sa, &b, sb);
+                if (least < 0.0 || c < least) {
+                    least = c;
+                    ca = slices(tile, a, sa);
+                    cb = slices(tile, b, sb);
+                }
+            }
+        }
 }
 int64_t partial_bytes(const Cut &c, int64_t M, int64_t N)
 {
@@ -238,7 +272,7 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
     double us;
     q.copy_x = !direct(X, K);
     q.copy_w = !direct(W, K);
-    q.cut = cut_of(M, N, K, &us);
+    q.cut = best_cut({M, N, K}, &us);
     if (row_by_row(M, N, K, q.copy_x, q.copy_w, us)) {
         q.copy_x = q.copy_w = false;
         q.cut = {0, 1, 0};
@@ -282,18 +316,14 @@ struct GradRoom {
 GradRoom room_grad(Arena &a, int64_t M, int64_t N, int64_t K, const hg_matrix *W, const hg_matrix *X)
 {
     GradRoom r;
-    // Products on smaller tiles than 256×256 share a launch, and so an edge.
-    const Cut none{64, 1, 0};
-    double x64 = 0, x128 = 0, w64 = 0, w128 = 0;
-    r.cx = W != nullptr ? cut_of(M, K, N) : none;
-    r.cw = X != nullptr ? cut_of(N, K, M) : none;
-    if (W != nullptr && X != nullptr && r.cx.tile != 256 && r.cw.tile != 256 && r.cx.tile != r.cw.tile) {
-        const Cut cx64 = cut_as(M, K, N, 64, &x64), cx128 = cut_as(M, K, N, 128, &x128);
-        const Cut cw64 = cut_as(N, K, M, 64, &w64), cw128 = cut_as(N, K, M, 128, &w128);
-        const bool small = x64 + w64 < x128 + w128;
-        r.cx = small ? cx64 : cx128;
-        r.cw = small ? cw64 : cw128;
-    }
+    r.cx = r.cw = {64, 1, 0};
+    const Shape x{M, K, N}, w{N, K, M};
+    if (W != nullptr && X != nullptr)
+        best_cuts(x, w, r.cx, r.cw);
+    else if (W != nullptr)
+        r.cx = best_cut(x);
+    else if (X != nullptr)
+        r.cw = best_cut(w);
     r.copy_w = W != nullptr && !direct(W, K);
     r.copy_x = X != nullptr && (X->type == HG_E4M3 || !direct(X, K));
     const int64_t strips = M > 0 ? (M + strip_of(M, N) - 1) / strip_of(M, N) : 0;
