@@ -117,6 +117,19 @@ def test_only_what_is_wanted(hg, want):
     case(hg, 201, 131, 97, BF16, "gelu_tanh", want=want)
 
 
+@pytest.mark.parametrize("M,N,K", [(128, 1024, 2048), (1024, 512, 256), (300, 130, 2000), (64, 4096, 128)])
+def test_one_workspace_for_any_gradients(hg, M, N, K):
+    """The size for both operands is enough whichever gradients are wanted."""
+    dY, W, X, Z = (torch.randn(s, device=DEV).to(F16) for s in ((M, N), (N, K), (M, K), (M, N)))
+    work = hg.linear_grad_workspace(dY, W, X)
+    kw = dict(Z=Z, act=hg.ACT_SILU, work=work)
+    for one in (dict(dX=torch.empty_like(X)), dict(dW=torch.empty_like(W)), dict(dbias=torch.empty(N, device=DEV)),
+                dict(dX=torch.empty_like(X), dW=torch.empty_like(W))):
+        hg.linear_grad(dY, W, X, **one, **kw)
+        for key, out in one.items():
+            ref.check(out, *ref.grads(dY.cpu(), W.cpu(), X.cpu(), Z.cpu(), "silu")[key], key)
+
+
 @pytest.mark.parametrize("pad,shift", [(0, 1), (0, 8), (1, 0), (8, 0), (64, 4), (5, 3)])
 def test_strides_and_alignment(hg, pad, shift):
     case(hg, 75, 136, 200, F16, "silu", pad=pad, shift=shift)
