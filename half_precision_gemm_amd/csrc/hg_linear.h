@@ -48,9 +48,12 @@ struct Product {
     const uint16_t *A, *B;        // 16-byte aligned, lda and ldb multiples of 8 (not so row-wise)
     int64_t lda, ldb;
     int32_t M, N, K;              // rows, cols, length of the sum
-    int32_t splits, per;          // slices of the sum and their length in 64-wide stages
-    float *P;                     // splits > 1: fp32 partial sums, slice s at P + s·M·ldp
-    int64_t ldp;                  // multiple of 4
+    // The first `whole` tiles (edge×edge, in the order of tile_at) are computed
+    // in one piece, the others in `splits` slices of `per` 64-wide stages, each
+    // of which stores its fp32 partial sums as a tile of its own: slice s of the
+    // t-th such tile at P + (t·splits + s)·edge².
+    int32_t edge, whole, splits, per;
+    float *P;
     Finish f;
 };
 
@@ -300,22 +303,57 @@ struct Panel {
     }
 };
 
-// Workgroup or work item → (slice, tile row, tile column): ids regrouped per
-// XCD (consecutive ids run on different XCDs, each with its own L2), then
-// bands of 4 tile rows walked column by column, so that tiles on one XCD share
-// panels in its L2.
-__device__ __forceinline__ void place(int id, int total, int tiles_m, int tiles_n, int &slice, int &tm, int &tn)
+// How a product is spread over work items.
+struct Spread {
+    int tiles_m, tiles_n, items;
+};
+// Tiles in order: bands of 4 tile rows walked column by column.
+__device__ __forceinline__ void tile_at(int l, const Spread &w, int &tm, int &tn)
 {
-    const int per = total >> 3, rem = total & 7, x = id & 7;
-    const int q = x * per + min(x, rem) + (id >> 3);
-    const int tiles = tiles_m * tiles_n;
-    slice = q / tiles;
-    const int l = q - slice * tiles;
-    const int band = l / (4 * tiles_n), first = band * 4;
-    const int gsz = min(tiles_m - first, 4);
-    const int r = l - band * 4 * tiles_n;
+    const int band = l / (4 * w.tiles_n), first = band * 4;
+    const int gsz = min(w.tiles_m - first, 4);
+    const int r = l - band * 4 * w.tiles_n;
     tm = first + r % gsz;
     tn = r / gsz;
+}
+// Consecutive ids run on different XCDs, each with its own L2: the ids of one
+// XCD take consecutive places, so that its tiles share panels.
+__device__ __forceinline__ int per_xcd(int id, int total)
+{
+    const int per = total >> 3, rem = total & 7, x = id & 7;
+    return x * per + min(x, rem) + (id >> 3);
+}
+// One work item: the tile at (m0, n0), stages kt0 .. of its sum; a slice's
+// partial sums go to `part` (null: the whole sum).
+struct Item {
+    int m0, n0, kt0, nk;
+    float *part;
+};
+template <int EDGE>
+__device__ __forceinline__ Item item_at(const Product &p, const Spread &w, int id)
+{
+    Item t;
+    int l, slice = 0;
+    t.part = nullptr;
+    if (id < p.whole) {
+        l = per_xcd(id, p.whole);
+        t.kt0 = 0;
+        t.nk = (p.K + kStage - 1) / kStage;
+    } else {
+        const int rest = w.tiles_m * w.tiles_n - p.whole;
+        const int q = per_xcd(id - p.whole, rest * p.splits);
+        slice = q / rest;
+        l = q - slice * rest;
+        t.part = p.P + ((int64_t)l * p.splits + slice) * (EDGE * EDGE);
+        l += p.whole;
+        t.kt0 = slice * p.per;
+        t.nk = min((p.K + kStage - 1) / kStage - t.kt0, p.per);
+    }
+    int tm, tn;
+    tile_at(l, w, tm, tn);
+    t.m0 = tm * EDGE;
+    t.n0 = tn * EDGE;
+    return t;
 }
 
 template <bool BF16>
@@ -701,9 +739,9 @@ __device__ __forceinline__ void stage_get(const unsigned char *s, int row, int u
     }
 }
 
-// Finishes (or, with partial sums, stores as fp32) staged 16×W blocks of one
-// wave, one after the other down the tile: `slice` of the sum, columns c0 ..,
-// rows `row0` .. in steps of 16.
+// Finishes (or, of a slice of the sum, stores as fp32) staged 16×W blocks of one
+// wave, one after the other down the item's tile: columns c0 .., rows `row0` ..
+// in steps of 16.
 //
 // A block inside the matrix takes its passes together: the
 // reads from LDS, the activation's chains and the stores of PASSES rows per
@@ -711,18 +749,19 @@ __device__ __forceinline__ void stage_get(const unsigned char *s, int row, int u
 // decided once per block, not per row.  The residual of the next block is
 // requested before this block's stores, because the counter of vector memory
 // operations retires in order: a load issued after them would wait for them.
-template <int W, bool BF16>
+template <int EDGE, int W, bool BF16>
 struct Drain {
     static constexpr int UNITS = W / 8, ROWS = 64 / UNITS;      // lanes per row, rows per pass
     static constexpr int PASSES = 16 / ROWS;
     const Product &p;
     const unsigned char *stg;
-    int lane, slice, c0;
+    int lane, c0, m0, n0;
+    float *part;
     float bias[8];
     u32x4 ahead[PASSES][2];                                     // residual of the next block
 
-    __device__ __forceinline__ Drain(const Product &p_, const unsigned char *stg_, int lane_, int slice_, int c0_)
-        : p(p_), stg(stg_), lane(lane_), slice(slice_), c0(c0_)
+    __device__ __forceinline__ Drain(const Product &p_, const Item &t, const unsigned char *stg_, int lane_, int c0_)
+        : p(p_), stg(stg_), lane(lane_), c0(c0_), m0(t.m0), n0(t.n0), part(t.part)
     {
         load_bias(p.f, c0 + 8 * (lane % UNITS), bias);
     }
@@ -734,7 +773,7 @@ struct Drain {
     __device__ __forceinline__ void request(int row0)
     {
         const Finish &f = p.f;
-        if (!f.R || p.splits > 1 || !inside(row0))
+        if (!f.R || part || !inside(row0))
             return;
         const int64_t at = (int64_t)(row0 + lane / UNITS) * f.ldr + c0 + 8 * (lane % UNITS);
         const char *r = static_cast<const char *>(f.R) + at * (f.out32 ? 4 : 2);
@@ -762,10 +801,10 @@ struct Drain {
         for (int t = 0; t < PASSES; ++t)
             stage_get<W>(stg, r0 + ROWS * t, unit, v[t]);
         const int64_t row = row0 + r0;
-        if (p.splits > 1) {
-            float *d = p.P + ((int64_t)slice * p.M + row) * p.ldp + col;
+        if (part) {
+            float *d = part + (row0 + r0 - m0) * EDGE + col - n0;
 #pragma unroll
-            for (int t = 0; t < PASSES; ++t, d += ROWS * p.ldp) {
+            for (int t = 0; t < PASSES; ++t, d += ROWS * EDGE) {
                 *reinterpret_cast<floatx4 *>(d) = floatx4{v[t][0], v[t][1], v[t][2], v[t][3]};
                 *reinterpret_cast<floatx4 *>(d + 4) = floatx4{v[t][4], v[t][5], v[t][6], v[t][7]};
             }
@@ -834,12 +873,11 @@ struct Drain {
             float v[8];
             stage_get<W>(stg, r, unit, v);
             const int row = row0 + r;
-            if (p.splits > 1) {
+            if (part) {
                 if (row < p.M && col < p.N) {
-                    float *d = p.P + ((int64_t)slice * p.M + row) * p.ldp + col;
+                    float *d = part + (row - m0) * EDGE + col - n0;
                     *reinterpret_cast<floatx4 *>(d) = floatx4{v[0], v[1], v[2], v[3]};
-                    if (col + 4 < p.ldp)
-                        *reinterpret_cast<floatx4 *>(d + 4) = floatx4{v[4], v[5], v[6], v[7]};
+                    *reinterpret_cast<floatx4 *>(d + 4) = floatx4{v[4], v[5], v[6], v[7]};
                 }
             } else {
                 finish8<BF16>(p.f, row, col, v, bias);

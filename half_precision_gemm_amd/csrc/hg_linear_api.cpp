@@ -94,17 +94,23 @@ struct Arena {
     }
 };
 
-// How a product is cut: the tile edge (0: the row-wise product) and the
-// slices of its sum.
+// How a product is cut: the tile edge (0: the row-wise product), the tiles that
+// are computed in one piece, and the slices of the others' sums.
 struct Cut {
     int tile;
+    int64_t whole;
     int splits, per;
 };
+struct Shape {
+    int64_t M, N, K;
+    int64_t stages() const { return (K + kBK - 1) / kBK; }
+    int64_t tiles(int edge) const { return ((M + edge - 1) / edge) * ((N + edge - 1) / edge); }
+};
 
-// The expected time of one or two products that share a launch, in us, from
-// what the kernels measured on a 256-CU MI355X (graph replays, bf16, operands
-// in the last-level cache).  A work item (a tile's slice of the sum) takes
-// `fix` + `stage` per 64 of the sum, as many at once as the GPU has room for:
+// What the kernels measured on a 256-CU MI355X (graph replays, bf16, operands in
+// the last-level cache), in us.  A work item (a tile, or a slice of its sum)
+// takes `fix` + `stage` per 64 of the sum, as many at once as the GPU has room
+// for:
 //
 //    edge   alone on its CUs          GPU full                  items per CU
 //     64    1.0 + 0.265 / stage       3.2 + 0.45 / stage        2
@@ -117,67 +123,90 @@ struct Cut {
 // 128×1024×8192 one slice 33.9, eight 13.8; 2048×4096×4096 128×128 80.3,
 // 256×256 in two slices 72.9; 2000×6000×4000 128×128 125, 256×256 91.8;
 // 512×4096×4096 64×64 28.3, 128×128 in two slices 30.7.
-struct Shape {
-    int64_t M, N, K;
-    int64_t stages() const { return (K + kBK - 1) / kBK; }
+struct Rate {
+    double fix, stage;
+    int64_t slots;
 };
-double expected_us(int64_t cus, int tile, const Shape &a, int sa, const Shape *b = nullptr, int sb = 1)
+Rate rate_of(int64_t cus, int tile, int64_t items)
 {
-    auto tiles = [&](const Shape &p) { return ((p.M + tile - 1) / tile) * ((p.N + tile - 1) / tile); };
-    const int64_t na = tiles(a) * sa, nb = b != nullptr ? tiles(*b) * sb : 0, items = na + nb;
     const double fill = std::min(1.0, (double)items / (double)cus);
-    const bool shared = tile == 64 && items > cus;
-    const int64_t slots = shared ? 2 * cus : cus;
-    const double fix = tile == 64 ? (shared ? 3.2 : 1.0) : tile == 128 ? 5.0 : 7.0 + 6.0 * fill;
-    const double stage = tile == 64 ? (shared ? 0.45 : 0.265) : tile == 128 ? 0.55 : 1.05 + 0.35 * fill;
-    const double ta = fix + stage * (double)((a.stages() + sa - 1) / sa);
-    const double tb = b != nullptr ? fix + stage * (double)((b->stages() + sb - 1) / sb) : 0.0;
-    // Equal items go in rounds; unequal ones fill up after each other.
-    const double work = (double)na * ta + (double)nb * tb, longest = std::max(ta, tb);
-    const bool equal = nb == 0 || (ta < 1.25 * tb && tb < 1.25 * ta);
-    const double rounds = (double)((items + slots - 1) / slots);
-    const double run = equal ? rounds * work / (double)std::max<int64_t>(items, 1)
-                             : work / (double)slots + 0.25 * std::min(ta, tb);
-    double us = 2.0 + std::max(run, longest);
-    if (sa > 1 || sb > 1)
-        us += 3.0 + ((sa > 1 ? (double)sa * (double)a.M * (double)a.N : 0.0) +
-                     (b != nullptr && sb > 1 ? (double)sb * (double)b->M * (double)b->N : 0.0)) * 8.0 / 5e6;
-    return us;
+    if (tile == 64)
+        return items > cus ? Rate{3.2, 0.45, 2 * cus} : Rate{1.0, 0.265, cus};
+    return tile == 128 ? Rate{5.0, 0.55, cus} : Rate{7.0 + 6.0 * fill, 1.05 + 0.35 * fill, cus};
 }
-Cut slices(int tile, const Shape &p, int s)
+double reduce_us(int64_t tiles, int tile, int s)
+{
+    return s > 1 && tiles > 0 ? 3.0 + (double)tiles * (double)s * (double)tile * (double)tile * 8.0 / 5e6 : 0.0;
+}
+// One product, its tiles from `whole` on in s slices.
+double expected_us(int64_t cus, int tile, const Shape &p, int64_t whole, int s)
+{
+    const int64_t tiles = p.tiles(tile), rest = tiles - whole;
+    const Rate r = rate_of(cus, tile, whole + rest * s);
+    const double one = r.fix + r.stage * (double)p.stages(), part = r.fix + r.stage * (double)((p.stages() + s - 1) / s);
+    return 2.0 + (double)((whole + r.slots - 1) / r.slots) * one + (double)((rest * s + r.slots - 1) / r.slots) * part +
+           reduce_us(rest, tile, s);
+}
+// Two products in one launch, their sums in sa and sb slices.
+double expected_us(int64_t cus, int tile, const Shape &a, int sa, const Shape &b, int sb)
+{
+    const int64_t na = a.tiles(tile) * sa, nb = b.tiles(tile) * sb, items = na + nb;
+    const Rate r = rate_of(cus, tile, items);
+    const double ta = r.fix + r.stage * (double)((a.stages() + sa - 1) / sa);
+    const double tb = r.fix + r.stage * (double)((b.stages() + sb - 1) / sb);
+    // Equal items go in rounds; unequal ones fill up after each other.
+    const double work = (double)na * ta + (double)nb * tb;
+    const double run = ta < 1.25 * tb && tb < 1.25 * ta
+                           ? (double)((items + r.slots - 1) / r.slots) * work / (double)std::max<int64_t>(items, 1)
+                           : work / (double)r.slots + 0.25 * std::min(ta, tb);
+    const double reduce = reduce_us(a.tiles(tile), tile, sa) + reduce_us(b.tiles(tile), tile, sb);
+    return 2.0 + std::max({run, ta, tb}) + (sa > 1 && sb > 1 ? reduce - 3.0 : reduce);
+}
+Cut cut_into(int tile, const Shape &p, int64_t whole, int s)
 {
     Cut c;
     c.tile = tile;
     c.per = (int)((p.stages() + s - 1) / s);
     c.splits = c.per > 0 ? (int)((p.stages() + c.per - 1) / c.per) : 1;
+    c.whole = c.splits > 1 ? whole : p.tiles(tile);
     return c;
 }
 // Numbers of slices that are tried, as long as a slice has at least four stages
-// and the work items are no more than the GPU holds twice.
+// and the cut tiles' items are no more than the GPU holds twice.
 constexpr int kSlices[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
-bool may_slice(int64_t cus, int tile, const Shape &p, int s)
+bool may_slice(int64_t cus, int64_t tiles, const Shape &p, int s)
 {
-    return s == 1 || (p.stages() >= 4 * s &&
-                      ((p.M + tile - 1) / tile) * ((p.N + tile - 1) / tile) * s <= 2 * cus);
+    return s == 1 || (p.stages() >= 4 * s && tiles * s <= 2 * cus);
 }
 
+// A product's tiles are cut all, none, or only those of the last round, which
+// would leave most of the GPU idle (1729×10332×14080, 287 tiles of 256×256 on 256
+// CUs: none 698 us).
 Cut best_cut(const Shape &p, double *us = nullptr)
 {
     const int64_t cus = hg::cu_count();
-    Cut best{64, 1, 0};
+    Cut best{64, 0, 1, 0};
     double least = 0.0;
     bool first = true;
-    for (int tile : {64, 128, 256})
-        for (int s : kSlices) {
-            if (!may_slice(cus, tile, p, s))
+    for (int tile : {64, 128, 256}) {
+        const int64_t tiles = p.tiles(tile), slots = tile == 64 ? 2 * cus : cus, full = tiles / slots * slots;
+        for (int64_t whole : {(int64_t)0, full}) {
+            if (whole > 0 && whole == tiles)
                 break;
-            const double c = expected_us(cus, tile, p, s);
-            if (first || c < least) {
-                least = c;
-                best = slices(tile, p, s);
-                first = false;
+            for (int s : kSlices) {
+                if (!may_slice(cus, tiles - whole, p, s))
+                    break;
+                const double c = expected_us(cus, tile, p, whole, s);
+                if (first || c < least) {
+                    least = c;
+                    best = cut_into(tile, p, whole, s);
+                    first = false;
+                }
             }
+            if (full == 0)
+                break;
         }
+    }
     if (us != nullptr)
         *us = least;
     return best;
@@ -195,30 +224,31 @@ void best_cuts(const Shape &a, const Shape &b, Cut &ca, Cut &cb)
     double least = ca.tile == 256 || cb.tile == 256 ? ua + ub : -1.0;
     for (int tile : {64, 128})
         for (int sa : kSlices) {
-            if (!may_slice(cus, tile, a, sa))
+            if (!may_slice(cus, a.tiles(tile), a, sa))
                 break;
             for (int sb : kSlices) {
-                if (!may_slice(cus, tile, b, sb))
+                if (!may_slice(cus, b.tiles(tile), b, sb))
                     break;
-                const double c = expected_us(cus, tile, a, sa, &b, sb);
+                const double c = expected_us(cus, tile, a, sa, b, sb);
                 if (least < 0.0 || c < least) {
                     least = c;
-                    ca = slices(tile, a, sa);
-                    cb = slices(tile, b, sb);
+                    ca = cut_into(tile, a, 0, sa);
+                    cb = cut_into(tile, b, 0, sb);
                 }
             }
         }
 }
-int64_t partial_bytes(const Cut &c, int64_t M, int64_t N)
+int64_t partial_bytes(const Cut &c, const Shape &p)
 {
-    return c.splits > 1 ? (int64_t)c.splits * M * ((N + 3) / 4 * 4) * 4 : 0;
+    return c.splits > 1 ? (p.tiles(c.tile) - c.whole) * c.splits * c.tile * c.tile * 4 : 0;
 }
 void set_cut(lin::Product &p, const Cut &c, void *partials)
 {
+    p.edge = c.tile;
+    p.whole = (int32_t)c.whole;
     p.splits = c.splits;
     p.per = c.per;
     p.P = static_cast<float *>(partials);
-    p.ldp = ((int64_t)p.N + 3) / 4 * 4;
 }
 
 void set_output(lin::Finish &f, const hg_matrix *Y, int64_t rows, int64_t cols)
@@ -281,7 +311,7 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
     q.cut = best_cut({M, N, K}, &us);
     if (row_by_row(M, N, K, q.copy_x, q.copy_w, us)) {
         q.copy_x = q.copy_w = false;
-        q.cut = {0, 1, 0};
+        q.cut = {0, 0, 1, 0};
     }
     return q;
 }
@@ -298,7 +328,7 @@ LinearRoom room_linear(Arena &a, const LinearPlan &q, int64_t M, int64_t N, int6
     LinearRoom r;
     r.x = a.take(q.copy_x ? M * up8(K) * 2 : 0);
     r.w = a.take(q.copy_w ? N * up8(K) * 2 : 0);
-    r.p = a.take(partial_bytes(q.cut, M, N));
+    r.p = a.take(q.cut.tile != 0 ? partial_bytes(q.cut, {M, N, K}) : 0);
     return r;
 }
 
@@ -322,7 +352,7 @@ struct GradRoom {
 GradRoom room_grad(Arena &a, int64_t M, int64_t N, int64_t K, const hg_matrix *W, const hg_matrix *X)
 {
     GradRoom r;
-    r.cx = r.cw = {64, 1, 0};
+    r.cx = r.cw = {64, 0, 1, 0};
     const Shape x{M, K, N}, w{N, K, M};
     if (W != nullptr && X != nullptr)
         best_cuts(x, w, r.cx, r.cw);
@@ -337,8 +367,8 @@ GradRoom room_grad(Arena &a, int64_t M, int64_t N, int64_t K, const hg_matrix *W
     r.x = a.take(r.copy_x ? M * up8(K) * 2 : 0);
     r.w = a.take(r.copy_w ? N * up8(K) * 2 : 0);
     r.q = a.take(strips > 1 ? strips * N * 4 : 0);
-    r.px = a.take(W != nullptr ? partial_bytes(r.cx, M, K) : 0);
-    r.pw = a.take(X != nullptr ? partial_bytes(r.cw, N, K) : 0);
+    r.px = a.take(W != nullptr ? partial_bytes(r.cx, x) : 0);
+    r.pw = a.take(X != nullptr ? partial_bytes(r.cw, w) : 0);
     return r;
 }
 
@@ -426,6 +456,7 @@ int hg_linear(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
         p.f.ldzs = Z->lds;
     }
     if (K == 0) {                                 // an empty sum
+        p.edge = 64;
         return status_of(lin::launch_reduce(&p, nullptr, bf16, s));
     }
     set_cut(p, q.cut, room.p);

@@ -36,11 +36,6 @@ constexpr int kSlots = EDGE == 64 ? 5 : 4;
 template <int EDGE>
 constexpr int kLds = kSlots<EDGE> * 2 * EDGE * kStage * 2;
 
-// How a product is spread over workgroups.
-struct Spread {
-    int tiles_m, tiles_n, total;      // total: tiles × slices
-};
-
 template <int EDGE, bool TA, bool TB, bool KCHK, bool BF16>
 __device__ __forceinline__ void ring_tile(const Product &p, const Spread &w, int id, unsigned char *smem)
 {
@@ -52,14 +47,11 @@ __device__ __forceinline__ void ring_tile(const Product &p, const Spread &w, int
     constexpr int LA = SA::L, L = SA::L + SB::L;
     static_assert(NS >= 4 && (NS - 2) * L <= 63 && NS * SLOT == kLds<EDGE> && kLds<EDGE> >= NWAVES * 16 * WT * 4, "");
 
-    int slice, tm, tn;
-    place(id, w.total, w.tiles_m, w.tiles_n, slice, tm, tn);
-    const int m0 = tm * EDGE, n0 = tn * EDGE, K = p.K;
+    const Item t = item_at<EDGE>(p, w, id);
+    const int m0 = t.m0, n0 = t.n0, kt0 = t.kt0, nk = t.nk, K = p.K;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    const int kt0 = slice * p.per;                                           // stages of this slice
-    const int nk = min((K + BK - 1) / BK - kt0, p.per);
     const uint32_t lds_base = (uint32_t)reinterpret_cast<uintptr_t>(smem);
 
     Panel<EDGE, TA, KCHK> pa;
@@ -156,7 +148,7 @@ __device__ __forceinline__ void ring_tile(const Product &p, const Spread &w, int
 
     unsigned char *stg = smem + wave * (16 * WT * 4);
     const int row0 = m0 + wm * WT;
-    Drain<WT, BF16> out(p, stg, lane, slice, n0 + wn * WT);
+    Drain<EDGE, WT, BF16> out(p, t, stg, lane, n0 + wn * WT);
     out.request(row0);
     settle(out.bias);
 #pragma unroll
@@ -209,18 +201,18 @@ linear_ring_pair_kernel(const Product x, const Product y, const Strips b, const 
 {
     __shared__ __attribute__((aligned(1024))) unsigned char smem[kLds<EDGE>];
     const int id = blockIdx.x;
-    if (id < wx.total)
+    if (id < wx.items)
         ring_tile<EDGE, false, true, KCHK, BF16>(x, wx, id, smem);
-    else if (id < wx.total + wy.total)
-        ring_tile<EDGE, true, true, false, BF16>(y, wy, id - wx.total, smem);
+    else if (id < wx.items + wy.items)
+        ring_tile<EDGE, true, true, false, BF16>(y, wy, id - wx.items, smem);
     else
-        sum_strips(b, id - wx.total - wy.total, smem);
+        sum_strips(b, id - wx.items - wy.items, smem);
 }
 
 Spread spread(const Product &p, int edge, int64_t &total)
 {
     const int64_t tm = ((int64_t)p.M + edge - 1) / edge, tn = ((int64_t)p.N + edge - 1) / edge;
-    total = tm * tn * p.splits;
+    total = p.whole + (tm * tn - p.whole) * p.splits;
     return {(int)tm, (int)tn, total > 0x7fffffff ? 0 : (int)total};
 }
 

@@ -193,22 +193,27 @@ __global__ void __launch_bounds__(THREADS) prepare_kernel(const Slope g, const C
         copy_rows<BF16>(w, b - slopes - xblocks, wblocks);
 }
 
-// One product's slices added in order, then what its epilogue does.
+// The slices of one product's cut tiles added in order, then what its epilogue
+// does (K = 0: no slices, every tile).
 template <bool BF16>
-__device__ __forceinline__ void reduce_rows(const Product &p, int block, int blocks)
+__device__ __forceinline__ void reduce_tiles(const Product &p, const Spread &w, int block, int blocks)
 {
-    const int64_t units = ((int64_t)p.N + kBlock8 - 1) / kBlock8 * 4, total = (int64_t)p.M * units;
+    const int edge = p.edge, units = edge / 8, area = edge * edge;
+    const int64_t total = (int64_t)w.items * edge * units;
     for (int64_t i = (int64_t)block * THREADS + threadIdx.x; i < total; i += (int64_t)blocks * THREADS) {
-        const int row = (int)(i / units), col = (int)(i - row * units) * 8;
+        const int t = (int)(i / (edge * units)), at = (int)(i - (int64_t)t * edge * units);
+        const int r = at / units, c = at % units * 8;
+        int tm, tn;
+        tile_at(p.whole + t, w, tm, tn);
+        const int row = tm * edge + r, col = tn * edge + c;
+        if (row >= p.M)
+            continue;                                       // (four neighbours together)
         float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, b[8];
         if (col < p.N) {
-            const float *q = p.P + (int64_t)row * p.ldp + col;
-            const bool two = col + 4 < p.ldp;
-            for (int s = 0; s < p.splits; ++s, q += (int64_t)p.M * p.ldp) {
-                const floatx4 lo = *reinterpret_cast<const floatx4 *>(q);
-                floatx4 hi = {0, 0, 0, 0};
-                if (two)
-                    hi = *reinterpret_cast<const floatx4 *>(q + 4);
+            const float *q = p.P + (int64_t)t * p.splits * area + r * edge + c;
+#pragma unroll 4
+            for (int s = 0; s < p.splits; ++s, q += area) {
+                const floatx4 lo = *reinterpret_cast<const floatx4 *>(q), hi = *reinterpret_cast<const floatx4 *>(q + 4);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     v[e] += lo[e];
@@ -221,12 +226,13 @@ __device__ __forceinline__ void reduce_rows(const Product &p, int block, int blo
     }
 }
 template <bool BF16>
-__global__ void __launch_bounds__(THREADS) reduce_kernel(const Product p, const Product q, int pblocks, int qblocks)
+__global__ void __launch_bounds__(THREADS) reduce_kernel(const Product p, const Product q, const Spread wp, const Spread wq,
+                                                         int pblocks, int qblocks)
 {
     if ((int)blockIdx.x < pblocks)
-        reduce_rows<BF16>(p, blockIdx.x, pblocks);
+        reduce_tiles<BF16>(p, wp, blockIdx.x, pblocks);
     else
-        reduce_rows<BF16>(q, blockIdx.x - pblocks, qblocks);
+        reduce_tiles<BF16>(q, wq, blockIdx.x - pblocks, qblocks);
 }
 
 template <bool BF16>
@@ -298,19 +304,27 @@ hipError_t launch_prepare(const Slope &g, const Copy &x, const Copy &w, bool bf1
 
 hipError_t launch_reduce(const Product *p, const Product *q, bool bf16, hipStream_t s)
 {
-    auto blocks = [](const Product *x) {
-        return x ? blocks_for((int64_t)x->M * (((int64_t)x->N + kBlock8 - 1) / kBlock8 * 4)) : 0;
+    // items: the cut tiles
+    auto cut = [](const Product *x) -> Spread {
+        if (!x)
+            return {0, 0, 0};
+        const int tm = (int)(((int64_t)x->M + x->edge - 1) / x->edge), tn = (x->N + x->edge - 1) / x->edge;
+        return {tm, tn, tm * tn - x->whole};
     };
-    const int pb = blocks(p), qb = blocks(q);
+    auto blocks = [](const Product *x, const Spread &w) {
+        return w.items > 0 ? blocks_for((int64_t)w.items * x->edge * (x->edge / 8)) : 0;
+    };
+    const Spread wp = cut(p), wq = cut(q);
+    const int pb = blocks(p, wp), qb = blocks(q, wq);
     const Product none{};
     if (pb + qb == 0)
         return hipSuccess;
     if (bf16)
         hipLaunchKernelGGL((reduce_kernel<true>), dim3((unsigned)(pb + qb)), dim3(THREADS), 0, s, p ? *p : none,
-                           q ? *q : none, pb, qb);
+                           q ? *q : none, wp, wq, pb, qb);
     else
         hipLaunchKernelGGL((reduce_kernel<false>), dim3((unsigned)(pb + qb)), dim3(THREADS), 0, s, p ? *p : none,
-                           q ? *q : none, pb, qb);
+                           q ? *q : none, wp, wq, pb, qb);
     return hipGetLastError();
 }
 

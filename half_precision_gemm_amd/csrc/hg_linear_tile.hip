@@ -81,7 +81,7 @@ __device__ __forceinline__ void put(const floatx4 (&blk)[T], uint32_t stg, int l
 }
 
 template <bool TA, bool TB, bool KCHK, bool BF16>
-__global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p, int tiles_m, int tiles_n, int total)
+__global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p, const Spread w)
 {
     __shared__ __attribute__((aligned(1024))) unsigned char smem[LDS_BYTES];
     int lane = threadIdx.x & 63;
@@ -89,32 +89,21 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
     const int wm = wave >> 1, wn = wave & 1;
     const uint32_t lds_base = (uint32_t)reinterpret_cast<uintptr_t>(smem);
 
-    struct Tile {
-        int slice, m0, n0, nk;
-    };
     Panel<EDGE, TA, KCHK> pa;
     Panel<EDGE, TB, KCHK> pb;
-    const int stages = (p.K + kStage - 1) / kStage;
-    auto find = [&](int id, Tile &t) __attribute__((always_inline)) {
-        int tm, tn;
-        place(id, total, tiles_m, tiles_n, t.slice, tm, tn);
-        t.m0 = tm * EDGE;
-        t.n0 = tn * EDGE;
-        t.nk = min(stages - t.slice * p.per, p.per);
-    };
     auto load = [](i32x4 r, lds_u32 *dst, int o) __attribute__((always_inline)) {
         hg_lin_tile_load_lds(r, dst, 16, o, 0, 0, 0);
     };
-    auto issue_a = [&](const Tile &t, int kt, int slot, int i) __attribute__((always_inline)) {
+    auto issue_a = [&](const Item &t, int kt, int slot, int i) __attribute__((always_inline)) {
         pa.issue(load, kt, kt < t.nk, lds_base + slot * SLOT, i, wave, lane);
     };
-    auto issue_b = [&](const Tile &t, int kt, int slot, int i) __attribute__((always_inline)) {
+    auto issue_b = [&](const Item &t, int kt, int slot, int i) __attribute__((always_inline)) {
         pb.issue(load, kt, kt < t.nk, lds_base + LDS_B + slot * SLOT, i, wave, lane);
     };
     // Stages 0 and 1 of a tile (the K loop issues the rest).
-    auto begin = [&](const Tile &t) __attribute__((always_inline)) {
-        pa.set(p.A, p.lda, t.m0, p.M, p.K, t.slice * p.per, wave, lane);
-        pb.set(p.B, p.ldb, t.n0, p.N, p.K, t.slice * p.per, wave, lane);
+    auto begin = [&](const Item &t) __attribute__((always_inline)) {
+        pa.set(p.A, p.lda, t.m0, p.M, p.K, t.kt0, wave, lane);
+        pb.set(p.B, p.ldb, t.n0, p.N, p.K, t.kt0, wave, lane);
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
 #pragma unroll
@@ -135,8 +124,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
     floatx4 acc[T][T];
     half8 fa[2][TQ], fb[2][T];         // A: by quarter parity; B: by k-step
     int id = blockIdx.x;
-    Tile t;
-    find(id, t);
+    Item t = item_at<EDGE>(p, w, id);
     begin(t);
     // An interior epilogue issues at least one store in each of its 32 passes
     // after the next tile's 4·L first loads, and the counter retires in order:
@@ -222,13 +210,13 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
         const int row0 = t.m0 + wm * WT;
         const int stg = 2 * SLOT + wave * (16 * WT * 4);
         prev = t.m0 + EDGE <= p.M && t.n0 + EDGE <= p.N ? 1 : 2;
-        Drain<WT, BF16> out(p, smem + stg, lane, t.slice, t.n0 + wn * WT);
+        Drain<EDGE, WT, BF16> out(p, t, smem + stg, lane, t.n0 + wn * WT);
         out.request(row0);
         __builtin_amdgcn_sched_barrier(0);
         id += gridDim.x;
-        const bool more = id < total;
+        const bool more = id < w.items;
         if (more) {
-            find(id, t);
+            t = item_at<EDGE>(p, w, id);
             begin(t);
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -253,11 +241,12 @@ template <bool TA, bool TB, bool BF16>
 hipError_t launch(const Product &p, hipStream_t s)
 {
     const int tiles_m = (int)(((int64_t)p.M + EDGE - 1) / EDGE), tiles_n = (p.N + EDGE - 1) / EDGE;
-    const int64_t total = (int64_t)tiles_m * tiles_n * p.splits;
+    const int64_t total = p.whole + ((int64_t)tiles_m * tiles_n - p.whole) * p.splits;
     if (total <= 0)
         return hipSuccess;
     if (total > 0x7fffffff - 4096)
         return hipErrorInvalidConfiguration;
+    const Spread w{tiles_m, tiles_n, (int)total};
     // one workgroup per CU, a multiple of 8 so that a workgroup's tiles stay on its XCD
     int64_t grid = cu_count();
     grid = grid / 8 * 8 > 0 ? grid / 8 * 8 : grid;
@@ -265,10 +254,10 @@ hipError_t launch(const Product &p, hipStream_t s)
         grid = total;
     if (!(TA && TB) && p.K % kStage != 0)
         hipLaunchKernelGGL((linear_tile_kernel<TA, TB, !(TA && TB), BF16>), dim3((unsigned)grid), dim3(THREADS), 0, s, p,
-                           tiles_m, tiles_n, (int)total);
+                           w);
     else
         hipLaunchKernelGGL((linear_tile_kernel<TA, TB, false, BF16>), dim3((unsigned)grid), dim3(THREADS), 0, s, p,
-                           tiles_m, tiles_n, (int)total);
+                           w);
     return hipGetLastError();
 }
 
