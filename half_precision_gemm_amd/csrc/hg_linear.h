@@ -374,21 +374,33 @@ __device__ __forceinline__ uint16_t narrow(float v)
         return __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
-// Eight 16-bit elements at p[0 .. n-1] (the others 0; n may pass 8).
+// The 16-bit elements p[0 .. n-1] of eight, the others 0 (n may pass 8, or be
+// none).  Short of eight, every load takes an index that is there, so that
+// none of them is behind a branch and they wait for memory together.
+__device__ __forceinline__ u32x4 load16x8(const void *p, int n)
+{
+    const uint16_t *h = static_cast<const uint16_t *>(p);
+    u32x4 w = {0, 0, 0, 0};
+    if (n >= 8) {
+        w = *reinterpret_cast<const u32x4_any *>(h);
+    } else if (n > 0) {
+        uint32_t x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = h[min(e, n - 1)];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            w[e >> 1] |= (e < n ? x[e] : 0u) << (16 * (e & 1));
+    }
+    return w;
+}
 template <bool BF16>
 __device__ __forceinline__ void load8(const void *p, int n, float (&v)[8])
 {
-    const uint16_t *h = static_cast<const uint16_t *>(p);
-    if (n >= 8) {
-        const u32x4 w = *reinterpret_cast<const u32x4_any *>(h);
+    const u32x4 w = load16x8(p, n);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = widen<BF16>((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = e < n ? widen<BF16>(h[e]) : 0.0f;
-    }
+    for (int e = 0; e < 8; ++e)
+        v[e] = widen<BF16>((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
 }
 template <bool BF16>
 __device__ __forceinline__ u32x4 pack8(const float (&v)[8])
@@ -598,13 +610,18 @@ __device__ __forceinline__ void values8(u32x2 w, float scale, float (&v)[8])
 }
 __device__ __forceinline__ u32x2 load_codes(const uint8_t *p, int n)
 {
-    if (n >= 8)
-        return *reinterpret_cast<const u32x2_any *>(p);
     u32x2 w = {0, 0};
+    if (n >= 8) {
+        w = *reinterpret_cast<const u32x2_any *>(p);
+    } else if (n > 0) {
+        uint32_t x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (e < n)
-            w[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
+        for (int e = 0; e < 8; ++e)
+            x[e] = p[min(e, n - 1)];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            w[e >> 2] |= (e < n ? x[e] : 0u) << (8 * (e & 3));
+    }
     return w;
 }
 __device__ __forceinline__ void store_codes(uint8_t *p, int n, u32x2 w)
@@ -664,10 +681,13 @@ __device__ __forceinline__ void finish8(const Finish &f, int row, int col, float
                         v[4 * h + e] += w[e];
                 }
             } else {
+                float w[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (e < n)
-                        v[e] += r[e];
+                    w[e] = r[min(e, n - 1)];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] += e < n ? w[e] : 0.0f;
             }
         }
         if (n >= 8) {
@@ -691,12 +711,18 @@ __device__ __forceinline__ void finish8(const Finish &f, int row, int col, float
     }
 }
 
-// The biases of columns col .. col + 7 (0 past the last).
+// The biases of columns col .. col + 7 (past the last: its, not used).
 __device__ __forceinline__ void load_bias(const Finish &f, int col, float (&b)[8])
 {
+    if (f.bias) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        b[e] = f.bias && col + e < f.cols ? f.bias[col + e] : 0.0f;
+        for (int e = 0; e < 8; ++e)
+            b[e] = f.bias[min(col + e, f.cols - 1)];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            b[e] = 0.0f;
+    }
 }
 
 // Waits for the biases here: otherwise the compiler waits for them inside the

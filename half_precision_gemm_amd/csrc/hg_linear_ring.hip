@@ -194,17 +194,18 @@ __device__ __forceinline__ void sum_strips(const Strips &b, int block, unsigned 
 }
 
 // The two products of a gradient and the end of its column sums, which do not
-// depend on each other, in one launch: their tiles fill the GPU together.
+// depend on each other, in one launch: their tiles fill the GPU together, the
+// longer ones (y_first: y's) first, so that short ones end the launch.
 template <int EDGE, bool KCHK, bool BF16>
 __global__ void __launch_bounds__(THREADS, 1)
-linear_ring_pair_kernel(const Product x, const Product y, const Strips b, const Spread wx, const Spread wy)
+linear_ring_pair_kernel(const Product x, const Product y, const Strips b, const Spread wx, const Spread wy, int y_first)
 {
     __shared__ __attribute__((aligned(1024))) unsigned char smem[kLds<EDGE>];
-    const int id = blockIdx.x;
-    if (id < wx.items)
-        ring_tile<EDGE, false, true, KCHK, BF16>(x, wx, id, smem);
-    else if (id < wx.items + wy.items)
-        ring_tile<EDGE, true, true, false, BF16>(y, wy, id - wx.items, smem);
+    const int id = blockIdx.x, at_x = y_first ? id - wy.items : id, at_y = y_first ? id : id - wx.items;
+    if (at_x >= 0 && at_x < wx.items)
+        ring_tile<EDGE, false, true, KCHK, BF16>(x, wx, at_x, smem);
+    else if (at_y >= 0 && at_y < wy.items)
+        ring_tile<EDGE, true, true, false, BF16>(y, wy, at_y, smem);
     else
         sum_strips(b, id - wx.items - wy.items, smem);
 }
@@ -244,13 +245,14 @@ hipError_t launch_pair(const Product *x, const Product *y, const Strips &b, hipS
         return hipSuccess;
     if (total > 0x7fffffff)
         return hipErrorInvalidConfiguration;
+    const int y_first = py.per > px.per;
     // (both k-major: the buffer's range ends the sum)
     if (px.K % BK != 0)
         hipLaunchKernelGGL((linear_ring_pair_kernel<EDGE, true, BF16>), dim3((unsigned)total), dim3(THREADS), 0, s, px,
-                           py, b, wx, wy);
+                           py, b, wx, wy, y_first);
     else
         hipLaunchKernelGGL((linear_ring_pair_kernel<EDGE, false, BF16>), dim3((unsigned)total), dim3(THREADS), 0, s, px,
-                           py, b, wx, wy);
+                           py, b, wx, wy, y_first);
     return hipGetLastError();
 }
 

@@ -97,16 +97,7 @@ __device__ __forceinline__ void copy_rows(const Copy &q, int block, int blocks)
             restore8(static_cast<const uint8_t *>(q.src) + r * q.lds, q.scales + r * q.ldss, c, n, v);
             w = pack8<BF16>(v);
         } else {
-            const uint16_t *s = static_cast<const uint16_t *>(q.src) + r * q.lds + c;
-            if (n == 8) {
-                w = *reinterpret_cast<const u32x4_any *>(s);
-            } else {
-                w = u32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e < n)
-                        w[e >> 1] |= (uint32_t)s[e] << (16 * (e & 1));
-            }
+            w = load16x8(static_cast<const uint16_t *>(q.src) + r * q.lds + c, n);
         }
         *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(q.dst) + r * q.ldd + c) = w;
     }

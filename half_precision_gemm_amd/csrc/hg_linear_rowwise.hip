@@ -27,17 +27,6 @@ namespace {
 
 constexpr int WAVES = 8, THREADS = WAVES * 64, PIECE = 64;
 
-// k .. k+7 of a row, zero from K on.
-__device__ __forceinline__ half8 tail8(const uint16_t *row, int k, int K)
-{
-    u32x4 w = {0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (k + e < K)
-            w[e >> 1] |= (uint32_t)row[k + e] << (16 * (e & 1));
-    return __builtin_bit_cast(half8, w);
-}
-
 // NB blocks of 16 rows of W, MB blocks of 16 rows of X.
 template <int NB, int MB, bool BF16>
 __global__ void __launch_bounds__(THREADS, 1) linear_rowwise_kernel(const Product p)
@@ -132,10 +121,10 @@ __global__ void __launch_bounds__(THREADS, 1) linear_rowwise_kernel(const Produc
         for (int s = 0; s < 2; ++s) {
 #pragma unroll
             for (int j = 0; j < NB; ++j)
-                q.w[j][s] = tail8(w[j], k + 32 * s, K);
+                q.w[j][s] = __builtin_bit_cast(half8, load16x8(w[j] + k + 32 * s, K - k - 32 * s));
 #pragma unroll
             for (int i = 0; i < MB; ++i)
-                q.x[i][s] = tail8(x[i], k + 32 * s, K);
+                q.x[i][s] = __builtin_bit_cast(half8, load16x8(x[i] + k + 32 * s, K - k - 32 * s));
         }
         multiply(q);
     }
