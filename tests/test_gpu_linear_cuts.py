@@ -1,0 +1,132 @@
+"""The linear layer and its gradient on small integers, at sizes that cut the
+products every way: each tile edge, no slices, all tiles in slices, only the
+last round's tiles in slices, the row-wise form, both products of a gradient in
+one launch or in two.
+
+Sums of integers in -2 .. 2 stay below 2^24, so every fp32 sum is exact in any
+order, and so is torch's fp32 product; what is rounded is rounded once.  The
+workspace holds NaN before the call and the outputs are surrounded by a
+pattern."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+SHAPES = [(4133, 4365, 2048), (4133, 4365, 640), (2048, 2100, 1024), (2100, 1500, 1500), (1500, 1500, 6000),
+          (3000, 6000, 4000), (700, 1000, 3000), (130, 260, 4096), (65, 64, 4096), (300, 4000, 8192),
+          (1100, 1100, 4200), (2050, 2050, 300), (2050, 2050, 1000), (1300, 1400, 1600), (2000, 2000, 4096),
+          (90, 8192, 512), (90, 70000, 64), (16, 4096, 16384), (33, 5000, 2056), (4096, 8192, 512), (8300, 520, 1000),
+          (257, 4096, 8200), (1, 70000, 72), (64, 64, 1031), (2, 1 << 20, 8), (80, 24, 1 << 20)]
+
+
+def ints(g, *shape):
+    return torch.randint(-2, 3, shape, generator=g, device=DEV, dtype=torch.int8).float()
+
+
+def room(M, N, t):
+    buf = torch.full((M + 2, N + 8), -77.0, dtype=t, device=DEV)
+    return buf, buf[1:M + 1, :N]
+
+
+def around(buf, M, N):
+    assert (buf[0] == -77).all() and (buf[M + 1] == -77).all() and (buf[:, N:] == -77).all()
+
+
+def nan_work(need):
+    return torch.full((need // 4 + 4,), float("nan"), device=DEV)
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_forward(hg, M, N, K):
+    print(f"[cuts] forward {M}x{N}x{K}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(M * 31 + N * 7 + K)
+    X, W, b, R = ints(g, M, K), ints(g, N, K), ints(g, N), ints(g, M, N)
+    z = X @ W.t() + b
+    for t, out, save8 in ((F16, F32, True), (BF16, BF16, False)):
+        Xh, Wh = X.to(t), W.to(t)
+        buf, Y = room(M, N, out)
+        zbuf, Z = room(M, N, t)
+        Z8 = hg.checkpoint8_empty(M, N, DEV)
+        hg.linear(Xh, Wh, Y, bias=b, act=hg.ACT_RELU, residual=R.to(out), Z=Z8 if save8 else Z,
+                  work=nan_work(hg.linear_workspace_size(Xh, Wh)))
+        around(buf, M, N)
+        assert torch.equal(Y, (z.relu() + R).to(out))
+        if save8 and K < 1 << 20:                  # z is an integer below 2^11: exact in fp16
+            assert float(z.abs().max()) < 2048
+            want = hg.checkpoint8_write(z.half(), *hg.checkpoint8_empty(M, N, DEV))
+            assert torch.equal(Z8[0], want[0]) and torch.equal(Z8[1], want[1])
+        elif not save8:
+            around(zbuf, M, N)
+            assert torch.equal(Z, z.to(t))
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_gradient(hg, M, N, K):
+    print(f"[cuts] gradient {M}x{N}x{K}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(M * 37 + N * 11 + K)
+    X, W, dY, Z = ints(g, M, K), ints(g, N, K), ints(g, M, N), ints(g, M, N)
+    dw0, db0 = ints(g, N, K), ints(g, N)
+    dz = torch.where(Z > 0, dY, 0.0)
+    dx, dw, db = dz @ W, dz.t() @ X, dz.sum(0)
+    for t, wt, acc, want in ((F16, F32, False, "xwb"), (BF16, F32, True, "xwb"), (BF16, BF16, False, "x"),
+                             (F16, F16, False, "w")):
+        Xh, Wh, dYh, Zh = X.to(t), W.to(t), dY.to(t), Z.to(t)
+        xb, dX = room(M, K, t)
+        wb, dW = room(N, K, wt)
+        dB = db0.clone()
+        if acc:
+            dW.copy_(dw0)
+        hg.linear_grad(dYh, Wh, Xh, Z=Zh, act=hg.ACT_RELU, dX=dX if "x" in want else None,
+                       dW=dW if "w" in want else None, dbias=dB if "b" in want else None, accumulate=acc,
+                       work=nan_work(hg.linear_grad_workspace_size(dYh, Wh, Xh)))
+        around(xb, M, K)
+        around(wb, N, K)
+        if "x" in want:
+            assert torch.equal(dX, dx.to(t))
+        if "w" in want:
+            assert torch.equal(dW, (dw + dw0 if acc else dw).to(wt))
+        if "b" in want:
+            assert torch.equal(dB, db + db0 if acc else db)
+
+
+@pytest.mark.parametrize("M,N,K", [(2050, 2050, 1000), (4133, 4365, 2048), (300, 4000, 8192)])
+def test_cut_products_in_place_and_again(hg, M, N, K):
+    """Slices with the residual in place, twice on one workspace: nothing of the first call is left in the second."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    X, W, R = ints(g, M, K).to(F16), ints(g, N, K).to(F16), ints(g, M, N)
+    Y = R.clone()
+    work = nan_work(hg.linear_workspace_size(X, W))
+    hg.linear(X, W, Y, residual=Y, work=work)
+    hg.linear(X, W, Y, residual=Y, work=work)
+    assert torch.equal(Y, 2 * (X.float() @ W.float().t()) + R)
+
+
+def test_offsets_past_32_bits(hg):
+    """Every matrix with rows so far apart that its last element lies past 2^32 bytes."""
+    M, N, K, ld = 70000, 72, 136, 32768
+    g = torch.Generator(device=DEV).manual_seed(4)
+    X, W, dY, Z = ints(g, M, K), ints(g, N, K), ints(g, M, N), ints(g, M, N)
+
+    def far(x, t):
+        big = torch.empty(M, ld, dtype=t, device=DEV)
+        v = big[:, 8:8 + x.shape[1]]
+        v.copy_(x)
+        return v
+    Xh, dYh, Zh = far(X, F16), far(dY, F16), far(Z, F16)
+    Y, R = far(dY, F32), far(Z, F32)
+    hg.linear(Xh, W.to(F16), Y, residual=R, act=hg.ACT_RELU, Z=Zh)
+    z = X @ W.t()
+    assert torch.equal(Y, z.relu() + Z) and torch.equal(Zh, z.half())
+    Zh.copy_(Z)
+    dX, dW, db = far(X, F16), torch.empty(N, K, device=DEV), torch.empty(N, device=DEV)
+    hg.linear_grad(dYh, W.to(F16), Xh, Z=Zh, act=hg.ACT_RELU, dX=dX, dW=dW, dbias=db)
+    dz = torch.where(Z > 0, dY, 0.0)
+    assert torch.equal(dX, (dz @ W).half()) and torch.equal(dW, dz.t() @ X) and torch.equal(db, dz.sum(0))
+    codes, scales = torch.empty(M, ld * 2, dtype=torch.uint8, device=DEV)[:, :K], torch.empty(M, 5, dtype=torch.uint8, device=DEV)
+    hg.checkpoint8_write(Xh, codes, scales)
+    back = hg.checkpoint8_read(codes, scales, far(Z[:, :1].expand(M, K), F16))
+    assert torch.equal(back, Xh)                       # small integers are exact in e4m3
+    hg.linear_grad(dYh, W.to(F16), (codes, scales), Z=Zh, act=hg.ACT_RELU, dW=dW, accumulate=True)
+    assert torch.equal(dW, 2 * (dz.t() @ X))
