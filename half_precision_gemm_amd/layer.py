@@ -13,7 +13,7 @@ import ctypes
 
 import torch
 
-from . import HG_BF16, HG_F16, HG_F32, HgError, _stream_handle, lib
+from . import HG_BF16, HG_F16, HG_F32, HgError, _raw_stream, lib
 
 HG_E4M3 = 3
 E4M3_BLOCK = 32
@@ -48,6 +48,7 @@ lib.hg_checkpoint8_read.restype = _int
 # torch's getter of the current device without the checks of
 # torch.cuda.current_device() (the tensors at hand are on the GPU already).
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_stream = _raw_stream or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _HALF = {torch.float16: HG_F16, torch.bfloat16: HG_BF16}
 _ONLY = {torch.float16: {torch.float16: HG_F16}, torch.bfloat16: {torch.bfloat16: HG_BF16},
          torch.float32: {torch.float32: HG_F32}}
@@ -57,8 +58,8 @@ _BYTES = {torch.uint8: HG_E4M3}
 
 
 def _lead(t, name, types, dev):
-    """The leading dimension of a valid matrix on device `dev` (None: on any);
-    raises for anything else."""
+    """The leading dimension of a valid matrix on device `dev`; raises for
+    anything else."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in types:
@@ -67,7 +68,7 @@ def _lead(t, name, types, dev):
         raise ValueError(f"{name} must be 2-D")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if dev is not None and t.get_device() != dev:
+    if t.get_device() != dev:
         raise ValueError("all tensors must be on one device")
     (rows, cols), (ld, unit) = t.shape, t.stride()
     if rows and cols > 1 and unit != 1:
@@ -112,7 +113,7 @@ def _saved(m, name, dtype, dev):
 def _device(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    return t.get_device() if t.is_cuda else None
+    return t.get_device() if t.is_cuda else None       # _lead refuses the host's by name
 
 
 def _vector(v, name, n, dev):
@@ -133,23 +134,21 @@ def _new_room(need, like):
     return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
 
 
-def _call(fn, name, like, *args):
-    """fn(*args, the current stream of `like`'s device), with that device current."""
-    st = _on_device(like, fn, *args, _stream_handle(like))
-    if st != 0:
-        raise HgError(name, st)
-
-
-def _on_device(like, fn, *args):
-    dev = like.get_device()
-    if _current_device() == dev:
-        return fn(*args)
+def _elsewhere(fn, dev, args):
     with torch.cuda.device(dev):
         return fn(*args)
 
 
-def _size(fn, name, like, *args):
-    need = _on_device(like, fn, *args)
+def _call(fn, name, dev, *args):
+    """fn(*args, the current stream of device `dev`), with that device current."""
+    args += (_stream(dev),)
+    st = fn(*args) if _current_device() == dev else _elsewhere(fn, dev, args)
+    if st != 0:
+        raise HgError(name, st)
+
+
+def _size(fn, name, dev, *args):
+    need = fn(*args) if _current_device() == dev else _elsewhere(fn, dev, args)
     if need < 0:
         raise HgError(name, int(need))
     return int(need)
@@ -170,8 +169,8 @@ def _linear_operands(X, W):
 
 def linear_workspace_size(X, W) -> int:
     """Bytes of workspace linear needs for these operands (hg_linear_workspace_size)."""
-    x, w, M, N, K, _ = _linear_operands(X, W)
-    return _size(lib.hg_linear_workspace_size, "hg_linear_workspace_size", X, M, N, K, x, w)
+    x, w, M, N, K, dev = _linear_operands(X, W)
+    return _size(lib.hg_linear_workspace_size, "hg_linear_workspace_size", dev, M, N, K, x, w)
 
 
 def linear_workspace(X, W):
@@ -209,12 +208,12 @@ def linear(X, W, Y, bias=None, act: int = 0, residual=None, Z=None, work=None):
         wptr, wbytes = _room(work, dev)
     args = (int(act), M, N, K, x, w, b, r, y, z)
     try:
-        _call(lib.hg_linear, "hg_linear", X, *args, wptr, wbytes)
+        _call(lib.hg_linear, "hg_linear", dev, *args, wptr, wbytes)
     except HgError as e:
         if work is not None or e.status != _NO_WORK:
             raise
-        need = _size(lib.hg_linear_workspace_size, "hg_linear_workspace_size", X, M, N, K, x, w)
-        _call(lib.hg_linear, "hg_linear", X, *args, _new_room(need, X).data_ptr(), need)
+        need = _size(lib.hg_linear_workspace_size, "hg_linear_workspace_size", dev, M, N, K, x, w)
+        _call(lib.hg_linear, "hg_linear", dev, *args, _new_room(need, X).data_ptr(), need)
     return Y
 
 
@@ -240,8 +239,8 @@ def _grad_operands(dY, W, X):
 def linear_grad_workspace_size(dY, W, X) -> int:
     """Bytes of workspace linear_grad needs for these operands
     (hg_linear_grad_workspace_size); W or X None: without dX or dW."""
-    dy, w, x, M, N, K, _ = _grad_operands(dY, W, X)
-    return _size(lib.hg_linear_grad_workspace_size, "hg_linear_grad_workspace_size", dY, M, N, K, dy, w, x)
+    dy, w, x, M, N, K, dev = _grad_operands(dY, W, X)
+    return _size(lib.hg_linear_grad_workspace_size, "hg_linear_grad_workspace_size", dev, M, N, K, dy, w, x)
 
 
 def linear_grad_workspace(dY, W, X):
@@ -284,11 +283,11 @@ def linear_grad(dY, W, X, Z=None, act: int = 0, dX=None, dW=None, dbias=None, ac
     elif act != 0:
         raise ValueError("the activation's gradient needs Z")
     if work is None:
-        work = _new_room(_size(lib.hg_linear_grad_workspace_size, "hg_linear_grad_workspace_size", dY, M, N, K, dy, w,
+        work = _new_room(_size(lib.hg_linear_grad_workspace_size, "hg_linear_grad_workspace_size", dev, M, N, K, dy, w,
                                x), dY)
     if work is not None:
         wptr, wbytes = _room(work, dev)
-    _call(lib.hg_linear_grad, "hg_linear_grad", dY, int(act), M, N, K, dy, w, x, z, gx, gw, gb,
+    _call(lib.hg_linear_grad, "hg_linear_grad", dev, int(act), M, N, K, dy, w, x, z, gx, gw, gb,
           1 if accumulate else 0, wptr, wbytes)
     return dX, dW, dbias
 
@@ -304,18 +303,18 @@ def _checkpoint(X, codes, scales):
     x, c = _matrix(X, "X", _HALF, dev), _pair((codes, scales), "the checkpoint", dev)
     if codes.shape != X.shape:
         raise ValueError(f"codes {tuple(codes.shape)} do not match X {tuple(X.shape)}")
-    return x, c, X.shape[0], X.shape[1]
+    return x, c, *X.shape, dev
 
 
 def checkpoint8_write(X, codes, scales):
     """X (float16 or bfloat16) as an 8-bit checkpoint; returns (codes, scales)."""
-    x, c, M, N = _checkpoint(X, codes, scales)
-    _call(lib.hg_checkpoint8_write, "hg_checkpoint8_write", X, M, N, x, c)
+    x, c, M, N, dev = _checkpoint(X, codes, scales)
+    _call(lib.hg_checkpoint8_write, "hg_checkpoint8_write", dev, M, N, x, c)
     return codes, scales
 
 
 def checkpoint8_read(codes, scales, X):
     """The values of an 8-bit checkpoint, written to X (float16 or bfloat16); returns X."""
-    x, c, M, N = _checkpoint(X, codes, scales)
-    _call(lib.hg_checkpoint8_read, "hg_checkpoint8_read", X, M, N, c, x)
+    x, c, M, N, dev = _checkpoint(X, codes, scales)
+    _call(lib.hg_checkpoint8_read, "hg_checkpoint8_read", dev, M, N, c, x)
     return X
