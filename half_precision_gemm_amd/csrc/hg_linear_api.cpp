@@ -276,22 +276,21 @@ bool bad_work(const void *work, int64_t need) { return need > 0 && (work == null
 // Whether the forward product of M <= kFewRows rows goes row by row: one
 // launch that reads W once, but X once for every 16 rows of W.  Its time is
 // that of the CU with the most rows of W: per 16 rows and element of the sum
-// 1.2 ns, and 0.05 for every row of X (rounded up to 16 from 17 on).  Measured
-// against 64×64 tiles in their best slices, bf16, us (M × N × K): 1×4096×4096
-// 7.3 / 10.9, 16×4096×4096 9.8 / 11.5, 16×1024×1024 4.2 / 6.9, 16×4096×16384
-// 33.6 / 25.5, 16×16384×4096 26.7 / 21.8, 64×4096×4096 22.3 / 12.6.  Those are
-// weights out of the last-level cache; out of HBM, as a model's weights are,
-// tiles take 3 us more and reach 4.6 TB/s (1×512×8192 11.3 / 15.0,
-// 8×4096×16384 35.6 / 37.5, 16×16384×4096 33.8 / 33.4).
-// Operands that the tiles would have to copy first (twice their bytes at 5 TB/s, a
-// launch) count that.
+// 1.15 ns, and 0.045 for every row of X (rounded up to 16 from 17 on).  Tiles
+// are priced with weights out of HBM, as a model's weights are: 3 us more than
+// out of the last-level cache, and 4.6 TB/s at best.  Both, measured with
+// weights out of HBM, bf16, us (M × N × K), row-wise / tiles: 1×4096×4096
+// 9.0 / 14, 16×4096×4096 11.4 / 14, 64×4096×4096 22 / 14.4, 16×1024×1024 4.6 /
+// 9, 16×4096×16384 33.5 / 36.9, 32×4096×16384 46.4 / 38, 32×16384×4096 39.9 /
+// 33.5, 1×512×8192 11.3 / 15.  Operands that the tiles would have to copy first
+// (twice their bytes at 5 TB/s, a launch) count that.
 bool row_by_row(int64_t M, int64_t N, int64_t K, bool copy_x, bool copy_w, double tiles_us)
 {
     if (M > lin::kFewRows)
         return false;
     const int64_t blocks = (N + 15) / 16, cus = hg::cu_count();
     const double rows = M > 16 ? (double)((M + 15) / 16 * 16) : (double)M;
-    const double us = 2.2 + (double)((blocks + cus - 1) / cus) * (double)K * (1.2 + 0.05 * rows) * 1e-3;
+    const double us = 2.2 + (double)((blocks + cus - 1) / cus) * (double)K * (1.15 + 0.045 * rows) * 1e-3;
     tiles_us = std::max(tiles_us + 3.0, 4.0 + (double)N * (double)K * 2.0 / 4.6e6);
     double copies = copy_x || copy_w ? 3.0 : 0.0;
     copies += (copy_x ? (double)M * (double)K * 4.0 / 5e6 : 0.0) + (copy_w ? (double)N * (double)K * 4.0 / 5e6 : 0.0);
