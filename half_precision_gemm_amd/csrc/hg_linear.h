@@ -436,14 +436,17 @@ __device__ __forceinline__ void store8(void *p, int n, const float (&v)[8])
 // multiply does (0 times anything is 0); NaN passes through.  An activation is
 // 5 to 15 vector operations and two quarter-rate ones per element, which a
 // 256×256 tile pays for outside its matrix work: the constants are folded.
+// The slopes' s(1 - s) is e·s² with s = 1/(1 + e), exact to a few roundings
+// where 1 - s would have lost its digits.
 constexpr float kLog2e = 1.4426950408889634f;
 // s(x) with x given as -x·log2(e).
 __device__ __forceinline__ float logistic2(float x) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x)); }
 __device__ __forceinline__ float times(float z, float w) { return hg_lin_mul_legacy(z, w); }
+constexpr double kTanh2 = 1.5957691216057308;                // 2·sqrt(2/pi)
 // -2u·log2(e) of gelu_tanh.
 __device__ __forceinline__ float tanh_arg(float z, float z2)
 {
-    constexpr float c = -1.5957691216057308f * kLog2e;      // 2·sqrt(2/pi)
+    constexpr float c = (float)(-kTanh2 * 1.4426950408889634);
     return z * __builtin_fmaf(0.044715f * c, z2, c);
 }
 
@@ -492,12 +495,13 @@ __device__ __forceinline__ float slope(float dy, float z)
         normal_cdf(z, cdf, pdf);
         return dy * (cdf + times(z, pdf));
     } else if constexpr (ACT == kGeluTanh) {
-        const float z2 = z * z;
-        const float s = logistic2(tanh_arg(z, z2));
-        return dy * (s + times(z * __builtin_fmaf(0.21406964f, z2, 1.59576912f), s * (1.0f - s)));
+        const float z2 = z * z, e = __builtin_amdgcn_exp2f(tanh_arg(z, z2));
+        const float s = __builtin_amdgcn_rcpf(1.0f + e);
+        return dy * (s + times(z * __builtin_fmaf((float)(3 * 0.044715 * kTanh2), z2, (float)kTanh2), times(e, s * s)));
     } else if constexpr (ACT == kSilu) {
-        const float s = logistic2(-kLog2e * z);
-        return dy * (s + times(z, s * (1.0f - s)));
+        const float e = __builtin_amdgcn_exp2f(-kLog2e * z);
+        const float s = __builtin_amdgcn_rcpf(1.0f + e);
+        return dy * (s + times(z, times(e, s * s)));
     } else {
         return dy;
     }

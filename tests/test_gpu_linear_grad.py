@@ -175,6 +175,41 @@ def test_limits(hg):
     assert db[4] == 0
 
 
+@pytest.mark.parametrize("t", [F16, BF16])
+@pytest.mark.parametrize("name", ref.ACTS[1:])
+def test_slopes_of_every_value(hg, name, t):
+    """act' of all 2^16 values of a type, from dbias of one row with dY = 1.  Roundings of the formula: the
+    logistic's exponent is off by 2^-23 of itself (at most 2^-17 where e·s² is above 2^-40) and its factors by a few
+    2^-23; z·phi(z) and z·w·e·s² stay below 1.2; Phi's own formula is off by 0.75e-7: 2^-19 together."""
+    Z = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(1, -1).view(t)
+    db = torch.empty(65536, device=DEV)
+    hg.linear_grad(torch.ones(1, 65536, dtype=t, device=DEV), None, None, Z=Z.to(DEV), act=act_of(hg, name), dbias=db)
+    z, got = Z[0].double(), db.cpu().double()
+    fine = z.isfinite()
+    want = ref.slope(z.clamp(-200, 200), name)          # constant beyond
+    assert ((got - want).abs()[fine] <= 2.0 ** -19).all(), float((got - want).abs()[fine].max())
+    assert got[z.isnan()].isnan().all()
+    assert (got[z == float("inf")] == 1).all() and (got[z == float("-inf")] == 0).all()
+
+
+@pytest.mark.parametrize("t", [F16, BF16])
+@pytest.mark.parametrize("name", ref.ACTS)
+def test_activations_of_every_value(hg, name, t):
+    """act of all 2^16 values of a type through linear with K = 1, X = 1: within 2^-20·|z| (linear_ref.py)."""
+    W = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(-1, 1).view(t)
+    Y = torch.empty(1, 65536, device=DEV)
+    hg.linear(torch.ones(1, 1, dtype=t, device=DEV), W.to(DEV), Y, act=act_of(hg, name))
+    z, got = W[:, 0].double(), Y[0].cpu().double()
+    fine = z.isfinite()
+    want = ref.act(z, name)
+    if name != "none":
+        want = torch.where(z < -100, 0.0, want)         # where 64 bits meet inf times zero
+    assert ((got - want).abs()[fine] <= 2.0 ** -20 * z.abs()[fine] + 2.0 ** -149).all()
+    assert got[z.isnan()].isnan().all()
+    assert (got[z == float("inf")] == float("inf")).all()
+    assert (got[z == float("-inf")] == (float("-inf") if name == "none" else 0)).all()
+
+
 def test_padding_is_not_read(hg):
     """NaN behind the last column of every operand (strided() puts it there) reaches nothing: K and N no multiple of
     8 or 64, the last chunk and the last stage of every sum partial."""
