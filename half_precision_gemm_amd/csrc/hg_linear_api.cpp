@@ -22,27 +22,48 @@ int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
 int64_t blocks8(int64_t n) { return (n + HG_E4M3_BLOCK - 1) / HG_E4M3_BLOCK; }
 int64_t esize(int type) { return type == HG_F32 ? 4 : type == HG_E4M3 ? 1 : 2; }
 
-// Bytes [lo, hi); empty when lo == hi.
+// Bytes [lo, hi), empty when lo == hi; of a matrix its first `width` bytes of
+// every `pitch`.
 struct Span {
     uintptr_t lo, hi;
+    uint64_t width, pitch;
 };
-bool meet(const Span &a, const Span &b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
+// Different columns of one array (two matrices of the same pitch) do not meet.
+bool meet(const Span &a, const Span &b)
+{
+    if (!(a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi))
+        return false;
+    if (a.pitch != b.pitch)
+        return true;
+    const Span &l = a.lo <= b.lo ? a : b, &h = a.lo <= b.lo ? b : a;
+    const uint64_t d = (uint64_t)(h.lo - l.lo) % a.pitch;
+    return d < l.width || d + h.width > a.pitch;
+}
 Span span_of(const void *p, int64_t bytes)
 {
     const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return p == nullptr || bytes <= 0 ? Span{0, 0} : Span{lo, lo + (uintptr_t)bytes};
+    if (p == nullptr || bytes <= 0)
+        return {0, 0, 0, 1};
+    return {lo, lo + (uintptr_t)bytes, (uint64_t)bytes, (uint64_t)bytes};
+}
+Span rows_of(const void *p, int64_t rows, int64_t pitch, int64_t width)
+{
+    Span s = span_of(p, (rows - 1) * pitch + width);
+    s.width = (uint64_t)width;
+    s.pitch = (uint64_t)pitch;
+    return s;
 }
 Span data_span(const hg_matrix *m, int64_t rows, int64_t cols)
 {
     if (m == nullptr || rows <= 0 || cols <= 0)
-        return {0, 0};
-    return span_of(m->data, ((rows - 1) * m->ld + cols) * esize(m->type));
+        return span_of(nullptr, 0);
+    return rows_of(m->data, rows, m->ld * esize(m->type), cols * esize(m->type));
 }
 Span scale_span(const hg_matrix *m, int64_t rows, int64_t cols)
 {
     if (m == nullptr || m->type != HG_E4M3 || rows <= 0 || cols <= 0)
-        return {0, 0};
-    return span_of(m->scales, (rows - 1) * m->lds + blocks8(cols));
+        return span_of(nullptr, 0);
+    return rows_of(m->scales, rows, m->lds, blocks8(cols));
 }
 bool any_meet(std::initializer_list<Span> a, std::initializer_list<Span> b)
 {
@@ -415,7 +436,7 @@ int hg_linear(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
     const Span sx = data_span(X, M, K), sw = data_span(W, N, K), sb = span_of(bias, N * 4);
     const Span sr = data_span(R, M, N), sy = data_span(Y, M, N), sz = data_span(Z, M, N), ss = scale_span(Z, M, N);
     const bool in_place = R != nullptr && R->data == Y->data && R->ld == Y->ld;
-    if (any_meet({sy}, {sx, sw, sb, in_place ? Span{0, 0} : sr}))
+    if (any_meet({sy}, {sx, sw, sb, in_place ? span_of(nullptr, 0) : sr}))
         return -9;
     if (any_meet({sz, ss}, {sx, sw, sb, sr, sy}) || meet(sz, ss))
         return -10;

@@ -17,6 +17,7 @@ from . import HG_BF16, HG_F16, HG_F32, HgError, _raw_stream, lib
 
 HG_E4M3 = 3
 E4M3_BLOCK = 32
+_MAX_LD = 1 << 30                        # HG_LINEAR_MAX_LD; the row stride of a single row does not count
 ACT_GELU = 2
 ACT_GELU_TANH = 3
 ACT_SILU = 4
@@ -81,7 +82,7 @@ def _lead(t, name, types, dev):
 def _matrix(t, name, types, dev):
     try:                                 # an ordinary matrix, without the checks that name what is wrong
         ld, unit = t.stride()
-        if unit == 1 and ld >= t.shape[1] > 0 and t.get_device() == dev:
+        if unit == 1 and _MAX_LD >= ld >= t.shape[1] > 0 and t.get_device() == dev:
             return Matrix(t.data_ptr(), ld, None, 0, types[t.dtype])
     except (AttributeError, KeyError, TypeError, ValueError):
         pass

@@ -18,6 +18,10 @@
  * buffer; calls from several host threads are safe, and calls that overlap in
  * time need workspaces of their own (so do two captured graphs that may).
  * Every launch may be captured into a HIP graph.
+ *
+ * Overlap is judged by the bytes from a matrix's first element to its last,
+ * except between matrices whose rows are the same number of bytes apart:
+ * different columns of one array do not overlap.
  */
 #ifndef HGEMM_LINEAR_H
 #define HGEMM_LINEAR_H

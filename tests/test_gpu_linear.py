@@ -222,6 +222,30 @@ def test_two_streams_with_their_own_workspaces(hg):
     assert all(torch.equal(o, want[i]) for i in range(2) for o in outs[i])
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 64, 128), (5, 40, 72), (100, 72, 17), (300, 256, 264)])
+def test_columns_of_one_array(hg, M, N, K):
+    """X, Y and Z side by side in one array, as slices of one tensor: the same bits as apart, nothing else written."""
+    g = torch.Generator().manual_seed(M)
+    big = torch.randn(M, K + 2 * N + 24, generator=g).to(BF16).to(DEV)
+    W = torch.randn(N, K, generator=g).to(BF16).to(DEV)
+    X, Y, Z = big[:, 8:8 + K], big[:, 8 + K:8 + K + N], big[:, 16 + K + N:16 + K + 2 * N]
+    y, z = torch.empty(M, N, dtype=BF16, device=DEV), torch.empty(M, N, dtype=BF16, device=DEV)
+    want = big.clone()
+    hg.linear(X.contiguous(), W, y, act=act_of(hg, "silu"), Z=z)
+    hg.linear(X, W, Y, act=act_of(hg, "silu"), Z=Z)
+    want[:, 8 + K:8 + K + N] = y
+    want[:, 16 + K + N:16 + K + 2 * N] = z
+    assert torch.equal(big.view(torch.int16), want.view(torch.int16))
+
+
+def test_row_of_a_wide_array(hg):
+    """One row whose stride is past the largest leading dimension: a stride that no second row uses."""
+    X = torch.ones(1, 64, dtype=F16, device=DEV).as_strided((1, 64), (1 << 40, 1))
+    Y = torch.empty(1, 32, dtype=F16, device=DEV)
+    hg.linear(X, torch.ones(32, 64, dtype=F16, device=DEV), Y)
+    assert (Y == 64).all()
+
+
 def test_binding_refusals(hg):
     e = lambda m, n, t=F16: torch.zeros(m, n, dtype=t, device=DEV)  # noqa: E731
     X, W, Y = e(4, 16), e(8, 16), e(4, 8)

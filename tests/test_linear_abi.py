@@ -73,6 +73,21 @@ def test_linear_refusals(api, kw, code):
     assert linear(api, **kw) == code
 
 
+@pytest.mark.parametrize("X,Y,Z,code", [
+    ((0, 40), (34, 40), (50, 40), -11),               # bytes: X 0..33, Y 34..49, Z 50..65 of rows of 80: none meet
+    ((0, 40), (32, 40), (50, 40), -9),                # Y on X's last column
+    ((0, 40), (66, 40), (34, 40), -9),                # Y's end on the next row's X
+    ((0, 40), (34, 40), (48, 40), -10),               # Z on Y's last column
+    ((0, 40), (34, 40), (80 * 100, 40), -11),         # behind X's last row
+    ((0, 40), (34, 40), (80 * 99 + 18, 40), -10),     # in it, on X
+    ((0, 40), (34, 41), (50, 40), -9),                # another pitch
+])
+def test_columns_of_one_array(api, X, Y, Z, code):
+    """M = 100, K = 17, N = 8 in 16 bits; what does not overlap goes on to the missing workspace."""
+    X, Y, Z = (mat(api, P[0] + at, ld) for at, ld in (X, Y, Z))
+    assert linear(api, M=100, K=17, X=X, W=mat(api, P[1], 17), Y=Y, Z=Z, work=None) == code
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(act=9), -1), (dict(M=-1), -2), (dict(N=BIG + 1), -3), (dict(K=-1), -4), (dict(dY=NULL), -5),
     (dict(dY=(P[0], 8, F32)), -5), (dict(dY=(P[0], 7)), -5), (dict(W=NULL), -6), (dict(W=(P[1], 15)), -6),
