@@ -794,6 +794,17 @@ struct Drain {
     {
         load_bias(p.f, c0 + 8 * (lane % UNITS), bias);
     }
+    // What 256×256 tiles write passes the caches by: such a product's results
+    // are more than they hold, and they hold its operands (4096×8192×2048:
+    // gradient 272 -> 263 us; with Z 8192×16384×4096 823 -> 817).
+    template <class V, class U>
+    __device__ __forceinline__ void put(void *to, U v) const
+    {
+        if constexpr (EDGE == 256)
+            __builtin_nontemporal_store((V)v, static_cast<V *>(to));
+        else
+            *static_cast<V *>(to) = v;
+    }
     __device__ __forceinline__ bool inside(int row0) const
     {
         return row0 + 16 <= p.M && c0 + W <= p.N;
@@ -850,14 +861,14 @@ struct Drain {
             uint16_t *z = static_cast<uint16_t *>(f.Z) + row * f.ldz + col;
 #pragma unroll
             for (int t = 0; t < PASSES; ++t, z += ROWS * f.ldz)
-                *reinterpret_cast<u32x4_any *>(z) = pack8<BF16>(v[t]);
+                put<u32x4_any>(z, pack8<BF16>(v[t]));
         } else if (f.save == kSave8) {
             uint8_t *z = static_cast<uint8_t *>(f.Z) + row * f.ldz + col, *zs = f.Zs + row * f.ldzs + col / kBlock8;
 #pragma unroll
             for (int t = 0; t < PASSES; ++t, z += ROWS * f.ldz, zs += ROWS * f.ldzs) {
                 u32x2 w;
                 const int x = encode8<BF16>(v[t], 8, w);
-                *reinterpret_cast<u32x2_any *>(z) = w;
+                put<u32x2_any>(z, w);
                 if (unit % 4 == 0)
                     *zs = (uint8_t)(x + 127);
             }
@@ -884,14 +895,14 @@ struct Drain {
             float *c = static_cast<float *>(f.C) + row * f.ldc + col;
 #pragma unroll
             for (int t = 0; t < PASSES; ++t, c += ROWS * f.ldc) {
-                *reinterpret_cast<floatx4_any *>(c) = floatx4{v[t][0], v[t][1], v[t][2], v[t][3]};
-                *reinterpret_cast<floatx4_any *>(c + 4) = floatx4{v[t][4], v[t][5], v[t][6], v[t][7]};
+                put<floatx4_any>(c, floatx4{v[t][0], v[t][1], v[t][2], v[t][3]});
+                put<floatx4_any>(c + 4, floatx4{v[t][4], v[t][5], v[t][6], v[t][7]});
             }
         } else {
             uint16_t *c = static_cast<uint16_t *>(f.C) + row * f.ldc + col;
 #pragma unroll
             for (int t = 0; t < PASSES; ++t, c += ROWS * f.ldc)
-                *reinterpret_cast<u32x4_any *>(c) = pack8<BF16>(v[t]);
+                put<u32x4_any>(c, pack8<BF16>(v[t]));
         }
     }
     __device__ __forceinline__ void edge(int row0)
