@@ -73,7 +73,8 @@ hipError_t launch_ring(const Product &p, int tile, bool bf16, hipStream_t s);   
 // x (NT) and w (TT), either of them null, and the strips' sums in one launch.
 hipError_t launch_ring_pair(const Product *x, const Product *w, const Strips &b, int tile, bool bf16, hipStream_t s);
 hipError_t launch_tile(const Product &p, Layout l, bool bf16, hipStream_t s);               // 256
-hipError_t launch_rowwise(const Product &p, bool bf16, hipStream_t s);                      // M <= kFewRows; NN
+// M <= kFewRows, NN; direct: A and B as Product says.
+hipError_t launch_rowwise(const Product &p, bool direct, bool bf16, hipStream_t s);
 // The slices' partial sums of one or two products (either may be null).
 hipError_t launch_reduce(const Product *p, const Product *q, bool bf16, hipStream_t s);
 

@@ -295,23 +295,39 @@ int check_sizes(int64_t M, int64_t N, int64_t K, int first)
 bool bad_work(const void *work, int64_t need) { return need > 0 && (work == nullptr || ((uintptr_t)work & 15) != 0); }
 
 // Whether the forward product of M <= kFewRows rows goes row by row: one
-// launch that reads W once, but X once for every 16 rows of W.  Its time is
-// that of the CU with the most rows of W: per 16 rows and element of the sum
-// 1.15 ns, and 0.045 for every row of X (rounded up to 16 from 17 on).  Tiles
-// are priced with weights out of HBM, as a model's weights are: 3 us more than
-// out of the last-level cache, and 4.6 TB/s at best.  Both, measured with
-// weights out of HBM, bf16, us (M × N × K), row-wise / tiles: 1×4096×4096
-// 9.0 / 14, 16×4096×4096 11.4 / 14, 64×4096×4096 22 / 14.4, 16×1024×1024 4.6 /
-// 9, 16×4096×16384 33.5 / 36.9, 32×4096×16384 46.4 / 38, 32×16384×4096 39.9 /
-// 33.5, 1×512×8192 11.3 / 15.  Operands that the tiles would have to copy first
-// (twice their bytes at 5 TB/s, a launch) count that.
+// launch that reads W once, but X once for every 16 or 32 rows of W (a block).
+// What it takes, in us, from measurements with weights out of HBM, bf16: the
+// CUs take the blocks in rounds;
+//   through LDS, ns per k of a round: (0.85 + 0.42·fill) per 16 rows of W and
+//     0.33 per 16 of X, fill the part of the CUs that is busy; 2.5 us to begin
+//     with, in every round if X's rings leave no room for a second workgroup
+//     (with one, a last round that is not full costs half of one more);
+//   through registers, ns per 16 rows of W and k: 1.15, and 0.045 for every row
+//     of X (rounded up to 16 from 17 on).
+// Tiles are priced with weights out of HBM, as a model's weights are: 3 us more
+// than out of the last-level cache, and 4.6 TB/s at best.  Both, measured so,
+// us (M × N × K), row-wise / tiles: 1×4096×4096 9.2 / 14, 16×4096×4096 10.1 /
+// 14, 16×1024×1024 4.1 / 9, 16×4096×16384 28.0 / 36.9, 32×4096×16384 32.7 /
+// 37.6, 64×4096×16384 42.0 / 39.3, 32×16384×4096 30.3 / 33.1, 32×50264×2048
+// 60.3 / 50.1, 64×8192×8192 35.1 / 38.1.  Operands that the tiles would have to
+// copy first (twice their bytes at 5 TB/s, a launch) count that.
 bool row_by_row(int64_t M, int64_t N, int64_t K, bool copy_x, bool copy_w, double tiles_us)
 {
     if (M > lin::kFewRows)
         return false;
-    const int64_t blocks = (N + 15) / 16, cus = hg::cu_count();
-    const double rows = M > 16 ? (double)((M + 15) / 16 * 16) : (double)M;
-    const double us = 2.2 + (double)((blocks + cus - 1) / cus) * (double)K * (1.15 + 0.045 * rows) * 1e-3;
+    const int64_t cus = hg::cu_count(), per = (N + 31) / 32 >= cus ? 2 : 1, blocks = (N + 16 * per - 1) / (16 * per);
+    const double rounds = (double)((blocks + cus - 1) / cus), xb = M <= 16 ? 1.0 : M <= 32 ? 2.0 : 4.0;
+    double us;
+    if (!copy_x && !copy_w && (per == 1 || K >= 2048)) {
+        const double fill = std::min(1.0, (double)blocks / (double)cus);
+        const bool shared = (double)per * xb <= 2.0;
+        const double turns = shared ? 0.5 * (rounds + std::max(1.0, (double)blocks / (double)cus)) : rounds;
+        us = 2.5 * (shared ? 1.0 : rounds) + turns * (double)K * ((double)per * (0.85 + 0.42 * fill) + 0.33 * xb) * 1e-3;
+    } else {
+        const double rows = M > 16 ? 16.0 * xb : (double)M;
+        const int64_t b16 = (N + 15) / 16;
+        us = 2.2 + (double)((b16 + cus - 1) / cus) * (double)K * (1.15 + 0.045 * rows) * 1e-3;
+    }
     tiles_us = std::max(tiles_us + 3.0, 4.0 + (double)N * (double)K * 2.0 / 4.6e6);
     double copies = copy_x || copy_w ? 3.0 : 0.0;
     copies += (copy_x ? (double)M * (double)K * 4.0 / 5e6 : 0.0) + (copy_w ? (double)N * (double)K * 4.0 / 5e6 : 0.0);
@@ -319,7 +335,7 @@ bool row_by_row(int64_t M, int64_t N, int64_t K, bool copy_x, bool copy_w, doubl
 }
 
 struct LinearPlan {
-    bool copy_x, copy_w;
+    bool copy_x, copy_w, direct;
     Cut cut;
 };
 LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W)
@@ -328,6 +344,7 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
     double us;
     q.copy_x = !direct(X, K);
     q.copy_w = !direct(W, K);
+    q.direct = !q.copy_x && !q.copy_w;
     q.cut = best_cut({M, N, K}, &us);
     if (row_by_row(M, N, K, q.copy_x, q.copy_w, us)) {
         q.copy_x = q.copy_w = false;
@@ -493,7 +510,7 @@ int hg_linear(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
     }
     if (const hipError_t e = lin::launch_prepare(lin::Slope{}, cx, cw, bf16, s))
         return status_of(e);
-    const hipError_t e = q.cut.tile == 0     ? lin::launch_rowwise(p, bf16, s)
+    const hipError_t e = q.cut.tile == 0     ? lin::launch_rowwise(p, q.direct, bf16, s)
                          : q.cut.tile == 256 ? lin::launch_tile(p, lin::Layout::NN, bf16, s)
                                              : lin::launch_ring(p, q.cut.tile, bf16, s);
     if (e != hipSuccess || p.splits <= 1)

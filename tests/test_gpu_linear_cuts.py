@@ -130,3 +130,31 @@ def test_offsets_past_32_bits(hg):
     assert torch.equal(back, Xh)                       # small integers are exact in e4m3
     hg.linear_grad(dYh, W.to(F16), (codes, scales), Z=Zh, act=hg.ACT_RELU, dW=dW, accumulate=True)
     assert torch.equal(dW, 2 * (dz.t() @ X))
+
+
+@pytest.mark.parametrize("save", [None, "8"])
+@pytest.mark.parametrize("K", [8, 248, 256, 264, 1280, 2048, 2056, 4352])
+@pytest.mark.parametrize("N", [1, 16, 40, 4100, 8200, 16400])
+def test_few_rows(hg, N, K, save):
+    """Every count of rows that takes another form, sums that end inside a stage and are shorter or longer than the
+    ring, more workgroups than compute units, NaN behind every row and below the last one; K = 4352 is 17 stages."""
+    print(f"[cuts] few rows N={N} K={K} {save}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(N + K)
+    big = torch.full((65, K + 8), float("nan"), dtype=F16, device=DEV)
+    wide = torch.full((N + 1, K + 16), float("nan"), dtype=F16, device=DEV)
+    W = wide[:N, :K]
+    W.copy_(ints(g, N, K))
+    for M in (1, 2, 15, 16, 17, 32, 33, 48, 64):
+        big.fill_(float("nan"))
+        X = big[:M, :K]
+        X.copy_(ints(g, M, K))
+        want = torch.mm(X.float(), W.float().t())
+        buf, Y = room(M, N, F32)
+        Z = hg.checkpoint8_empty(M, N) if save else None
+        hg.linear(X, W, Y, Z=Z)
+        assert torch.equal(Y, want), (M, N, K)
+        around(buf, M, N)
+        if save:
+            assert want.abs().max() <= 2048               # exact in fp16
+            codes, scales = hg.checkpoint8_write(want.to(F16), *hg.checkpoint8_empty(M, N))
+            assert torch.equal(Z[0], codes) and torch.equal(Z[1], scales), (M, N, K)
