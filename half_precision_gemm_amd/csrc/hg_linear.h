@@ -70,6 +70,7 @@ struct Strips {
 };
 
 hipError_t launch_ring(const Product &p, int tile, bool bf16, hipStream_t s);               // 64 or 128; NN
+hipError_t launch_loose(const Product &p, bool bf16, hipStream_t s);                        // 64, any A and B; NN
 // x (NT) and w (TT), either of them null, and the strips' sums in one launch.
 hipError_t launch_ring_pair(const Product *x, const Product *w, const Strips &b, int tile, bool bf16, hipStream_t s);
 hipError_t launch_tile(const Product &p, Layout l, bool bf16, hipStream_t s);               // 256

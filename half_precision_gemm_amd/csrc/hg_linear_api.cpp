@@ -309,9 +309,10 @@ bool bad_work(const void *work, int64_t need) { return need > 0 && (work == null
 // us (M × N × K), row-wise / tiles: 1×4096×4096 9.2 / 14, 16×4096×4096 10.1 /
 // 14, 16×1024×1024 4.1 / 9, 16×4096×16384 28.0 / 36.9, 32×4096×16384 32.7 /
 // 37.6, 64×4096×16384 42.0 / 39.3, 32×16384×4096 30.3 / 33.1, 32×50264×2048
-// 60.3 / 50.1, 64×8192×8192 35.1 / 38.1.  Operands that the tiles would have to
-// copy first (twice their bytes at 5 TB/s, a launch) count that.
-bool row_by_row(int64_t M, int64_t N, int64_t K, bool copy_x, bool copy_w, double tiles_us)
+// 60.3 / 50.1, 64×8192×8192 35.1 / 38.1, 64×4096×16390 81 / 48.  Operands that
+// the tiles would have to copy first (twice their bytes at 5 TB/s, a launch)
+// count that, those that they take as they are (loose) do not.
+bool row_by_row(int64_t M, int64_t N, int64_t K, bool copy_x, bool copy_w, double tiles_us, bool loose)
 {
     if (M > lin::kFewRows)
         return false;
@@ -329,13 +330,16 @@ bool row_by_row(int64_t M, int64_t N, int64_t K, bool copy_x, bool copy_w, doubl
         us = 2.2 + (double)((b16 + cus - 1) / cus) * (double)K * (1.15 + 0.045 * rows) * 1e-3;
     }
     tiles_us = std::max(tiles_us + 3.0, 4.0 + (double)N * (double)K * 2.0 / 4.6e6);
+    if (loose)
+        return us < tiles_us;
     double copies = copy_x || copy_w ? 3.0 : 0.0;
     copies += (copy_x ? (double)M * (double)K * 4.0 / 5e6 : 0.0) + (copy_w ? (double)N * (double)K * 4.0 / 5e6 : 0.0);
     return us < tiles_us + copies;
 }
 
 struct LinearPlan {
-    bool copy_x, copy_w, direct;
+    bool copy_x, copy_w;
+    bool direct, loose;               // both operands direct; taken as they are by 64×64 tiles
     Cut cut;
 };
 LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W)
@@ -346,9 +350,17 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
     q.copy_w = !direct(W, K);
     q.direct = !q.copy_x && !q.copy_w;
     q.cut = best_cut({M, N, K}, &us);
-    if (row_by_row(M, N, K, q.copy_x, q.copy_w, us)) {
-        q.copy_x = q.copy_w = false;
+    // 64×64 tiles take operands that would have to be copied as they are: the
+    // slower loop costs less than the launch (copied / as they are, us:
+    // 333×1111×777 12.4 / 9.2, 100×100×101 6.8 / 5.9, 128×1024×8191 22.0 / 14.1,
+    // 1000×1000×4001 32.4 / 28.8, 2000×2000×1001 29.8 / 29.0, 700×3000×1001 26.5
+    // / 27.1).
+    q.loose = !q.direct && q.cut.tile == 64;
+    if (row_by_row(M, N, K, q.copy_x, q.copy_w, q.loose ? 1.15 * us : us, q.loose)) {
+        q.copy_x = q.copy_w = q.loose = false;
         q.cut = {0, 0, 1, 0};
+    } else if (q.loose) {
+        q.copy_x = q.copy_w = false;
     }
     return q;
 }
@@ -511,6 +523,7 @@ int hg_linear(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
     if (const hipError_t e = lin::launch_prepare(lin::Slope{}, cx, cw, bf16, s))
         return status_of(e);
     const hipError_t e = q.cut.tile == 0     ? lin::launch_rowwise(p, q.direct, bf16, s)
+                         : q.loose            ? lin::launch_loose(p, bf16, s)
                          : q.cut.tile == 256 ? lin::launch_tile(p, lin::Layout::NN, bf16, s)
                                              : lin::launch_ring(p, q.cut.tile, bf16, s);
     if (e != hipSuccess || p.splits <= 1)

@@ -65,7 +65,8 @@ __device__ __forceinline__ void finish_sums(const Product &p, float (*part)[MB *
 // nothing is staged, there is no barrier in the loop, and a wave has DEPTH
 // pieces in flight while it multiplies DEPTH others.  Rows past M or N are
 // read as the last row and their results dropped; a last piece of less than 64
-// k is loaded element by element.
+// k is loaded element by element (requested before the others, or as the row's
+// last eight with those before masked: no gain).
 template <int NB, int MB, bool BF16>
 __global__ void __launch_bounds__(THREADS, 1) linear_rowwise_kernel(const Product p)
 {
@@ -254,6 +255,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const Product
         wait_vmcnt<(NS - 2) * L>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
         const unsigned char *slot = smem + (kt % NS) * SLOT;
         const int c = ((wave * 4 + fhi) ^ frow) * 16;
         half8 w[NB], x[MB];
@@ -275,6 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const Product
     wait_vmcnt<0>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
     finish_sums<NB, MB, BF16>(p, reinterpret_cast<float(*)[MB * 16][NB * 16]>(smem), acc, n0, wave, lane);
 }
 

@@ -92,7 +92,7 @@ typedef struct hg_matrix {
  * No output may overlap an input, another output or the workspace, R = Y
  * excepted (-9, -10, -11).
  * An operand that is not 16-byte aligned, or whose ld or K is no multiple of
- * 8, is first copied to aligned rows in the workspace.
+ * 8, is first copied to aligned rows in the workspace if the product is large.
  */
 int hg_linear(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W, const float *bias,
               const hg_matrix *R, const hg_matrix *Y, const hg_matrix *Z, void *work, int64_t work_bytes, void *stream);

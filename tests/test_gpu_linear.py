@@ -260,4 +260,4 @@ def test_binding_refusals(hg):
     with pytest.raises(hg.HgError):
         hg.linear(X, W, X[:, :8])
     with pytest.raises(hg.HgError):
-        hg.linear(e(100, 17), e(64, 17), e(100, 64), work=e(1, 1, torch.uint8))
+        hg.linear(e(100, 8200), e(64, 8200), e(100, 64), work=e(1, 1, torch.uint8))

@@ -158,3 +158,33 @@ def test_few_rows(hg, N, K, save):
             assert want.abs().max() <= 2048               # exact in fp16
             codes, scales = hg.checkpoint8_write(want.to(F16), *hg.checkpoint8_empty(M, N))
             assert torch.equal(Z[0], codes) and torch.equal(Z[1], scales), (M, N, K)
+
+
+@pytest.mark.parametrize("t", [F16, BF16])
+@pytest.mark.parametrize("M,N,K", [(65, 64, 1), (64, 65, 7), (80, 70, 63), (333, 1111, 777), (100, 130, 65), (129, 64, 191),
+                                   (70, 333, 257), (128, 1024, 8191), (300, 257, 1537), (1000, 1000, 1001), (200, 64, 64)])
+def test_rows_at_odd_addresses(hg, M, N, K, t):
+    """Both operands at odd addresses and rows of odd length, sums of no, one and many whole stages, with slices and
+    without, NaN behind every row; with everything that follows the product."""
+    print(f"[cuts] odd {M}x{N}x{K} {t}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(M + N + K)
+
+    def odd(rows, cols):
+        ld = cols + 1 + cols % 2
+        flat = torch.full((rows * ld + 1,), float("nan"), dtype=t, device=DEV)
+        m = flat[1:].view(rows, ld)[:, :cols]
+        return m.copy_(ints(g, rows, cols))
+
+    X, W, b = odd(M, K), odd(N, K), ints(g, N)
+    R = ints(g, M, N)
+    z = torch.mm(X.float(), W.float().t()) + b
+    assert z.abs().max() < 2 ** 24
+    buf, Y = room(M, N, F32)
+    zbuf, Z = room(M, N, t)
+    hg.linear(X, W, Y, bias=b, act=1, residual=R, Z=Z)
+    assert torch.equal(Y, z.clamp(min=0) + R) and torch.equal(Z, z.to(t))
+    around(buf, M, N)
+    around(zbuf, M, N)
+    if K % 8 == 0:                                          # one operand at odd addresses, the other not
+        hg.linear(X.contiguous(), W, Y, bias=b, act=1, residual=R)
+        assert torch.equal(Y, z.clamp(min=0) + R)

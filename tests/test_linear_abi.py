@@ -55,9 +55,9 @@ BIG = 1 << 20
 @pytest.mark.parametrize("kw,code", [
     (dict(act=-1), -1), (dict(act=5), -1), (dict(M=-1), -2), (dict(M=(1 << 30) + 1), -2), (dict(N=-1), -3),
     (dict(N=BIG + 1), -3), (dict(K=-1), -4), (dict(K=BIG + 1), -4), (dict(X=NULL), -5), (dict(W=NULL), -6),
-    (dict(Y=NULL), -9), (dict(work=None, M=100, K=17, X=(P[0], 17), W=(P[1], 17)), -11),
-    (dict(work=P[6] + 8, M=100, K=17, X=(P[0], 17), W=(P[1], 17)), -11),
-    (dict(work_bytes=0, M=100, K=17, X=(P[0], 17), W=(P[1], 17)), -12),
+    (dict(Y=NULL), -9), (dict(work=None, M=100, K=8200, X=(P[0], 8200), W=(P[1], 8200)), -11),
+    (dict(work=P[6] + 8, M=100, K=8200, X=(P[0], 8200), W=(P[1], 8200)), -11),
+    (dict(work_bytes=0, M=100, K=8200, X=(P[0], 8200), W=(P[1], 8200)), -12),
     (dict(X=(None, 16)), -5), (dict(X=(P[0] + 1, 16)), -5), (dict(X=(P[0], 15)), -5), (dict(X=(P[0], (1 << 30) + 1)), -5),
     (dict(X=(P[0], 16, F32)), -5), (dict(X=(P[0], 16, E4M3)), -5), (dict(W=(P[1], 16, BF16)), -6), (dict(W=(P[1], 8)), -6),
     (dict(bias=P[2] + 2), -7), (dict(R=(P[3], 7)), -8), (dict(R=(P[3], 8, F32)), -8), (dict(Y=(P[4], 7)), -9),
@@ -66,7 +66,7 @@ BIG = 1 << 20
     (dict(Y=(P[0] + 16, 8)), -9), (dict(Y=(P[1], 8)), -9), (dict(Y=(P[2], 8)), -9), (dict(R=(P[4] + 16, 8)), -9),
     (dict(R=(P[4], 16)), -9), (dict(Z=(P[4] + 8, 8)), -10), (dict(Z=(P[0], 8)), -10),
     (dict(Z=(P[5], 8, E4M3, P[5] + 8, 1)), -10), (dict(Z=(P[5], 8, E4M3, P[4], 1)), -10),
-    (dict(M=100, K=17, X=(P[0], 17), W=(P[1], 17), work=P[4]), -11), (dict(M=100, K=17, X=(P[0], 17), W=(P[1], 17), work=P[0]), -11),
+    (dict(M=100, K=8200, X=(P[0], 8200), W=(P[1], 8200), work=P[4]), -11), (dict(M=100, K=8200, X=(P[0], 8200), W=(P[1], 8200), work=P[0]), -11),
 ])
 def test_linear_refusals(api, kw, code):
     kw = {k: mat(api, *v[:2], *(v[2:3] or (F16,)), *v[3:]) if isinstance(v, tuple) else v for k, v in kw.items()}
@@ -74,18 +74,18 @@ def test_linear_refusals(api, kw, code):
 
 
 @pytest.mark.parametrize("X,Y,Z,code", [
-    ((0, 40), (34, 40), (50, 40), -11),               # bytes: X 0..33, Y 34..49, Z 50..65 of rows of 80: none meet
-    ((0, 40), (32, 40), (50, 40), -9),                # Y on X's last column
-    ((0, 40), (66, 40), (34, 40), -9),                # Y's end on the next row's X
-    ((0, 40), (34, 40), (48, 40), -10),               # Z on Y's last column
-    ((0, 40), (34, 40), (80 * 100, 40), -11),         # behind X's last row
-    ((0, 40), (34, 40), (80 * 99 + 18, 40), -10),     # in it, on X
-    ((0, 40), (34, 41), (50, 40), -9),                # another pitch
+    ((0, 8224), (16400, 8224), (16416, 8224), -11),       # X, Y and Z: bytes 0, 16400, 16416 of rows of 16448
+    ((0, 8224), (16398, 8224), (16416, 8224), -9),        # Y on X's last column
+    ((0, 8224), (16434, 8224), (16400, 8224), -9),        # Y's end on the next row's X
+    ((0, 8224), (16400, 8224), (16414, 8224), -10),       # Z on Y's last column
+    ((0, 8224), (16400, 8224), (16448 * 100, 8224), -11),       # behind X's last row
+    ((0, 8224), (16400, 8224), (16448 * 99 + 18, 8224), -10),   # in it, on X
+    ((0, 8224), (16400, 8225), (16416, 8224), -9),        # another pitch
 ])
 def test_columns_of_one_array(api, X, Y, Z, code):
-    """M = 100, K = 17, N = 8 in 16 bits; what does not overlap goes on to the missing workspace."""
+    """M = 100, N = 8, K = 8200 in 16 bits; what does not overlap goes on to the missing workspace."""
     X, Y, Z = (mat(api, P[0] + at, ld) for at, ld in (X, Y, Z))
-    assert linear(api, M=100, K=17, X=X, W=mat(api, P[1], 17), Y=Y, Z=Z, work=None) == code
+    assert linear(api, M=100, K=8200, X=X, W=mat(api, P[1], 8200), Y=Y, Z=Z, work=None) == code
 
 
 @pytest.mark.parametrize("kw,code", [
