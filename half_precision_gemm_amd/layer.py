@@ -79,36 +79,36 @@ def _lead(t, name, types, dev):
     return ld if rows > 1 and cols else max(1, cols)
 
 
-def _matrix(t, name, types, dev):
+def _matrix(t, name, types, dev, part=""):
+    """(struct hg_matrix, shape)."""
     try:                                 # an ordinary matrix, without the checks that name what is wrong
         ld, unit = t.stride()
-        if unit == 1 and _MAX_LD >= ld >= t.shape[1] > 0 and t.get_device() == dev:
-            return Matrix(t.data_ptr(), ld, None, 0, types[t.dtype])
+        shape = t.shape
+        if unit == 1 and _MAX_LD >= ld >= shape[1] > 0 and t.get_device() == dev:
+            return Matrix(t.data_ptr(), ld, None, 0, types[t.dtype]), shape
     except (AttributeError, KeyError, TypeError, ValueError):
         pass
-    ld = _lead(t, name, types, dev)
-    return Matrix(t.data_ptr(), ld, None, 0, types[t.dtype])
+    ld = _lead(t, name + part, types, dev)
+    return Matrix(t.data_ptr(), ld, None, 0, types[t.dtype]), t.shape
 
 
 def _pair(pair, name, dev):
     if not (isinstance(pair, (tuple, list)) and len(pair) == 2):
         raise TypeError(f"{name} must be a tensor or a pair (codes, scales)")
     codes, scales = pair
-    c, s = _matrix(codes, name + "'s codes", _CODES, dev), _matrix(scales, name + "'s scales", _BYTES, dev)
-    (rows, cols), have = codes.shape, scales.shape
+    c, shape = _matrix(codes, name, _CODES, dev, "'s codes")
+    s, have = _matrix(scales, name, _BYTES, dev, "'s scales")
+    rows, cols = shape
     if have[0] != rows or have[1] != -(-cols // E4M3_BLOCK):
-        raise ValueError(f"{name}'s scales {tuple(have)} do not match codes {tuple(codes.shape)}: "
+        raise ValueError(f"{name}'s scales {tuple(have)} do not match codes {tuple(shape)}: "
                          f"expected {(rows, -(-cols // E4M3_BLOCK))}")
     c.scales, c.lds = s.data, s.ld
-    return c
+    return c, shape
 
 
 def _saved(m, name, dtype, dev):
     """(matrix, shape) of a 16-bit tensor or an 8-bit checkpoint."""
-    if isinstance(m, torch.Tensor):
-        return _matrix(m, name, _ONLY[dtype], dev), m.shape
-    d = _pair(m, name, dev)
-    return d, m[0].shape
+    return _matrix(m, name, _ONLY[dtype], dev) if isinstance(m, torch.Tensor) else _pair(m, name, dev)
 
 
 def _device(t, name):
@@ -160,9 +160,8 @@ _NO_WORK = -11              # hg_linear: a workspace is needed and there is none
 
 def _linear_operands(X, W):
     dev = _device(X, "X")
-    x = _matrix(X, "X", _HALF, dev)
-    w = _matrix(W, "W", _ONLY[X.dtype], dev)
-    (M, K), (N, k) = X.shape, W.shape
+    x, (M, K) = _matrix(X, "X", _HALF, dev)
+    w, (N, k) = _matrix(W, "W", _ONLY[X.dtype], dev)
     if k != K:
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}")
     return x, w, M, N, K, dev
@@ -189,8 +188,7 @@ def linear(X, W, Y, bias=None, act: int = 0, residual=None, Z=None, work=None):
     device tensor of at least linear_workspace_size(X, W) bytes (allocated with
     torch when None and needed)."""
     x, w, M, N, K, dev = _linear_operands(X, W)
-    y = _matrix(Y, "Y", _WIDE[X.dtype], dev)
-    shape = Y.shape
+    y, shape = _matrix(Y, "Y", _WIDE[X.dtype], dev)
     if shape[0] != M or shape[1] != N:
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}, Y {tuple(shape)}")
     r = z = b = wptr = None
@@ -198,9 +196,9 @@ def linear(X, W, Y, bias=None, act: int = 0, residual=None, Z=None, work=None):
     if bias is not None:
         b = _vector(bias, "bias", N, dev)
     if residual is not None:
-        r = _matrix(residual, "residual", _ONLY[Y.dtype], dev)
-        if residual.shape != shape:
-            raise ValueError(f"residual {tuple(residual.shape)} does not match Y {tuple(shape)}")
+        r, rshape = _matrix(residual, "residual", _ONLY[Y.dtype], dev)
+        if rshape != shape:
+            raise ValueError(f"residual {tuple(rshape)} does not match Y {tuple(shape)}")
     if Z is not None:
         z, zshape = _saved(Z, "Z", X.dtype, dev)
         if zshape != shape:
@@ -220,12 +218,10 @@ def linear(X, W, Y, bias=None, act: int = 0, residual=None, Z=None, work=None):
 
 def _grad_operands(dY, W, X):
     dev = _device(dY, "dY")
-    dy = _matrix(dY, "dY", _HALF, dev)
+    dy, (M, N) = _matrix(dY, "dY", _HALF, dev)
     w = x = K = None
-    M, N = dY.shape
     if W is not None:
-        w = _matrix(W, "W", _ONLY[dY.dtype], dev)
-        n, K = W.shape
+        w, (n, K) = _matrix(W, "W", _ONLY[dY.dtype], dev)
         if n != N:
             raise ValueError(f"shape mismatch: dY {tuple(dY.shape)}, W {tuple(W.shape)}")
     if X is not None:
@@ -266,21 +262,21 @@ def linear_grad(dY, W, X, Z=None, act: int = 0, dX=None, dW=None, dbias=None, ac
     if dX is not None:
         if W is None:
             raise ValueError("dX needs W")
-        gx = _matrix(dX, "dX", _ONLY[dY.dtype], dev)
-        if dX.shape[0] != M or dX.shape[1] != K:
-            raise ValueError(f"dX {tuple(dX.shape)} does not match {(M, K)}")
+        gx, shape = _matrix(dX, "dX", _ONLY[dY.dtype], dev)
+        if shape[0] != M or shape[1] != K:
+            raise ValueError(f"dX {tuple(shape)} does not match {(M, K)}")
     if dW is not None:
         if X is None:
             raise ValueError("dW needs X")
-        gw = _matrix(dW, "dW", _WIDE[dY.dtype], dev)
-        if dW.shape[0] != N or dW.shape[1] != K:
-            raise ValueError(f"dW {tuple(dW.shape)} does not match {(N, K)}")
+        gw, shape = _matrix(dW, "dW", _WIDE[dY.dtype], dev)
+        if shape[0] != N or shape[1] != K:
+            raise ValueError(f"dW {tuple(shape)} does not match {(N, K)}")
     if dbias is not None:
         gb = _vector(dbias, "dbias", N, dev)
     if Z is not None:
         z, shape = _saved(Z, "Z", dY.dtype, dev)
-        if shape != dY.shape:
-            raise ValueError(f"Z {tuple(shape)} does not match dY {tuple(dY.shape)}")
+        if shape[0] != M or shape[1] != N:
+            raise ValueError(f"Z {tuple(shape)} does not match dY {(M, N)}")
     elif act != 0:
         raise ValueError("the activation's gradient needs Z")
     if work is None:
@@ -301,10 +297,10 @@ def checkpoint8_empty(M: int, N: int, device="cuda"):
 
 def _checkpoint(X, codes, scales):
     dev = _device(X, "X")
-    x, c = _matrix(X, "X", _HALF, dev), _pair((codes, scales), "the checkpoint", dev)
-    if codes.shape != X.shape:
-        raise ValueError(f"codes {tuple(codes.shape)} do not match X {tuple(X.shape)}")
-    return x, c, *X.shape, dev
+    (x, shape), (c, have) = _matrix(X, "X", _HALF, dev), _pair((codes, scales), "the checkpoint", dev)
+    if have != shape:
+        raise ValueError(f"codes {tuple(have)} do not match X {tuple(shape)}")
+    return x, c, *shape, dev
 
 
 def checkpoint8_write(X, codes, scales):
