@@ -168,11 +168,14 @@ double expected_us(int64_t cus, int tile, const Shape &p, int64_t whole, int s)
     return 2.0 + (double)((whole + r.slots - 1) / r.slots) * one + (double)((rest * s + r.slots - 1) / r.slots) * part +
            reduce_us(rest, tile, s);
 }
-// Two products in one launch, their sums in sa and sb slices.
+// Two products in one launch, their sums in sa and sb slices.  128×128 tiles
+// take 6.0 + 0.62 there: a k-major operand takes twice the LDS reads (64×64 /
+// 128×128, M × N × K: 4000×500×700 33.6 / 39.8 us, 900×900×2500 38.7 / 43.0,
+// 777×1000×1304 26.6 / 25.5, 2048×2048×2048 80.9 / 63.8).
 double expected_us(int64_t cus, int tile, const Shape &a, int sa, const Shape &b, int sb)
 {
     const int64_t na = a.tiles(tile) * sa, nb = b.tiles(tile) * sb, items = na + nb;
-    const Rate r = rate_of(cus, tile, items);
+    const Rate r = tile == 128 ? Rate{6.0, 0.62, cus} : rate_of(cus, tile, items);
     const double ta = r.fix + r.stage * (double)((a.stages() + sa - 1) / sa);
     const double tb = r.fix + r.stage * (double)((b.stages() + sb - 1) / sb);
     // Equal items go in rounds; unequal ones fill up after each other.
