@@ -21,7 +21,7 @@ SOURCES = [os.path.join(CSRC, "hg_api.cpp"), os.path.join(CSRC, "hg_kernels.hip"
            os.path.join(CSRC, "hg_noalloc.hip"), os.path.join(CSRC, "hg_linear_api.cpp"),
            os.path.join(CSRC, "hg_linear_ring.hip"), os.path.join(CSRC, "hg_linear_rows.hip"),
            os.path.join(CSRC, "hg_linear_tile.hip"), os.path.join(CSRC, "hg_linear_rowwise.hip"),
-           os.path.join(CSRC, "hg_linear_loose.hip")]
+           os.path.join(CSRC, "hg_linear_loose.hip"), os.path.join(CSRC, "hg_linear_outer.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

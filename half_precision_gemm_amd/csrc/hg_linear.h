@@ -73,6 +73,7 @@ hipError_t launch_ring(const Product &p, int tile, bool bf16, hipStream_t s);   
 hipError_t launch_loose(const Product &p, bool bf16, hipStream_t s);                        // 64, any A and B; NN
 // x (NT) and w (TT), either of them null, and the strips' sums in one launch.
 hipError_t launch_ring_pair(const Product *x, const Product *w, const Strips &b, int tile, bool bf16, hipStream_t s);
+hipError_t launch_outer(const Product &p, bool bf16, hipStream_t s);                        // K <= kFewRows; TT
 hipError_t launch_tile(const Product &p, Layout l, bool bf16, hipStream_t s);               // 256
 // M <= kFewRows, NN; direct: A and B as Product says.
 hipError_t launch_rowwise(const Product &p, bool direct, bool bf16, hipStream_t s);
@@ -781,7 +782,11 @@ __device__ __forceinline__ void stage_get(const unsigned char *s, int row, int u
 // decided once per block, not per row.  The residual of the next block is
 // requested before this block's stores, because the counter of vector memory
 // operations retires in order: a load issued after them would wait for them.
-template <int EDGE, int W, bool BF16>
+//
+// PAST: what is written passes the caches by.  A large product's results are
+// more than they hold, and they hold its operands (256×256 tiles, 4096×8192×
+// 2048: gradient 272 -> 263 us; with Z 8192×16384×4096 823 -> 817).
+template <int EDGE, int W, bool BF16, bool PAST = EDGE == 256>
 struct Drain {
     static constexpr int UNITS = W / 8, ROWS = 64 / UNITS;      // lanes per row, rows per pass
     static constexpr int PASSES = 16 / ROWS;
@@ -797,13 +802,10 @@ struct Drain {
     {
         load_bias(p.f, c0 + 8 * (lane % UNITS), bias);
     }
-    // What 256×256 tiles write passes the caches by: such a product's results
-    // are more than they hold, and they hold its operands (4096×8192×2048:
-    // gradient 272 -> 263 us; with Z 8192×16384×4096 823 -> 817).
     template <class V, class U>
     __device__ __forceinline__ void put(void *to, U v) const
     {
-        if constexpr (EDGE == 256)
+        if constexpr (PAST)
             __builtin_nontemporal_store((V)v, static_cast<V *>(to));
         else
             *static_cast<V *>(to) = v;

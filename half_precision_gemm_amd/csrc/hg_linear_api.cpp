@@ -235,6 +235,16 @@ Cut best_cut(const Shape &p, double *us = nullptr)
         *us = least;
     return best;
 }
+// Whether a weight's gradient (b: its rows, its columns, the rows it is summed
+// over) is written along its rows (hg_linear_outer.hip) in a launch of its own:
+// few rows, and many more tiles than the GPU takes at once (gradients, tiles of
+// 64×64 / along the rows, us: 60×3840×1336, 1260 tiles, 22.9 / 24.2,
+// 2×512×16384, 2048, 24.8 / 16.7, 16×4096×4096 32.4 / 27.2, 3×2644×13440 62.3 /
+// 44.4, 8×8192×8192 85.8 / 66.9).
+bool along_rows(const Shape &b)
+{
+    return b.K <= lin::kFewRows && b.tiles(64) > 6 * (int64_t)hg::cu_count();
+}
 // Two products: each on its own if either is best on 256×256 tiles, else
 // together on one smaller edge.  (One launch for 256×256 tiles of both kinds
 // was slower: side by side they share less in L2, 8192×2048 with 4096 rows
@@ -244,6 +254,10 @@ void best_cuts(const Shape &a, const Shape &b, Cut &ca, Cut &cb)
     const int64_t cus = hg::cu_count();
     double ua, ub;
     ca = best_cut(a, &ua);
+    if (along_rows(b)) {
+        cb = {0, 0, 1, 0};
+        return;
+    }
     cb = best_cut(b, &ub);
     double least = ca.tile == 256 || cb.tile == 256 ? ua + ub : -1.0;
     for (int tile : {64, 128})
@@ -411,7 +425,7 @@ GradRoom room_grad(Arena &a, int64_t M, int64_t N, int64_t K, const hg_matrix *W
     else if (W != nullptr)
         r.cx = best_cut(x);
     else if (X != nullptr)
-        r.cw = best_cut(w);
+        r.cw = along_rows(w) ? Cut{0, 0, 1, 0} : best_cut(w);
     r.copy_w = W != nullptr && !direct(W, K);
     r.copy_x = X != nullptr && (X->type == HG_E4M3 || !direct(X, K));
     const int64_t strips = M > 0 ? (M + strip_of(M, N) - 1) / strip_of(M, N) : 0;
@@ -683,10 +697,14 @@ int hg_linear_grad(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *dY
         set_cut(pw, room.cw, room.pw);
     }
     const bool big_x = do_x && room.cx.tile == 256, big_w = do_w && room.cw.tile == 256;
-    const int edge = do_x && !big_x ? room.cx.tile : do_w && !big_w ? room.cw.tile : 64;
-    if (const hipError_t e = lin::launch_ring_pair(do_x && !big_x ? &px : nullptr, do_w && !big_w ? &pw : nullptr, b,
-                                                   edge, bf16, s))
+    const bool outer = do_w && room.cw.tile == 0, pair_w = do_w && !big_w && !outer;
+    const int edge = do_x && !big_x ? room.cx.tile : pair_w ? room.cw.tile : 64;
+    const lin::Product *one = do_x && !big_x ? &px : nullptr, *two = pair_w ? &pw : nullptr;
+    if (const hipError_t e = lin::launch_ring_pair(one, two, b, edge, bf16, s))
         return status_of(e);
+    if (outer)
+        if (const hipError_t e = lin::launch_outer(pw, bf16, s))
+            return status_of(e);
     if (big_x)
         if (const hipError_t e = lin::launch_tile(px, lin::Layout::NT, bf16, s))
             return status_of(e);

@@ -188,3 +188,26 @@ def test_rows_at_odd_addresses(hg, M, N, K, t):
     if K % 8 == 0:                                          # one operand at odd addresses, the other not
         hg.linear(X.contiguous(), W, Y, bias=b, act=1, residual=R)
         assert torch.equal(Y, z.clamp(min=0) + R)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("out", [F16, F32])
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (7, 130, 60000), (64, 2000, 5000), (33, 4100, 1928), (16, 40000, 200),
+                                   (2, 33000, 136), (63, 64, 100000), (9, 8256, 1000)])
+def test_weight_of_few_rows(hg, M, N, K, out, accumulate):
+    """dW of few rows: runs of one and many tiles, a last one that is not whole, more strips than places."""
+    print(f"[cuts] weight {M}x{N}x{K} {out} {accumulate}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(M + N + K)
+    X, dY = ints(g, M, K), ints(g, M, N)
+    buf, dW = room(N, K, out)
+    old = ints(g, N, K)
+    dW.copy_(old)
+    db = torch.empty(N, device=DEV)
+    want = torch.mm(dY.t().contiguous(), X) + (old if accumulate else 0)
+    assert want.abs().max() <= 2048                       # exact in fp16
+    t = F16 if out is F16 else BF16
+    hg.linear_grad(dY.to(t), None, X.to(t), dW=dW, dbias=None if accumulate else db, accumulate=accumulate)
+    assert torch.equal(dW.float(), want)
+    around(buf, N, K)
+    if not accumulate:
+        assert torch.equal(db, dY.sum(0))
