@@ -118,6 +118,17 @@ hipError_t launch_zero(void *C, int64_t ldc, int64_t rows, int64_t cols, bool wi
 
 #if defined(__HIPCC__)
 
+// A launch whose own status is returned (not what an earlier call left).
+template <class... P, class... A>
+hipError_t start(void (*kernel)(P...), int64_t blocks, int threads, hipStream_t s, const A &...a)
+{
+    return [&](P... p) {
+        void *args[] = {const_cast<void *>(static_cast<const void *>(&p))...};
+        return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3((unsigned)blocks), dim3((unsigned)threads),
+                               args, 0, s);
+    }(a...);
+}
+
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));

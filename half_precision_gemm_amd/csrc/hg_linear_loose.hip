@@ -160,11 +160,7 @@ hipError_t launch_loose(const Product &p, bool bf16, hipStream_t s)
     if (total > 0x7fffffff)
         return hipErrorInvalidConfiguration;
     const Spread w{(int)tm, (int)tn, (int)total};
-    if (bf16)
-        hipLaunchKernelGGL((linear_loose_kernel<true>), dim3((unsigned)total), dim3(THREADS), 0, s, p, w);
-    else
-        hipLaunchKernelGGL((linear_loose_kernel<false>), dim3((unsigned)total), dim3(THREADS), 0, s, p, w);
-    return hipGetLastError();
+    return start(bf16 ? linear_loose_kernel<true> : linear_loose_kernel<false>, total, THREADS, s, p, w);
 }
 
 }  // namespace lin

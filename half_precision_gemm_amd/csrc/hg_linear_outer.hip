@@ -135,13 +135,8 @@ hipError_t launch_outer(const Product &p, bool bf16, hipStream_t s)
         return hipSuccess;
     if (total > 0x7fffffff)
         return hipErrorInvalidConfiguration;
-    if (bf16)
-        hipLaunchKernelGGL((linear_outer_kernel<true>), dim3((unsigned)total), dim3(THREADS), 0, s, p, (int)tn,
-                           (int)group, (int)groups);
-    else
-        hipLaunchKernelGGL((linear_outer_kernel<false>), dim3((unsigned)total), dim3(THREADS), 0, s, p, (int)tn,
-                           (int)group, (int)groups);
-    return hipGetLastError();
+    return start(bf16 ? linear_outer_kernel<true> : linear_outer_kernel<false>, total, THREADS, s, p, (int)tn, (int)group,
+                 (int)groups);
 }
 
 }  // namespace lin

@@ -226,11 +226,8 @@ hipError_t launch(const Product &p, hipStream_t s)
         return hipSuccess;
     if (total > 0x7fffffff)
         return hipErrorInvalidConfiguration;
-    if (p.K % BK != 0)
-        hipLaunchKernelGGL((linear_ring_kernel<EDGE, true, BF16>), dim3((unsigned)total), dim3(THREADS), 0, s, p, w);
-    else
-        hipLaunchKernelGGL((linear_ring_kernel<EDGE, false, BF16>), dim3((unsigned)total), dim3(THREADS), 0, s, p, w);
-    return hipGetLastError();
+    return start(p.K % BK != 0 ? linear_ring_kernel<EDGE, true, BF16> : linear_ring_kernel<EDGE, false, BF16>, total,
+                 THREADS, s, p, w);
 }
 
 template <int EDGE, bool BF16>
@@ -247,13 +244,8 @@ hipError_t launch_pair(const Product *x, const Product *y, const Strips &b, hipS
         return hipErrorInvalidConfiguration;
     const int y_first = py.per > px.per;
     // (both k-major: the buffer's range ends the sum)
-    if (px.K % BK != 0)
-        hipLaunchKernelGGL((linear_ring_pair_kernel<EDGE, true, BF16>), dim3((unsigned)total), dim3(THREADS), 0, s, px,
-                           py, b, wx, wy, y_first);
-    else
-        hipLaunchKernelGGL((linear_ring_pair_kernel<EDGE, false, BF16>), dim3((unsigned)total), dim3(THREADS), 0, s, px,
-                           py, b, wx, wy, y_first);
-    return hipGetLastError();
+    return start(px.K % BK != 0 ? linear_ring_pair_kernel<EDGE, true, BF16> : linear_ring_pair_kernel<EDGE, false, BF16>,
+                 total, THREADS, s, px, py, b, wx, wy, y_first);
 }
 
 }  // namespace

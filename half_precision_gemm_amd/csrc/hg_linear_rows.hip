@@ -238,54 +238,38 @@ hipError_t prepare(const Slope &g, const Copy &x, const Copy &w, hipStream_t s)
     if (total > 0x7fffffff)
         return hipErrorInvalidConfiguration;
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)total), dim3(THREADS), 0, s, g, x, w, (int)(tiles > 0 ? tiles : 1),
-                           (int)slopes, xb, wb);
+        return start(kernel, total, THREADS, s, g, x, w, (int)(tiles > 0 ? tiles : 1), (int)slopes, xb, wb);
     };
     const bool e = g.save == kSave8;
     switch (g.act) {
-    case kRelu: e ? go(prepare_kernel<BF16, kRelu, kSave8>) : go(prepare_kernel<BF16, kRelu, kSave16>); break;
-    case kGelu: e ? go(prepare_kernel<BF16, kGelu, kSave8>) : go(prepare_kernel<BF16, kGelu, kSave16>); break;
-    case kGeluTanh: e ? go(prepare_kernel<BF16, kGeluTanh, kSave8>) : go(prepare_kernel<BF16, kGeluTanh, kSave16>); break;
-    case kSilu: e ? go(prepare_kernel<BF16, kSilu, kSave8>) : go(prepare_kernel<BF16, kSilu, kSave16>); break;
-    default: go(prepare_kernel<BF16, kNone, kSave16>); break;
+    case kRelu: return go(e ? prepare_kernel<BF16, kRelu, kSave8> : prepare_kernel<BF16, kRelu, kSave16>);
+    case kGelu: return go(e ? prepare_kernel<BF16, kGelu, kSave8> : prepare_kernel<BF16, kGelu, kSave16>);
+    case kGeluTanh: return go(e ? prepare_kernel<BF16, kGeluTanh, kSave8> : prepare_kernel<BF16, kGeluTanh, kSave16>);
+    case kSilu: return go(e ? prepare_kernel<BF16, kSilu, kSave8> : prepare_kernel<BF16, kSilu, kSave16>);
+    default: return go(prepare_kernel<BF16, kNone, kSave16>);
     }
-    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_zero(void *C, int64_t ldc, int64_t rows, int64_t cols, bool wide, hipStream_t s)
 {
-    const dim3 grid((unsigned)blocks_for(rows * cols));
-    if (wide)
-        hipLaunchKernelGGL((zero_kernel<true>), grid, dim3(THREADS), 0, s, C, ldc, rows, cols);
-    else
-        hipLaunchKernelGGL((zero_kernel<false>), grid, dim3(THREADS), 0, s, C, ldc, rows, cols);
-    return hipGetLastError();
+    return start(wide ? zero_kernel<true> : zero_kernel<false>, blocks_for(rows * cols), THREADS, s, C, ldc, rows, cols);
 }
 
 hipError_t launch_write8(const void *X, int64_t ldx, uint8_t *C, int64_t ldc, uint8_t *S, int64_t lds, int64_t rows,
                          int64_t cols, bool bf16, hipStream_t s)
 {
-    const dim3 grid((unsigned)blocks_for(rows * ((cols + kBlock8 - 1) / kBlock8 * 4)));
-    const uint16_t *x = static_cast<const uint16_t *>(X);
-    if (bf16)
-        hipLaunchKernelGGL((write8_kernel<true>), grid, dim3(THREADS), 0, s, x, ldx, C, ldc, S, lds, rows, cols);
-    else
-        hipLaunchKernelGGL((write8_kernel<false>), grid, dim3(THREADS), 0, s, x, ldx, C, ldc, S, lds, rows, cols);
-    return hipGetLastError();
+    const int blocks = blocks_for(rows * ((cols + kBlock8 - 1) / kBlock8 * 4));
+    return start(bf16 ? write8_kernel<true> : write8_kernel<false>, blocks, THREADS, s, static_cast<const uint16_t *>(X),
+                 ldx, C, ldc, S, lds, rows, cols);
 }
 
 hipError_t launch_read8(const uint8_t *C, int64_t ldc, const uint8_t *S, int64_t lds, void *X, int64_t ldx, int64_t rows,
                         int64_t cols, bool bf16, hipStream_t s)
 {
-    const dim3 grid((unsigned)blocks_for(rows * ((cols + 7) / 8)));
-    uint16_t *x = static_cast<uint16_t *>(X);
-    if (bf16)
-        hipLaunchKernelGGL((read8_kernel<true>), grid, dim3(THREADS), 0, s, C, ldc, S, lds, x, ldx, rows, cols);
-    else
-        hipLaunchKernelGGL((read8_kernel<false>), grid, dim3(THREADS), 0, s, C, ldc, S, lds, x, ldx, rows, cols);
-    return hipGetLastError();
+    return start(bf16 ? read8_kernel<true> : read8_kernel<false>, blocks_for(rows * ((cols + 7) / 8)), THREADS, s, C, ldc, S,
+                 lds, static_cast<uint16_t *>(X), ldx, rows, cols);
 }
 
 hipError_t launch_prepare(const Slope &g, const Copy &x, const Copy &w, bool bf16, hipStream_t s)
@@ -310,13 +294,8 @@ hipError_t launch_reduce(const Product *p, const Product *q, bool bf16, hipStrea
     const Product none{};
     if (pb + qb == 0)
         return hipSuccess;
-    if (bf16)
-        hipLaunchKernelGGL((reduce_kernel<true>), dim3((unsigned)(pb + qb)), dim3(THREADS), 0, s, p ? *p : none,
-                           q ? *q : none, wp, wq, pb, qb);
-    else
-        hipLaunchKernelGGL((reduce_kernel<false>), dim3((unsigned)(pb + qb)), dim3(THREADS), 0, s, p ? *p : none,
-                           q ? *q : none, wp, wq, pb, qb);
-    return hipGetLastError();
+    return start(bf16 ? reduce_kernel<true> : reduce_kernel<false>, pb + qb, THREADS, s, p ? *p : none, q ? *q : none, wp, wq,
+                 pb, qb);
 }
 
 }  // namespace lin

@@ -282,25 +282,18 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const Product
 }
 
 template <int NB, int MB, bool BF16>
-void launch(const Product &p, bool stream, hipStream_t s)
+hipError_t launch(const Product &p, bool stream, hipStream_t s)
 {
-    const dim3 grid((unsigned)((p.N + 16 * NB - 1) / (16 * NB)));
-    if (stream)
-        hipLaunchKernelGGL((linear_stream_kernel<NB, MB, BF16>), grid, dim3(THREADS), 0, s, p);
-    else
-        hipLaunchKernelGGL((linear_rowwise_kernel<NB, MB, BF16>), grid, dim3(THREADS), 0, s, p);
+    return start(stream ? linear_stream_kernel<NB, MB, BF16> : linear_rowwise_kernel<NB, MB, BF16>,
+                 (p.N + 16 * NB - 1) / (16 * NB), THREADS, s, p);
 }
 
 template <int NB, bool BF16>
 hipError_t launch(const Product &p, bool stream, hipStream_t s)
 {
-    if (p.M <= 16)
-        launch<NB, 1, BF16>(p, stream, s);
-    else if (p.M <= 32)
-        launch<NB, 2, BF16>(p, stream, s);
-    else
-        launch<NB, 4, BF16>(p, stream, s);
-    return hipGetLastError();
+    return p.M <= 16   ? launch<NB, 1, BF16>(p, stream, s)
+           : p.M <= 32 ? launch<NB, 2, BF16>(p, stream, s)
+                       : launch<NB, 4, BF16>(p, stream, s);
 }
 
 }  // namespace

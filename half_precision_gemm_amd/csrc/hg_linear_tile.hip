@@ -252,13 +252,9 @@ hipError_t launch(const Product &p, hipStream_t s)
     grid = grid / 8 * 8 > 0 ? grid / 8 * 8 : grid;
     if (grid > total)
         grid = total;
-    if (!(TA && TB) && p.K % kStage != 0)
-        hipLaunchKernelGGL((linear_tile_kernel<TA, TB, !(TA && TB), BF16>), dim3((unsigned)grid), dim3(THREADS), 0, s, p,
-                           w);
-    else
-        hipLaunchKernelGGL((linear_tile_kernel<TA, TB, false, BF16>), dim3((unsigned)grid), dim3(THREADS), 0, s, p,
-                           w);
-    return hipGetLastError();
+    return start(!(TA && TB) && p.K % kStage != 0 ? linear_tile_kernel<TA, TB, !(TA && TB), BF16>
+                                                  : linear_tile_kernel<TA, TB, false, BF16>,
+                 grid, THREADS, s, p, w);
 }
 
 }  // namespace

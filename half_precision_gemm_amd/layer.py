@@ -112,9 +112,11 @@ def _saved(m, name, dtype, dev):
 
 
 def _device(t, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    return t.get_device() if t.is_cuda else None       # _lead refuses the host's by name
+    try:
+        dev = t.get_device()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    return dev if dev >= 0 else None                   # _lead refuses the host's by name
 
 
 def _vector(v, name, n, dev):

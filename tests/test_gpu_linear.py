@@ -1,5 +1,7 @@
 """hg_linear: Y = act(X·Wᵀ + bias) + R with the pre-activation saved in 16 or 8
 bits, against 64 bits (linear_ref.py: definitions and bounds)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -244,6 +246,22 @@ def test_row_of_a_wide_array(hg):
     Y = torch.empty(1, 32, dtype=F16, device=DEV)
     hg.linear(X, torch.ones(32, 64, dtype=F16, device=DEV), Y)
     assert (Y == 64).all()
+
+
+def test_an_error_that_another_call_left_is_not_reported(hg):
+    """An earlier HIP call's error stays with it: the launches' own status is what counts."""
+    hip = ctypes.CDLL(hg.LIB_PATH)                        # the runtime that the library is linked to
+    X = torch.ones(4, 64, dtype=F16, device=DEV)
+    W, Y = torch.ones(64, 64, dtype=F16, device=DEV), torch.empty(4, 64, dtype=F16, device=DEV)
+    dW, pair = torch.empty_like(W), hg.checkpoint8_empty(4, 64)
+    work = hg.linear_grad_workspace(Y, W, X)
+    for call in (lambda: hg.linear(X, W, Y), lambda: hg.checkpoint8_write(X, *pair),
+                 lambda: hg.linear_grad(Y, W, X, dW=dW, work=work)):
+        assert hip.hipSetDevice(9999) != 0
+        call()
+        hip.hipGetLastError()
+    torch.cuda.synchronize()
+    assert (Y == 64).all() and (dW == 256).all()
 
 
 def test_binding_refusals(hg):
