@@ -45,7 +45,7 @@ struct Finish {
 // One product: C[rows×cols] = Σ_k A(i, k)·B(j, k).  An operand is stored
 // either k-contiguous (A[i·lda + k]) or, TA / TB, k-major (A[k·lda + i]).
 struct Product {
-    const uint16_t *A, *B;        // 16-byte aligned, lda and ldb multiples of 8 (not so row-wise)
+    const uint16_t *A, *B;        // 16-byte aligned, lda and ldb multiples of 8 (not so through registers)
     int64_t lda, ldb;
     int32_t M, N, K;              // rows, cols, length of the sum
     // The first `whole` tiles (edge×edge, in the order of tile_at) are computed
@@ -57,7 +57,7 @@ struct Product {
     Finish f;
 };
 
-constexpr int kFewRows = 64;      // rows that the row-wise product takes
+constexpr int kFewRows = 64;      // rows that the forms for few rows take
 
 enum class Layout { NN, NT, TT };   // (TA, TB) = (0, 0), (0, 1), (1, 1)
 

@@ -115,7 +115,7 @@ struct Arena {
     }
 };
 
-// How a product is cut: the tile edge (0: the row-wise product), the tiles that
+// How a product is cut: the tile edge (0: the forms for few rows), the tiles that
 // are computed in one piece, and the slices of the others' sums.
 struct Cut {
     int tile;
