@@ -75,8 +75,8 @@ hipError_t launch_loose(const Product &p, bool bf16, hipStream_t s);            
 hipError_t launch_ring_pair(const Product *x, const Product *w, const Strips &b, int tile, bool bf16, hipStream_t s);
 hipError_t launch_outer(const Product &p, bool bf16, hipStream_t s);                        // K <= kFewRows; TT
 hipError_t launch_tile(const Product &p, Layout l, bool bf16, hipStream_t s);               // 256
-// M <= kFewRows, NN; direct: A and B as Product says.
-hipError_t launch_rowwise(const Product &p, bool direct, bool bf16, hipStream_t s);
+// M <= kFewRows, NN; direct: A and B as Product says, odd: rows at odd elements.
+hipError_t launch_rowwise(const Product &p, bool direct, bool odd, bool bf16, hipStream_t s);
 // The slices' partial sums of one or two products (either may be null).
 hipError_t launch_reduce(const Product *p, const Product *q, bool bf16, hipStream_t s);
 
@@ -387,6 +387,37 @@ __device__ __forceinline__ uint16_t narrow(float v)
     else
         return __builtin_bit_cast(uint16_t, (_Float16)v);
 }
+
+// Eight 16-bit elements from p on: loaded, and taken later.  ODD: p
+// may be at an odd element, where a wide load takes three times as long (4×2112
+// ×2727 12.8 us, with 2726 6.9): then the aligned words around them are loaded
+// and shifted into place.  (The word at either end holds one more element, which
+// is not used, and lies in one page with them.)
+template <bool ODD>
+struct Raw {
+    u32x4 w;
+    __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const u32x4_any *>(p); }
+    __device__ __forceinline__ u32x4 get(const uint16_t *) const { return w; }
+};
+template <>
+struct Raw<true> {
+    u32x4 w;
+    uint32_t next;
+    __device__ __forceinline__ void load(const uint16_t *p)
+    {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), odd = a >> 1 & 1;
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(a - 2 * odd);
+        w = *reinterpret_cast<const u32x4_any *>(q);
+        next = q[3 + odd];
+    }
+    // p: as for load, or that plus an even number of elements.
+    __device__ __forceinline__ u32x4 get(const uint16_t *p) const
+    {
+        const uint32_t shift = ((uint32_t)reinterpret_cast<uintptr_t>(p) & 2) * 8;
+        return u32x4{__builtin_amdgcn_alignbit(w[1], w[0], shift), __builtin_amdgcn_alignbit(w[2], w[1], shift),
+                     __builtin_amdgcn_alignbit(w[3], w[2], shift), __builtin_amdgcn_alignbit(next, w[3], shift)};
+    }
+};
 
 // The 16-bit elements p[0 .. n-1] of eight, the others 0 (n may pass 8, or be
 // none).  Short of eight, every load takes an index that is there, so that

@@ -103,6 +103,13 @@ bool direct(const hg_matrix *m, int64_t cols)
            (reinterpret_cast<uintptr_t>(m->data) & 15) == 0;
 }
 
+// Whether a row of a 16-bit matrix may begin at an address that no 32-bit word
+// begins at.
+bool odd_rows(const hg_matrix *m, int64_t rows)
+{
+    return (reinterpret_cast<uintptr_t>(m->data) & 3) != 0 || (rows > 1 && m->ld % 2 != 0);
+}
+
 // Bump allocation of 256-byte multiples; with a null base it only counts.
 struct Arena {
     char *base;
@@ -356,7 +363,7 @@ bool row_by_row(int64_t M, int64_t N, int64_t K, bool copy_x, bool copy_w, doubl
 
 struct LinearPlan {
     bool copy_x, copy_w;
-    bool direct, loose;               // both operands direct; taken as they are by 64×64 tiles
+    bool direct, loose, odd;          // both operands direct; taken as they are by 64×64 tiles; rows at odd elements
     Cut cut;
 };
 LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W)
@@ -366,6 +373,7 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
     q.copy_x = !direct(X, K);
     q.copy_w = !direct(W, K);
     q.direct = !q.copy_x && !q.copy_w;
+    q.odd = odd_rows(X, M) || odd_rows(W, N);
     q.cut = best_cut({M, N, K}, &us);
     // 64×64 tiles take operands that would have to be copied as they are: the
     // slower loop costs less than the launch (copied / as they are, us:
@@ -539,7 +547,7 @@ int hg_linear(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
     }
     if (const hipError_t e = lin::launch_prepare(lin::Slope{}, cx, cw, bf16, s))
         return status_of(e);
-    const hipError_t e = q.cut.tile == 0     ? lin::launch_rowwise(p, q.direct, bf16, s)
+    const hipError_t e = q.cut.tile == 0     ? lin::launch_rowwise(p, q.direct, q.odd, bf16, s)
                          : q.loose            ? lin::launch_loose(p, bf16, s)
                          : q.cut.tile == 256 ? lin::launch_tile(p, lin::Layout::NN, bf16, s)
                                              : lin::launch_ring(p, q.cut.tile, bf16, s);

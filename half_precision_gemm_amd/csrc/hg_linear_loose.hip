@@ -11,6 +11,8 @@
 //    two 16-byte pieces of either operand, eight neighbours 128 bytes of a row.
 //    DEPTH stages are in flight in registers, the compiler's own counting waits
 //    for the oldest only; two LDS slots, one barrier per stage.
+//    (Rows at odd elements loaded as aligned words and shifted, as the forms for
+//    few rows do: 333×1111×777 9.3 -> 11.4 us, not here.)
 //  * Rows past the last are read as the last row and their results dropped.
 //  * The end of the sum that is no whole stage comes first: its loads are in
 //    flight together with the first whole stages'.

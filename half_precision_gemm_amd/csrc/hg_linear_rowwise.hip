@@ -58,8 +58,8 @@ __device__ __forceinline__ void finish_sums(const Product &p, float (*part)[MB *
     finish8<BF16>(p.f, row, n0 + c, v, bias);
 }
 
-// NB blocks of 16 rows of W, MB blocks of 16 rows of X, at any address and of
-// any length.  W goes from memory straight to registers in the matrix core's
+// NB blocks of 16 rows of W, MB blocks of 16 rows of X, at any address (ODD: odd
+// elements too) and of any length.  W goes from memory straight to registers in the matrix core's
 // operand layout (lane l: row l mod 16, 8 k from 8·(l div 16) on: one 16-byte
 // load, which global memory takes at any even address), X likewise from L2;
 // nothing is staged, there is no barrier in the loop, and a wave has DEPTH
@@ -67,7 +67,11 @@ __device__ __forceinline__ void finish_sums(const Product &p, float (*part)[MB *
 // read as the last row and their results dropped; a last piece of less than 64
 // k is loaded element by element (requested before the others, or as the row's
 // last eight with those before masked: no gain).
-template <int NB, int MB, bool BF16>
+template <int NB, int MB, bool ODD>
+struct Pieces {
+    Raw<ODD> w[NB][2], x[MB][2];
+};
+template <int NB, int MB, bool ODD, bool BF16>
 __global__ void __launch_bounds__(THREADS, 1) linear_rowwise_kernel(const Product p)
 {
     constexpr int DEPTH = NB * 2 + MB * 2 <= 4 ? 4 : NB * 2 + MB * 2 <= 8 ? 2 : 1;
@@ -90,29 +94,28 @@ __global__ void __launch_bounds__(THREADS, 1) linear_rowwise_kernel(const Produc
 #pragma unroll
         for (int j = 0; j < NB; ++j)
             acc[i][j] = floatx4{0, 0, 0, 0};
-    struct Piece {
-        half8 w[NB][2], x[MB][2];
-    };
+    using Piece = Pieces<NB, MB, ODD>;
     auto load = [&](int piece, Piece &q) __attribute__((always_inline)) {
         const int k = piece * PIECE + 8 * fhi;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
-                q.w[b][s] = __builtin_bit_cast(half8, *reinterpret_cast<const u32x4_any *>(w[b] + k + 32 * s));
+                q.w[b][s].load(w[b] + k + 32 * s);
 #pragma unroll
             for (int b = 0; b < MB; ++b)
-                q.x[b][s] = __builtin_bit_cast(half8, *reinterpret_cast<const u32x4_any *>(x[b] + k + 32 * s));
+                q.x[b][s].load(x[b] + k + 32 * s);
         }
     };
-    auto multiply = [&](const Piece &q) __attribute__((always_inline)) {
+    auto multiply = [&](const auto &q) __attribute__((always_inline)) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int i = 0; i < MB; ++i)
 #pragma unroll
                 for (int j = 0; j < NB; ++j)
-                    acc[i][j] = mfma_16x16x32<BF16>(q.w[j][s], q.x[i][s], acc[i][j]);
+                    acc[i][j] = mfma_16x16x32<BF16>(__builtin_bit_cast(half8, q.w[j][s].get(w[j])),
+                                                    __builtin_bit_cast(half8, q.x[i][s].get(x[i])), acc[i][j]);
     };
     // This wave's whole pieces: wave, wave + 8, ..; groups of DEPTH, the next
     // group's loads in flight over this one's products.
@@ -130,6 +133,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_rowwise_kernel(const Produc
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d)
             load(next(), g[d]);
+        __builtin_amdgcn_sched_barrier(0);                        // all of them before the products that follow
     };
     auto use = [&](const Piece (&g)[DEPTH]) __attribute__((always_inline)) {
 #pragma unroll
@@ -160,16 +164,16 @@ __global__ void __launch_bounds__(THREADS, 1) linear_rowwise_kernel(const Produc
     }
     // The rest of the sum, by the wave whose turn it is.
     if (K % PIECE != 0 && whole % WAVES == wave) {
-        Piece q;
+        Pieces<NB, MB, false> q;
         const int k = whole * PIECE + 8 * fhi;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
 #pragma unroll
             for (int j = 0; j < NB; ++j)
-                q.w[j][s] = __builtin_bit_cast(half8, load16x8(w[j] + k + 32 * s, K - k - 32 * s));
+                q.w[j][s].w = load16x8(w[j] + k + 32 * s, K - k - 32 * s);
 #pragma unroll
             for (int i = 0; i < MB; ++i)
-                q.x[i][s] = __builtin_bit_cast(half8, load16x8(x[i] + k + 32 * s, K - k - 32 * s));
+                q.x[i][s].w = load16x8(x[i] + k + 32 * s, K - k - 32 * s);
         }
         multiply(q);
     }
@@ -282,31 +286,33 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const Product
 }
 
 template <int NB, int MB, bool BF16>
-hipError_t launch(const Product &p, bool stream, hipStream_t s)
+hipError_t launch(const Product &p, bool stream, bool odd, hipStream_t s)
 {
-    return start(stream ? linear_stream_kernel<NB, MB, BF16> : linear_rowwise_kernel<NB, MB, BF16>,
+    return start(stream ? linear_stream_kernel<NB, MB, BF16>
+                 : odd  ? linear_rowwise_kernel<NB, MB, true, BF16>
+                        : linear_rowwise_kernel<NB, MB, false, BF16>,
                  (p.N + 16 * NB - 1) / (16 * NB), THREADS, s, p);
 }
 
 template <int NB, bool BF16>
-hipError_t launch(const Product &p, bool stream, hipStream_t s)
+hipError_t launch(const Product &p, bool stream, bool odd, hipStream_t s)
 {
-    return p.M <= 16   ? launch<NB, 1, BF16>(p, stream, s)
-           : p.M <= 32 ? launch<NB, 2, BF16>(p, stream, s)
-                       : launch<NB, 4, BF16>(p, stream, s);
+    return p.M <= 16   ? launch<NB, 1, BF16>(p, stream, odd, s)
+           : p.M <= 32 ? launch<NB, 2, BF16>(p, stream, odd, s)
+                       : launch<NB, 4, BF16>(p, stream, odd, s);
 }
 
 }  // namespace
 
-hipError_t launch_rowwise(const Product &p, bool direct, bool bf16, hipStream_t s)
+hipError_t launch_rowwise(const Product &p, bool direct, bool odd, bool bf16, hipStream_t s)
 {
     // 32 rows of W per workgroup where that still gives every CU one, and for
     // an 8-bit save, whose blocks of 32 columns stay in one workgroup.
     const bool two = p.f.save == kSave8 || (p.N + 31) / 32 >= cu_count();
     const bool stream = direct && (!two || p.K >= 8 * SK);
     if (two)
-        return bf16 ? launch<2, true>(p, stream, s) : launch<2, false>(p, stream, s);
-    return bf16 ? launch<1, true>(p, stream, s) : launch<1, false>(p, stream, s);
+        return bf16 ? launch<2, true>(p, stream, odd, s) : launch<2, false>(p, stream, odd, s);
+    return bf16 ? launch<1, true>(p, stream, odd, s) : launch<1, false>(p, stream, odd, s);
 }
 
 }  // namespace lin

@@ -54,7 +54,7 @@ extern "C" {
 
 /*
  * A row-major matrix: element (i, j) at data[i*ld + j], ld >= max(1, columns).
- * Elements behind the last column are neither read nor written.
+ * Elements behind the last column are neither used nor written.
  * HG_E4M3: data holds one code per element, scales the scale bytes, block b of
  * row i at scales[i*lds + b], lds >= ceil(columns / 32).  scales and lds are
  * ignored for the other types.

@@ -211,3 +211,26 @@ def test_weight_of_few_rows(hg, M, N, K, out, accumulate):
     around(buf, N, K)
     if not accumulate:
         assert torch.equal(db, dY.sum(0))
+
+
+@pytest.mark.parametrize("t", [F16, BF16])
+@pytest.mark.parametrize("K", [1, 7, 9, 63, 65, 511, 513, 1023, 2049])
+@pytest.mark.parametrize("N", [1, 40, 8211])
+def test_few_rows_at_odd_elements(hg, N, K, t):
+    """Rows of W, of X or of both at odd elements: odd bases, odd row lengths, NaN before, between and behind rows."""
+    print(f"[cuts] few odd rows N={N} K={K} {t}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(N + K)
+
+    def put(rows, cols, base, ld):
+        flat = torch.full((rows * ld + base + 1,), float("nan"), dtype=t, device=DEV)
+        return flat[base:base + rows * ld].view(rows, ld)[:, :cols].copy_(ints(g, rows, cols))
+
+    odd, even = K + 1 + K % 2, K + 2 - K % 2
+    W = [put(N, K, 1, odd), put(N, K, 0, odd), put(N, K, 1, even), put(N, K, 0, even)]
+    for M in (1, 2, 16, 17, 33, 64):
+        for i, X in enumerate((put(M, K, 0, even), put(M, K, 1, odd), put(M, K, 0, odd), put(M, K, 1, even))):
+            want = torch.mm(X.float(), W[i].float().t())
+            buf, Y = room(M, N, F32)
+            hg.linear(X, W[i], Y)
+            assert torch.equal(Y, want), (M, N, K, i)
+            around(buf, M, N)
