@@ -193,7 +193,8 @@ def test_rows_at_odd_addresses(hg, M, N, K, t):
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("out", [F16, F32])
 @pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (7, 130, 60000), (64, 2000, 5000), (33, 4100, 1928), (16, 40000, 200),
-                                   (2, 33000, 136), (63, 64, 100000), (9, 8256, 1000)])
+                                   (2, 33000, 136), (63, 64, 100000), (9, 8256, 1000), (5, 4111, 1931),
+                                   (64, 2049, 3005)])
 def test_weight_of_few_rows(hg, M, N, K, out, accumulate):
     """dW of few rows: runs of one and many tiles, a last one that is not whole, more strips than places."""
     print(f"[cuts] weight {M}x{N}x{K} {out} {accumulate}", flush=True)
