@@ -69,7 +69,8 @@ __device__ __forceinline__ constexpr int sched(int q, int k)
 // the blocks, the compiler copies accumulators to vector registers ahead of
 // the loop and spills; unrolled, the epilogue's code is there eight times.
 // (The stores' completion is not the compiler's to track: a wave's LDS
-// accesses execute in order, and the reads that follow are waited for.)
+// accesses execute in order, so the reads that follow them need no wait; the
+// barrier before the next tile does.)
 __device__ __forceinline__ void put(const floatx4 (&blk)[T], uint32_t stg, int lane)
 {
 #pragma unroll
@@ -142,6 +143,10 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
             wait_vmcnt<AFTER_EPILOGUE>();
         else
             wait_vmcnt<0>();
+        // The writes of put() are in as well: a wave whose part of the last tile
+        // was outside the matrix read none of them back, and behind the barrier
+        // the others load stage 2 into the same slot.
+        wait_lgkmcnt<0>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
