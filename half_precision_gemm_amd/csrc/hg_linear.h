@@ -58,6 +58,8 @@ struct Product {
 };
 
 constexpr int kFewRows = 64;      // rows that the forms for few rows take
+// HIP refuses a launch of 2^32 threads: the most workgroups of 256.
+constexpr int64_t kMostBlocks = 0xffffffffll / 256;
 
 enum class Layout { NN, NT, TT };   // (TA, TB) = (0, 0), (0, 1), (1, 1)
 

@@ -210,6 +210,13 @@ bool may_slice(int64_t cus, int64_t tiles, const Shape &p, int s)
     return s == 1 || (p.stages() >= 4 * s && tiles * s <= 2 * cus);
 }
 
+// Whether so many items, and the blocks that end column sums, fit one launch (the
+// 256×256 kernel walks its tiles and has no such limit).
+bool may_launch(int tile, int64_t items)
+{
+    return tile == 256 || items + (HG_LINEAR_MAX_WIDTH + 31) / 32 <= lin::kMostBlocks;
+}
+
 // A product's tiles are cut all, none, or only those of the last round, which
 // would leave most of the GPU idle (1729×10332×14080, 287 tiles of 256×256 on 256
 // CUs: none 698 us).
@@ -225,7 +232,7 @@ Cut best_cut(const Shape &p, double *us = nullptr)
             if (whole > 0 && whole == tiles)
                 break;
             for (int s : kSlices) {
-                if (!may_slice(cus, tiles - whole, p, s))
+                if (!may_slice(cus, tiles - whole, p, s) || !may_launch(tile, whole + (tiles - whole) * s))
                     break;
                 const double c = expected_us(cus, tile, p, whole, s);
                 if (first || c < least) {
@@ -272,7 +279,7 @@ void best_cuts(const Shape &a, const Shape &b, Cut &ca, Cut &cb)
             if (!may_slice(cus, a.tiles(tile), a, sa))
                 break;
             for (int sb : kSlices) {
-                if (!may_slice(cus, b.tiles(tile), b, sb))
+                if (!may_slice(cus, b.tiles(tile), b, sb) || !may_launch(tile, a.tiles(tile) * sa + b.tiles(tile) * sb))
                     break;
                 const double c = expected_us(cus, tile, a, sa, b, sb);
                 if (least < 0.0 || c < least) {
@@ -282,6 +289,10 @@ void best_cuts(const Shape &a, const Shape &b, Cut &ca, Cut &cb)
                 }
             }
         }
+    if (least < 0.0) {                            // too many items for one launch
+        ca = cut_into(256, a, 0, 1);
+        cb = cut_into(256, b, 0, 1);
+    }
 }
 int64_t partial_bytes(const Cut &c, const Shape &p)
 {

@@ -159,7 +159,7 @@ hipError_t launch_loose(const Product &p, bool bf16, hipStream_t s)
     const int64_t total = p.whole + (tm * tn - p.whole) * p.splits;
     if (total <= 0)
         return hipSuccess;
-    if (total > 0x7fffffff)
+    if (total > kMostBlocks)
         return hipErrorInvalidConfiguration;
     const Spread w{(int)tm, (int)tn, (int)total};
     return start(bf16 ? linear_loose_kernel<true> : linear_loose_kernel<false>, total, THREADS, s, p, w);

@@ -133,7 +133,7 @@ hipError_t launch_outer(const Product &p, bool bf16, hipStream_t s)
     const int64_t groups = (tn + group - 1) / group, total = tm * groups;
     if (total <= 0)
         return hipSuccess;
-    if (total > 0x7fffffff)
+    if (total > kMostBlocks)
         return hipErrorInvalidConfiguration;
     return start(bf16 ? linear_outer_kernel<true> : linear_outer_kernel<false>, total, THREADS, s, p, (int)tn, (int)group,
                  (int)groups);

@@ -214,7 +214,7 @@ Spread spread(const Product &p, int edge, int64_t &total)
 {
     const int64_t tm = ((int64_t)p.M + edge - 1) / edge, tn = ((int64_t)p.N + edge - 1) / edge;
     total = p.whole + (tm * tn - p.whole) * p.splits;
-    return {(int)tm, (int)tn, total > 0x7fffffff ? 0 : (int)total};
+    return {(int)tm, (int)tn, total > kMostBlocks ? 0 : (int)total};
 }
 
 template <int EDGE, bool BF16>
@@ -224,7 +224,7 @@ hipError_t launch(const Product &p, hipStream_t s)
     const Spread w = spread(p, EDGE, total);
     if (total <= 0)
         return hipSuccess;
-    if (total > 0x7fffffff)
+    if (total > kMostBlocks)
         return hipErrorInvalidConfiguration;
     return start(p.K % BK != 0 ? linear_ring_kernel<EDGE, true, BF16> : linear_ring_kernel<EDGE, false, BF16>, total,
                  THREADS, s, p, w);
@@ -240,7 +240,7 @@ hipError_t launch_pair(const Product *x, const Product *y, const Strips &b, hipS
     const int64_t total = tx + ty + (b.strips > 0 ? (b.cols + 31) / 32 : 0);
     if (total <= 0)
         return hipSuccess;
-    if (total > 0x7fffffff)
+    if (total > kMostBlocks)
         return hipErrorInvalidConfiguration;
     const int y_first = py.per > px.per;
     // (both k-major: the buffer's range ends the sum)

@@ -235,7 +235,7 @@ hipError_t prepare(const Slope &g, const Copy &x, const Copy &w, hipStream_t s)
     const int64_t total = slopes + xb + wb;
     if (total == 0)
         return hipSuccess;
-    if (total > 0x7fffffff)
+    if (total > kMostBlocks)
         return hipErrorInvalidConfiguration;
     auto go = [&](auto kernel) {
         return start(kernel, total, THREADS, s, g, x, w, (int)(tiles > 0 ? tiles : 1), (int)slopes, xb, wb);
