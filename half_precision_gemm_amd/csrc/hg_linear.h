@@ -58,6 +58,10 @@ struct Product {
 };
 
 constexpr int kFewRows = 64;      // rows that the forms for few rows take
+// Blocks of 16 rows of W that a workgroup of those takes: two where that still
+// gives every CU one, and for a Z in 8 bits, whose blocks of 32 columns stay in
+// one workgroup.
+inline int weight_blocks(int64_t N, bool save8) { return save8 || (N + 31) / 32 >= cu_count() ? 2 : 1; }
 // HIP refuses a launch of 2^32 threads: the most workgroups of 256.
 constexpr int64_t kMostBlocks = 0xffffffffll / 256;
 

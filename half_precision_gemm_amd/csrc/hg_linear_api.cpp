@@ -347,11 +347,17 @@ bool bad_work(const void *work, int64_t need) { return need > 0 && (work == null
 // 60.3 / 50.1, 64×8192×8192 35.1 / 38.1, 64×4096×16390 81 / 48.  Operands that
 // the tiles would have to copy first (twice their bytes at 5 TB/s, a launch)
 // count that, those that they take as they are (loose) do not.
-bool row_by_row(int64_t M, int64_t N, int64_t K, bool copy_x, bool copy_w, double tiles_us, bool loose)
+//
+// save8: Z in 8 bits, whose blocks of 32 columns stay in one workgroup: 32 rows of
+// W in each at any N, half as many workgroups (row-wise / tiles, us: 16×4096×4096
+// 12.6 / 13.3, 64×4096×4096 18.0 / 15.0, 16×2048×8192 19.4 / 13.6, 32×4096×8192
+// 25.4 / 23.2, 64×2048×4096 17.5 / 13.2, 16×1024×1024 5.6 / 7.6, 64×4096×1024 9.6 /
+// 8.9).
+bool row_by_row(int64_t M, int64_t N, int64_t K, bool save8, bool copy_x, bool copy_w, double tiles_us, bool loose)
 {
     if (M > lin::kFewRows)
         return false;
-    const int64_t cus = hg::cu_count(), per = (N + 31) / 32 >= cus ? 2 : 1, blocks = (N + 16 * per - 1) / (16 * per);
+    const int64_t cus = hg::cu_count(), per = lin::weight_blocks(N, save8), blocks = (N + 16 * per - 1) / (16 * per);
     const double rounds = (double)((blocks + cus - 1) / cus), xb = M <= 16 ? 1.0 : M <= 32 ? 2.0 : 4.0;
     double us;
     if (!copy_x && !copy_w && (per == 1 || K >= 2048)) {
@@ -362,7 +368,7 @@ bool row_by_row(int64_t M, int64_t N, int64_t K, bool copy_x, bool copy_w, doubl
     } else {
         const double rows = M > 16 ? 16.0 * xb : (double)M;
         const int64_t b16 = (N + 15) / 16;
-        us = 2.2 + (double)((b16 + cus - 1) / cus) * (double)K * (1.15 + 0.045 * rows) * 1e-3;
+        us = 2.2 + (double)std::max((b16 + cus - 1) / cus, per) * (double)K * (1.15 + 0.045 * rows) * 1e-3;
     }
     tiles_us = std::max(tiles_us + 3.0, 4.0 + (double)N * (double)K * 2.0 / 4.6e6);
     if (loose)
@@ -377,7 +383,7 @@ struct LinearPlan {
     bool direct, loose, odd;          // both operands direct; taken as they are by 64×64 tiles; rows at odd elements
     Cut cut;
 };
-LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W)
+LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W, bool save8)
 {
     LinearPlan q;
     double us;
@@ -392,7 +398,7 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
     // 1000×1000×4001 32.4 / 28.8, 2000×2000×1001 29.8 / 29.0, 700×3000×1001 26.5
     // / 27.1).
     q.loose = !q.direct && q.cut.tile == 64;
-    if (row_by_row(M, N, K, q.copy_x, q.copy_w, q.loose ? 1.15 * us : us, q.loose)) {
+    if (row_by_row(M, N, K, save8, q.copy_x, q.copy_w, q.loose ? 1.15 * us : us, q.loose)) {
         q.copy_x = q.copy_w = q.loose = false;
         q.cut = {0, 0, 1, 0};
     } else if (q.loose) {
@@ -471,9 +477,11 @@ int64_t hg_linear_workspace_size(int64_t M, int64_t N, int64_t K, const hg_matri
         return -5;
     if (M == 0 || N == 0 || K == 0)
         return 0;
-    Arena a{nullptr};
-    room_linear(a, plan_linear(M, N, K, X, W), M, N, K);
-    return a.used;
+    // A call that saves Z in 8 bits may take another kernel.
+    Arena a{nullptr}, b{nullptr};
+    room_linear(a, plan_linear(M, N, K, X, W, false), M, N, K);
+    room_linear(b, plan_linear(M, N, K, X, W, true), M, N, K);
+    return std::max(a.used, b.used);
 }
 
 int hg_linear(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W, const float *bias,
@@ -505,7 +513,7 @@ int hg_linear(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
         return -9;
     if (any_meet({sz, ss}, {sx, sw, sb, sr, sy}) || meet(sz, ss))
         return -10;
-    const LinearPlan q = plan_linear(M, N, K, X, W);
+    const LinearPlan q = plan_linear(M, N, K, X, W, Z != nullptr && Z->type == HG_E4M3);
     Arena count{nullptr};
     if (K > 0)
         room_linear(count, q, M, N, K);

@@ -306,9 +306,7 @@ hipError_t launch(const Product &p, bool stream, bool odd, hipStream_t s)
 
 hipError_t launch_rowwise(const Product &p, bool direct, bool odd, bool bf16, hipStream_t s)
 {
-    // 32 rows of W per workgroup where that still gives every CU one, and for
-    // an 8-bit save, whose blocks of 32 columns stay in one workgroup.
-    const bool two = p.f.save == kSave8 || (p.N + 31) / 32 >= cu_count();
+    const bool two = weight_blocks(p.N, p.f.save == kSave8) == 2;
     const bool stream = direct && (!two || p.K >= 8 * SK);
     if (two)
         return bf16 ? launch<2, true>(p, stream, odd, s) : launch<2, false>(p, stream, odd, s);

@@ -98,8 +98,8 @@ int hg_linear(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, cons
               const hg_matrix *R, const hg_matrix *Y, const hg_matrix *Z, void *work, int64_t work_bytes, void *stream);
 
 /* hg_linear_workspace_size — bytes hg_linear needs for these operands on the
- * current device (host only; of X and W the address' alignment, ld and type
- * are looked at); -i for an invalid argument i. */
+ * current device, whatever Y and Z (host only; of X and W the address'
+ * alignment, ld and type are looked at); -i for an invalid argument i. */
 int64_t hg_linear_workspace_size(int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W);
 
 /*

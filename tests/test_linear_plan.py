@@ -76,3 +76,27 @@ def test_launches_of_the_tallest_products(lib, M, N, K):
 def test_launches_of_the_tallest_gradients(lib, M, N, K, want):
     st, done = grad(lib, M, N, K, want=want)
     assert st == 0 and done and all(d["blocks"] <= MOST for _, d in done), done
+
+
+# M, N, K, whether row by row with Z in 16 bits and in 8 bits.  8 bits: 32 rows of W in a workgroup at any N, so half
+# as many workgroups; the measured figures stand beside the choice.
+FEW = [(16, 4096, 4096, True, True), (64, 4096, 4096, True, False), (1, 2048, 8192, True, False),
+       (16, 2048, 8192, True, False), (32, 4096, 8192, True, False), (64, 2048, 4096, True, False),
+       (16, 1024, 1024, True, True), (64, 4096, 1024, True, False), (16, 8192, 2048, True, True),
+       (16, 16384, 4096, True, True), (16, 4096, 4098, True, False), (65, 4096, 4096, False, False)]
+
+
+@pytest.mark.parametrize("M,N,K,rows16,rows8", FEW)
+def test_few_rows_are_priced_as_they_are_launched(lib, M, N, K, rows16, rows8):
+    for save, rows in ((None, rows16), (BF16, rows16), (E4M3, rows8)):
+        st, done = linear(lib, M, N, K, save=save)
+        assert st == 0 and ("rowwise" in [k for k, _ in done]) == rows, (save, done)
+
+
+@pytest.mark.parametrize("M", [1, 7, 16, 33, 64, 100])
+@pytest.mark.parametrize("N,K,ldx,ldw", [(2048, 8192, None, None), (4096, 4096, None, None), (4096, 4098, None, None),
+                                         (1000, 8191, 8192, 8193), (512, 16384, 16386, None), (64, 100, None, 101)])
+def test_one_workspace_for_any_saved_form(lib, M, N, K, ldx, ldw):
+    """hg_linear_workspace_size does not see Z: its size is enough for every form of it."""
+    for save in (None, BF16, E4M3):
+        assert linear(lib, M, N, K, save=save, ldx=ldx, ldw=ldw)[0] == 0, save
