@@ -255,7 +255,8 @@ def linear_grad(dY, W, X, Z=None, act: int = 0, dX=None, dW=None, dbias=None, ac
     of its type or 8-bit checkpoints (codes, scales).  Only the gradients that
     are given are computed: dX (M, K) of dY's type, dW (N, K) of dY's type or
     float32, dbias float32 of length N.  W may be None without dX, X without
-    dW, Z with ACT_NONE.  `accumulate`: dW and dbias are added to.  `work`:
+    dW, Z with ACT_NONE.  `accumulate`: dW and dbias are added to.  dz is
+    rounded to dY's type for dX and dW (float16: infinite past 65504).  `work`:
     device tensor of at least linear_grad_workspace_size(dY, W, X) bytes
     (allocated with torch when None)."""
     dy, w, x, M, N, K, dev = _grad_operands(dY, W, X)

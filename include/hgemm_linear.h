@@ -126,6 +126,9 @@ int64_t hg_linear_workspace_size(int64_t M, int64_t N, int64_t K, const hg_matri
  * dz = dY·act'(z) is computed in fp32; dbias sums it unrounded; for the two
  * products it is rounded once to dY's type (their matrix-core operand), so a
  * term of dX or dW carries a relative error of half a step of that type.
+ * HG_F16: a dz past 65504 is infinite there, as any value rounded to that type
+ * (the slopes of GELU and SiLU reach 1.13 and 1.10, so a dY above 58 000 may
+ * give one); dbias stays finite.
  * The sums are fp32, in a fixed order.  M = 0 sums nothing (dW and dbias are
  * zero, or stay as they are), N = 0 gives dX = 0.  No output may overlap an
  * input, another output or the workspace (-9, -10, -11, -13).
