@@ -530,3 +530,5 @@ from .layer import (ACT_GELU, ACT_GELU_TANH, ACT_SILU, E4M3_BLOCK, EXPORTS_LINEA
                     checkpoint8_empty, checkpoint8_read, checkpoint8_write, linear, linear_grad,
                     linear_grad_workspace, linear_grad_workspace_size, linear_workspace,
                     linear_workspace_size)
+from .adapters import (EXPORTS_ADAPTERS, linear_adapters, linear_adapters_workspace,  # noqa: E402,F401
+                       linear_adapters_workspace_size)

@@ -1,0 +1,109 @@
+// hg_adapters_api.cpp — host side of the C ABI declared in
+// include/hgemm_adapters.h.
+#include "hgemm_adapters.h"
+
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "hg_linear.h"
+#include "hg_linear_host.h"
+
+using namespace hg::host;
+
+namespace {
+
+namespace lin = hg::lin;
+
+// 16-bit numbers, or half as many fp32 ones, that a row of T takes: high and low
+// halves up to the matrix cores' 32 (lin::Adapters).
+int64_t width_of(int64_t rank) { return (2 * up8(rank) + 31) / 32 * 32; }
+
+// The largest tiles that may be taken: 256×256 ones add the terms of whole
+// eights only.
+int most_tile_of(int64_t rank) { return rank % 8 == 0 ? 256 : 128; }
+
+struct Beside {
+    const hg_adapters *l;
+    const hg_matrix *X;
+    int64_t M, N, K;
+
+    bool any() const { return l->count > 0 && l->rank > 0; }
+    static bool strides(const void *p, int64_t ld, int64_t stride, int64_t cols, bool touched)
+    {
+        return ld >= std::max<int64_t>(1, cols) && ld <= HG_LINEAR_MAX_LD && stride >= 0 &&
+               stride <= HG_ADAPTERS_MAX_STRIDE && !(touched && p == nullptr) &&
+               (reinterpret_cast<uintptr_t>(p) & 1) == 0;
+    }
+    int valid() const
+    {
+        if (l == nullptr || l->count < 0 || l->count > HG_ADAPTERS_MAX_COUNT || l->rank < 0 ||
+            l->rank > HG_ADAPTERS_MAX_RANK || l->type != X->type)
+            return -11;
+        if (!any())
+            return HG_OK;
+        const bool touched = M > 0 && N > 0 && K > 0;
+        if (!strides(l->A, l->lda, l->stride_a, K, touched) || !strides(l->B, l->ldb, l->stride_b, l->rank, touched) ||
+            (touched && l->which == nullptr) || (reinterpret_cast<uintptr_t>(l->which) & 7) != 0 ||
+            (reinterpret_cast<uintptr_t>(l->scales) & 3) != 0)
+            return -11;
+        return HG_OK;
+    }
+    bool meets(const Span &s) const
+    {
+        if (!any())
+            return false;
+        const int64_t last = l->count - 1, r = l->rank;
+        return any_meet({s}, {span_of(l->which, M * 8), span_of(l->scales, l->count * 4),
+                              span_of(l->A, (last * l->stride_a + (r - 1) * l->lda + K) * 2),
+                              span_of(l->B, (last * l->stride_b + (N - 1) * l->ldb + r) * 2)});
+    }
+    int check(const Span &y, const Span &z, const Span &zs) const
+    {
+        return meets(y) || meets(z) || meets(zs) ? -11 : HG_OK;
+    }
+    int most_tile() const { return most_tile_of(l->rank); }
+    void *room(Arena &a) const { return a.take(any() ? M * width_of(l->rank) * 2 : 0); }
+    hipError_t begin(lin::Product &p, Arena &a, bool few, bool bf16, hipStream_t s) const
+    {
+        if (!any())
+            return hipSuccess;
+        void *T = room(a);
+        const int64_t ldt = few ? up8(l->rank) : width_of(l->rank);
+        p.ad = {l->which, static_cast<const uint16_t *>(l->B), T, l->stride_b, l->ldb, ldt, (int32_t)l->count, l->rank};
+        return lin::launch_shrink({static_cast<const uint16_t *>(X->data), static_cast<const uint16_t *>(l->A), l->which,
+                                   l->scales, T, X->ld, l->lda, l->stride_a, ldt, (int32_t)M, (int32_t)K,
+                                   (int32_t)l->count, l->rank, few},
+                                  bf16, s);
+    }
+};
+
+}  // namespace
+
+extern "C" {
+
+int64_t hg_linear_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, const hg_matrix *X,
+                                          const hg_matrix *W)
+{
+    const int64_t need = linear_room(M, N, K, X, W, most_tile_of(rank));
+    if (need < 0 && need > -4)
+        return need;
+    if (rank < 0 || rank > HG_ADAPTERS_MAX_RANK)
+        return -4;
+    if (need < 0)
+        return need - 1;
+    if (M == 0 || N == 0 || K == 0)
+        return 0;
+    Arena a{nullptr};
+    a.take(M * width_of(rank) * 2);
+    return need + a.used;
+}
+
+int hg_linear_adapters(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W,
+                       const float *bias, const hg_matrix *R, const hg_matrix *Y, const hg_matrix *Z,
+                       const hg_adapters *adapters, void *work, int64_t work_bytes, void *stream)
+{
+    return linear_call<-12>(act, M, N, K, X, W, bias, R, Y, Z, Beside{adapters, X, M, N, K}, work, work_bytes, stream);
+}
+
+}  // extern "C"

@@ -42,6 +42,24 @@ struct Finish {
     int32_t out32;
 };
 
+constexpr int kFewRows = 64;      // rows that the forms for few rows take
+
+// What the rows' low-rank adapters add to a product's sums: row i, column j gets
+// Σ_k T(i, k)·B_g(j, k) with g = which[i], nothing if g is outside 0 .. count-1.
+// T holds the scaled X·A_gᵀ: of M <= kFewRows rows taken row by row in fp32 (up8
+// = rank up to a multiple of 8 values per row, zeros behind the rank), else as
+// two 16-bit numbers whose sum it is, up8 high ones and up8 low ones, with zeros
+// up to a multiple of 32.  The rest of such a number is 2^-16 (bf16) or 2^-22
+// of it, and the sums take it as 2·up8 more terms of the matrix cores' 32 at
+// once: at rank 16 as many instructions as one 16-bit number would take.
+struct Adapters {
+    const int64_t *which;         // M values
+    const uint16_t *B;            // adapter g: cols×rank at B + g·stride, null: no adapters
+    const void *T;
+    int64_t stride, ldb, ldt;
+    int32_t count, rank;
+};
+
 // One product: C[rows×cols] = Σ_k A(i, k)·B(j, k).  An operand is stored
 // either k-contiguous (A[i·lda + k]) or, TA / TB, k-major (A[k·lda + i]).
 struct Product {
@@ -55,9 +73,9 @@ struct Product {
     int32_t edge, whole, splits, per;
     float *P;
     Finish f;
+    Adapters ad;
 };
 
-constexpr int kFewRows = 64;      // rows that the forms for few rows take
 // Blocks of 16 rows of W that a workgroup of those takes: two where that still
 // gives every CU one, and for a Z in 8 bits, whose blocks of 32 columns stay in
 // one workgroup.
@@ -118,6 +136,20 @@ struct Slope {
 };
 // What the gradient's products wait for, in one launch.
 hipError_t launch_prepare(const Slope &g, const Copy &x, const Copy &w, bool bf16, hipStream_t s);
+
+// T of Adapters from X (M×K, any address) and the adapters' A (adapter g: rank×K
+// at A + g·stride), with the adapters' scales (null: 1); rows without an adapter
+// are left alone.  wide: fp32, else two 16-bit numbers.
+struct Shrink {
+    const uint16_t *X, *A;
+    const int64_t *which;
+    const float *scales;
+    void *T;
+    int64_t ldx, lda, stride, ldt;
+    int32_t M, K, count, rank;
+    bool wide;
+};
+hipError_t launch_shrink(const Shrink &q, bool bf16, hipStream_t s);
 
 // rows×cols zeros (fp32 or 16 bits).
 hipError_t launch_zero(void *C, int64_t ldc, int64_t rows, int64_t cols, bool wide, hipStream_t s);
@@ -788,6 +820,87 @@ __device__ __forceinline__ void settle(float (&b)[8])
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         __asm__ volatile("" : "+v"(b[e]));
+}
+
+// ---- Adapters, as the kernels take them.
+//
+// The adapter of a row, -1 for none.
+__device__ __forceinline__ int adapter_of(const Adapters &a, int row, int rows)
+{
+    const int64_t g = row < rows ? a.which[row] : -1;
+    return g >= 0 && g < a.count ? (int)g : -1;
+}
+// The least of the lanes' values, the same in all of them.
+__device__ __forceinline__ int least_of_wave(int v)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        v = min(v, __shfl_xor(v, d));
+    return __builtin_amdgcn_readfirstlane(v);
+}
+
+// Adds the adapters' terms to a wave's accumulators, TI×TJ blocks of 16×16 at
+// (row0, col0), after its sum of products and before what ends it.
+//
+// One turn for every adapter among the wave's rows, in ascending order: its T and
+// B come from L2 straight into the matrix core's operand layout, 32 terms at a
+// time.  A block whose rows all have this adapter takes the products as they are;
+// one with other rows among them keeps those rows' sums (a choice by lane, not
+// zeros in T: an infinity or NaN of one request's adapter stays in its rows).
+// Rows past the last are not stored and may get anything.  With prompts one
+// after the other most waves take one turn, whose loads are one wait of memory;
+// rows of different adapters side by side cost a turn each.
+template <bool BF16, int TI, int TJ>
+__device__ __forceinline__ void add_adapters(const Product &p, int row0, int col0, int lane, floatx4 (&acc)[TI][TJ])
+{
+    const Adapters &a = p.ad;
+    const int frow = lane & 15, fhi = lane >> 4;
+    const int chunks = (a.rank + 7) / 8, steps = (2 * chunks + 3) / 4;
+    int mine[TI];
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+        mine[i] = adapter_of(a, row0 + 16 * i + frow, p.M);
+    for (int g = -1;;) {
+        int next = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+            next = min(next, mine[i] > g ? mine[i] : 0x7fffffff);
+        g = least_of_wave(next);
+        if (g == 0x7fffffff)
+            return;
+        const uint16_t *B = a.B + g * a.stride;
+        for (int s = 0; s < steps; ++s) {
+            const int c = 4 * s + fhi, cb = c < chunks ? c : c - chunks;      // low halves meet the same B
+            const int left = c < 2 * chunks ? a.rank - 8 * cb : 0;
+            half8 b[TJ], t[TI];
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+                b[j] = __builtin_bit_cast(half8, load16x8(B + min(col0 + 16 * j + frow, p.N - 1) * a.ldb + 8 * cb, left));
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+                t[i] = *reinterpret_cast<const half8 *>(static_cast<const uint16_t *>(a.T) +
+                                                        min(row0 + 16 * i + frow, p.M - 1) * a.ldt + 8 * c);
+#pragma unroll
+            for (int i = 0; i < TI; ++i) {
+                const bool me = mine[i] == g;
+                if (__builtin_amdgcn_ballot_w64(me) == 0)
+                    continue;
+                if (__builtin_amdgcn_ballot_w64(!me && row0 + 16 * i + frow < p.M) == 0) {
+#pragma unroll
+                    for (int j = 0; j < TJ; ++j)
+                        acc[i][j] = mfma_16x16x32<BF16>(b[j], t[i], acc[i][j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < TJ; ++j) {
+                        const floatx4 sum = mfma_16x16x32<BF16>(b[j], t[i], acc[i][j]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[i][j][e] = me ? sum[e] : acc[i][j][e];
+                    }
+                }
+            }
+        }
+    }
 }
 
 // ---- Wave-private staging of a 16×W block of sums (fp32) in LDS, from the

@@ -24,7 +24,7 @@ namespace {
 
 constexpr int EDGE = 64, THREADS = 256, DEPTH = 4;
 
-template <bool BF16>
+template <bool BF16, bool ADAPT>
 __global__ void __launch_bounds__(THREADS, 2) linear_loose_kernel(const Product p, const Spread w)
 {
     using S = Side<EDGE, false>;
@@ -135,6 +135,10 @@ __global__ void __launch_bounds__(THREADS, 2) linear_loose_kernel(const Product 
             }
         }
     }
+    if constexpr (ADAPT) {
+        if (t.kt0 == 0)
+            add_adapters<BF16>(p, t.m0 + wm * WT, t.n0 + wn * WT, lane, acc);
+    }
     meet();
 
     unsigned char *stg = smem + wave * (16 * WT * 4);
@@ -162,7 +166,9 @@ hipError_t launch_loose(const Product &p, bool bf16, hipStream_t s)
     if (total > kMostBlocks)
         return hipErrorInvalidConfiguration;
     const Spread w{(int)tm, (int)tn, (int)total};
-    return start(bf16 ? linear_loose_kernel<true> : linear_loose_kernel<false>, total, THREADS, s, p, w);
+    if (p.ad.B != nullptr)
+        return start(bf16 ? linear_loose_kernel<true, true> : linear_loose_kernel<false, true>, total, THREADS, s, p, w);
+    return start(bf16 ? linear_loose_kernel<true, false> : linear_loose_kernel<false, false>, total, THREADS, s, p, w);
 }
 
 }  // namespace lin

@@ -36,7 +36,7 @@ constexpr int kSlots = EDGE == 64 ? 5 : 4;
 template <int EDGE>
 constexpr int kLds = kSlots<EDGE> * 2 * EDGE * kStage * 2;
 
-template <int EDGE, bool TA, bool TB, bool KCHK, bool BF16>
+template <int EDGE, bool TA, bool TB, bool KCHK, bool BF16, bool ADAPT = false>
 __device__ __forceinline__ void ring_tile(const Product &p, const Spread &w, int id, unsigned char *smem)
 {
     using SA = Side<EDGE, TA>;
@@ -140,6 +140,10 @@ __device__ __forceinline__ void ring_tile(const Product &p, const Spread &w, int
         if (kt + 1 < nk)
             step(kt + 1, f1, f0);
     }
+    if constexpr (ADAPT) {
+        if (kt0 == 0)
+            add_adapters<BF16>(p, m0 + wm * WT, n0 + wn * WT, lane, acc);
+    }
     // The ring's last loads (zero fills) and everyone's reads are done before
     // the slots are used for the staging of the results.
     wait_vmcnt<0>();
@@ -162,11 +166,11 @@ __device__ __forceinline__ void ring_tile(const Product &p, const Spread &w, int
     }
 }
 
-template <int EDGE, bool KCHK, bool BF16>
+template <int EDGE, bool KCHK, bool BF16, bool ADAPT>
 __global__ void __launch_bounds__(THREADS, 1) linear_ring_kernel(const Product p, const Spread w)
 {
     __shared__ __attribute__((aligned(1024))) unsigned char smem[kLds<EDGE>];
-    ring_tile<EDGE, false, false, KCHK, BF16>(p, w, blockIdx.x, smem);
+    ring_tile<EDGE, false, false, KCHK, BF16, ADAPT>(p, w, blockIdx.x, smem);
 }
 
 // db = (db +) the strips' sums of 32 columns: eight threads to a column, each
@@ -226,8 +230,11 @@ hipError_t launch(const Product &p, hipStream_t s)
         return hipSuccess;
     if (total > kMostBlocks)
         return hipErrorInvalidConfiguration;
-    return start(p.K % BK != 0 ? linear_ring_kernel<EDGE, true, BF16> : linear_ring_kernel<EDGE, false, BF16>, total,
-                 THREADS, s, p, w);
+    if (p.ad.B != nullptr)
+        return start(p.K % BK != 0 ? linear_ring_kernel<EDGE, true, BF16, true> : linear_ring_kernel<EDGE, false, BF16, true>,
+                     total, THREADS, s, p, w);
+    return start(p.K % BK != 0 ? linear_ring_kernel<EDGE, true, BF16, false> : linear_ring_kernel<EDGE, false, BF16, false>,
+                 total, THREADS, s, p, w);
 }
 
 template <int EDGE, bool BF16>

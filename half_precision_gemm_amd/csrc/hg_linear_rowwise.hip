@@ -58,6 +58,48 @@ __device__ __forceinline__ void finish_sums(const Product &p, float (*part)[MB *
     finish8<BF16>(p.f, row, n0 + c, v, bias);
 }
 
+// Where a workgroup's sums begin: at what the rows' adapters add (hg_linear.h,
+// Adapters), or at zero.  Wave w takes the rank's eighths w, w + 8, ..: a lane the
+// columns and rows whose sums it holds, with T in fp32 and eight of B in one load
+// for each of them, so that 64 rows of 64 adapters cost what those of one do, and
+// no more than one wait of memory for B up to a rank of 64.
+template <int NB, int MB, bool BF16>
+__device__ __forceinline__ void begin_sums(const Product &p, floatx4 (&acc)[MB][NB], int n0, int wave, int lane)
+{
+    const Adapters &a = p.ad;
+    const int frow = lane & 15, fhi = lane >> 4;
+    int mine[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+        mine[i] = adapter_of(a, 16 * i + frow, p.M);
+    for (int k = 8 * wave; k < a.rank; k += 8 * WAVES) {
+        const int left = a.rank - k;
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+            if (mine[i] < 0)
+                continue;
+            const float *T = static_cast<const float *>(a.T) + (16 * i + frow) * a.ldt + k;
+            const floatx4 lo = *reinterpret_cast<const floatx4 *>(T), hi = *reinterpret_cast<const floatx4 *>(T + 4);
+            const uint16_t *B = a.B + mine[i] * a.stride + k;
+            u32x4 b[NB][4];
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    b[j][e] = load16x8(B + min(n0 + 16 * j + 4 * fhi + e, p.N - 1) * a.ldb, left);
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        acc[i][j][e] = __builtin_fmaf(q < 4 ? lo[q] : hi[q - 4],
+                                                      widen<BF16>((uint16_t)(b[j][e][q >> 1] >> (16 * (q & 1)))),
+                                                      acc[i][j][e]);
+        }
+    }
+}
+
 // NB blocks of 16 rows of W, MB blocks of 16 rows of X, at any address (ODD: odd
 // elements too) and of any length.  W goes from memory straight to registers in the matrix core's
 // operand layout (lane l: row l mod 16, 8 k from 8·(l div 16) on: one 16-byte
@@ -71,7 +113,7 @@ template <int NB, int MB, bool ODD>
 struct Pieces {
     Raw<ODD> w[NB][2], x[MB][2];
 };
-template <int NB, int MB, bool ODD, bool BF16>
+template <int NB, int MB, bool ODD, bool BF16, bool ADAPT>
 __global__ void __launch_bounds__(THREADS, 1) linear_rowwise_kernel(const Product p)
 {
     constexpr int DEPTH = NB * 2 + MB * 2 <= 4 ? 4 : NB * 2 + MB * 2 <= 8 ? 2 : 1;
@@ -94,6 +136,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_rowwise_kernel(const Produc
 #pragma unroll
         for (int j = 0; j < NB; ++j)
             acc[i][j] = floatx4{0, 0, 0, 0};
+    if constexpr (ADAPT)
+        begin_sums<NB, MB, BF16>(p, acc, n0, wave, lane);
     using Piece = Pieces<NB, MB, ODD>;
     auto load = [&](int piece, Piece &q) __attribute__((always_inline)) {
         const int k = piece * PIECE + 8 * fhi;
@@ -195,7 +239,7 @@ constexpr int kStreamSlot = 16 * (NB + MB) * SK * 2;
 template <int NB, int MB>
 constexpr int kStreamSlots = (NB * MB <= 2 ? 80 : 160) * 1024 / kStreamSlot<NB, MB>;
 
-template <int NB, int MB, bool BF16>
+template <int NB, int MB, bool BF16, bool ADAPT>
 __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const Product p)
 {
     constexpr int NS = kStreamSlots<NB, MB>, SLOT = kStreamSlot<NB, MB>;
@@ -250,6 +294,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const Product
 #pragma unroll
         for (int j = 0; j < NB; ++j)
             acc[i][j] = floatx4{0, 0, 0, 0};
+    if constexpr (ADAPT)
+        begin_sums<NB, MB, BF16>(p, acc, n0, wave, lane);
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s)
         issue(s);
@@ -285,13 +331,20 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const Product
     finish_sums<NB, MB, BF16>(p, reinterpret_cast<float(*)[MB * 16][NB * 16]>(smem), acc, n0, wave, lane);
 }
 
+template <int NB, int MB, bool BF16, bool ADAPT>
+hipError_t launch_one(const Product &p, bool stream, bool odd, hipStream_t s)
+{
+    return start(stream ? linear_stream_kernel<NB, MB, BF16, ADAPT>
+                 : odd  ? linear_rowwise_kernel<NB, MB, true, BF16, ADAPT>
+                        : linear_rowwise_kernel<NB, MB, false, BF16, ADAPT>,
+                 (p.N + 16 * NB - 1) / (16 * NB), THREADS, s, p);
+}
+
 template <int NB, int MB, bool BF16>
 hipError_t launch(const Product &p, bool stream, bool odd, hipStream_t s)
 {
-    return start(stream ? linear_stream_kernel<NB, MB, BF16>
-                 : odd  ? linear_rowwise_kernel<NB, MB, true, BF16>
-                        : linear_rowwise_kernel<NB, MB, false, BF16>,
-                 (p.N + 16 * NB - 1) / (16 * NB), THREADS, s, p);
+    return p.ad.B != nullptr ? launch_one<NB, MB, BF16, true>(p, stream, odd, s)
+                             : launch_one<NB, MB, BF16, false>(p, stream, odd, s);
 }
 
 template <int NB, bool BF16>

@@ -81,7 +81,73 @@ __device__ __forceinline__ void put(const floatx4 (&blk)[T], uint32_t stg, int l
                          : "memory");
 }
 
-template <bool TA, bool TB, bool KCHK, bool BF16>
+// Whether one of eight 16-bit numbers is infinite or NaN: its exponent is all
+// ones, so that its magnitude plus the exponent's last place carries to the sign.
+template <bool BF16>
+__device__ __forceinline__ bool not_finite(const half8 &v)
+{
+    constexpr uint32_t one = BF16 ? 0x00800080u : 0x04000400u;
+    const u32x4 w = (__builtin_bit_cast(u32x4, v) & 0x7fff7fffu) + one;
+    return ((w[0] | w[1] | w[2] | w[3]) & 0x80008000u) != 0;
+}
+
+// The adapters' terms of a wave's 64 blocks (hg_linear.h), ranks that are a
+// multiple of 8.  Accumulators that a choice or a branch touches leave their
+// registers (add_adapters() spills a thousand of them here), so this is straight
+// code: one more 32-wide step of the K loop for every adapter among the wave's 128
+// rows, T zero in the rows of others.  So that zero times an infinity or NaN of
+// this adapter's B does not reach those rows, eight numbers with one among them
+// count as zeros, and the adapter's own rows get a NaN from T instead.
+template <bool BF16>
+__device__ __forceinline__ void add_adapters_straight(const Product &p, int row0, int col0, int lane, floatx4 (&acc)[T][T])
+{
+    const Adapters &a = p.ad;
+    const int frow = lane & 15, fhi = lane >> 4;
+    const int chunks = a.rank / 8, steps = (2 * chunks + 3) / 4;
+    int mine[T];
+#pragma unroll
+    for (int i = 0; i < T; ++i)
+        mine[i] = adapter_of(a, row0 + 16 * i + frow, p.M);
+    const uint16_t *rows = static_cast<const uint16_t *>(a.T);
+    for (int g = -1;;) {
+        int next = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+            next = min(next, mine[i] > g ? mine[i] : 0x7fffffff);
+        g = least_of_wave(next);
+        if (g == 0x7fffffff)
+            return;
+        for (int s = 0; s < steps; ++s) {
+            const int c = 4 * s + fhi, cb = c < chunks ? c : c < 2 * chunks ? c - chunks : 0;
+            const uint16_t *B = a.B + g * a.stride + 8 * cb;
+            half8 b[T], t[T];
+#pragma unroll
+            for (int j = 0; j < T; ++j)
+                b[j] = __builtin_bit_cast(half8, *reinterpret_cast<const u32x4_any *>(B + min(col0 + 16 * j + frow, p.N - 1) * a.ldb));
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+                t[i] = *reinterpret_cast<const half8 *>(rows + min(row0 + 16 * i + frow, p.M - 1) * a.ldt + 8 * c);
+            bool bad = false;
+#pragma unroll
+            for (int j = 0; j < T; ++j) {
+                const bool x = not_finite<BF16>(b[j]);
+                bad |= x;
+                b[j] = __builtin_bit_cast(half8, __builtin_bit_cast(u32x4, b[j]) & (x ? 0u : ~0u));
+            }
+            const uint32_t nan = __builtin_amdgcn_ballot_w64(bad) != 0 ? 0x7fff7fffu : 0u;
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+                t[i] = __builtin_bit_cast(half8, (__builtin_bit_cast(u32x4, t[i]) | nan) & (mine[i] == g ? ~0u : 0u));
+#pragma unroll
+            for (int j = 0; j < T; ++j)
+#pragma unroll
+                for (int i = 0; i < T; ++i)
+                    acc[i][j] = mfma_16x16x32<BF16>(b[j], t[i], acc[i][j]);
+        }
+    }
+}
+
+template <bool TA, bool TB, bool KCHK, bool BF16, bool ADAPT = false>
 __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p, const Spread w)
 {
     __shared__ __attribute__((aligned(1024))) unsigned char smem[LDS_BYTES];
@@ -201,6 +267,10 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
             as = an;
             bs = bn;
         }
+        if constexpr (ADAPT) {
+            if (t.kt0 == 0)
+                add_adapters_straight<BF16>(p, t.m0 + wm * WT, t.n0 + wn * WT, lane, acc);
+        }
         // the ring's last loads (zero fills) and everyone's reads are done:
         // the slots are free
         wait_vmcnt<0>();
@@ -257,6 +327,12 @@ hipError_t launch(const Product &p, hipStream_t s)
     grid = grid / 8 * 8 > 0 ? grid / 8 * 8 : grid;
     if (grid > total)
         grid = total;
+    if constexpr (!TA && !TB) {
+        if (p.ad.B != nullptr)
+            return start(p.K % kStage != 0 ? linear_tile_kernel<false, false, true, BF16, true>
+                                           : linear_tile_kernel<false, false, false, BF16, true>,
+                         grid, THREADS, s, p, w);
+    }
     return start(!(TA && TB) && p.K % kStage != 0 ? linear_tile_kernel<TA, TB, !(TA && TB), BF16>
                                                   : linear_tile_kernel<TA, TB, false, BF16>,
                  grid, THREADS, s, p, w);

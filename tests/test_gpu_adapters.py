@@ -1,0 +1,260 @@
+"""hg_linear_adapters: Y = act(X·Wᵀ + bias + s_g·(X·A_gᵀ)·B_gᵀ) + R, g the row's
+adapter, against 64 bits.
+
+Bound, in the terms of linear_ref.py.  t = s_g·Σ x·a in fp32 is off by et =
+|s_g|·(K + 3)·u32·Σ|x|·|a|.  As two numbers of X's type, each a rounding of what
+the one before leaves, it is off by half(X's type)² of it more, in fp16 at least
+2^-25; |t| + that bounds the two.  The sum of K products and at most 2·(rank + 7)
++ 32 more terms is off by (K + 2·rank + 48)·u32 of their magnitudes, and by
+et·Σ|b|.  bias, act and R as linear_ref.linear's.
+"""
+import pytest
+import torch
+
+import linear_ref as ref
+from test_gpu_linear import BF16, DEV, F16, F32, act_of, room, strided
+
+pytestmark = pytest.mark.gpu
+U32 = ref.U32
+
+
+def operands(M, N, K, rank, count, t, order, seed=0, scales=True):
+    g = torch.Generator().manual_seed(seed * 1000003 + M * 7919 + N * 31 + K + rank)
+    X = torch.randn(M, K, generator=g).to(t)
+    W = (torch.randn(N, K, generator=g) / max(K, 1) ** 0.5).to(t)
+    A = (torch.randn(count, rank, K, generator=g) / max(K, 1) ** 0.5).to(t)
+    B = (0.5 * torch.randn(count, N, rank, generator=g)).to(t)
+    s = torch.rand(count, generator=g) + 0.5 if scales else None
+    if order == "single":
+        which = torch.randint(-1, count + 1, (M,), generator=g)
+    elif order == "one":
+        which = torch.full((M,), count - 1)
+    elif order == "none":
+        which = torch.full((M,), -1)
+    else:
+        which = torch.randint(-1, count, (M // 50 + 1,), generator=g).repeat_interleave(
+            torch.randint(1, 150, (M // 50 + 1,), generator=g))
+        which = torch.cat((which, which.new_full((M,), 0)))[:M]
+    return X, W, A, B, s, which.long()
+
+
+def expected(X, W, A, B, s, which, bias, name, R):
+    """(Y, Z, bound of Y, bound of Z) before the last rounding."""
+    K, rank, count, t = X.shape[1], A.shape[1], A.shape[0], X.dtype
+    x, w = X.double(), W.double()
+    z, mag = x @ w.t(), x.abs() @ w.abs().t()
+    ez = torch.zeros_like(z)
+    for g in range(count):
+        rows = (which == g).nonzero()[:, 0]
+        a, b, f = A[g].double(), B[g].double(), 1.0 if s is None else float(s[g])
+        v, size = f * (x[rows] @ a.t()), abs(f) * (x[rows].abs() @ a.abs().t())
+        e = (K + 3) * U32 * size
+        e = e + ref.half(t) ** 2 * (v.abs() + e) + (2.0 ** -25 if t == F16 else 0.0)
+        z[rows] += v @ b.t()
+        mag[rows] += (v.abs() + e) @ b.abs().t()
+        ez[rows] = e @ b.abs().t()
+    if bias is not None:
+        z, mag = z + bias.double(), mag + bias.double().abs()
+    ez = ez + (K + 2 * rank + 48) * U32 * mag
+    y = ref.act(z, name)
+    ey = 1.13 * ez + (z.abs() + ez) * 2.0 ** -20
+    if R is not None:
+        y = y + R.double()
+        ey = ey + U32 * (y.abs() + ey)
+    return y, z, ey, ez
+
+
+def stack(x, pad, shift=0):
+    """A (G, rows, cols) stack on the device, rows cols + pad apart, NaN between them."""
+    G, rows, cols = x.shape
+    buf = torch.full((G * (rows + 1) * (cols + pad) + shift,), float("nan"), dtype=x.dtype, device=DEV)
+    v = buf[shift:].view(G, rows + 1, cols + pad)[:, :rows, :cols]
+    v.copy_(x)
+    return v
+
+
+def case(hg, M, N, K, rank, count, t=BF16, order="runs", name="none", bias=False, R=False, out=None, save=None, pad=0,
+         shift=0, apad=0, opad=0, scales=True, seed=0):
+    print(f"[adapters] M={M} N={N} K={K} rank={rank} count={count} {t} {order} {name} out={out} save={save} pad={pad} "
+          f"shift={shift} apad={apad}", flush=True)
+    X, W, A, B, s, which = operands(M, N, K, rank, count, t, order, seed, scales)
+    g = torch.Generator().manual_seed(seed + 5)
+    b = torch.randn(N, generator=g) if bias else None
+    r = torch.randn(M, N, generator=g).to(out or t) if R else None
+    Y, around = room(M, N, out or t, opad)
+    Z = hg.checkpoint8_empty(M, N, DEV) if save == 8 else torch.empty(M, N, dtype=t, device=DEV) if save else None
+    got = hg.linear_adapters(strided(X, pad, shift), strided(W, pad, shift), Y, which.to(DEV), stack(A, apad, shift),
+                             stack(B, apad, shift), scales=None if s is None else s.to(DEV),
+                             bias=None if b is None else b.to(DEV), act=act_of(hg, name),
+                             residual=None if r is None else r.to(DEV), Z=Z)
+    assert got is Y
+    torch.cuda.synchronize()
+    around()
+    y, z, ey, ez = expected(X, W, A, B, s, which, b, name, r)
+    ref.check(Y, y, ey, "Y")
+    if save == 16:
+        ref.check(Z, z, ez, "Z")
+    elif save == 8:
+        v = ref.values8(*Z)
+        step = torch.exp2(Z[1].cpu().double() - 127).repeat_interleave(ref.BLOCK, 1)[:, :N]
+        assert ((v - z).abs() <= ez + torch.maximum(2.0 ** -4 * (z.abs() + ez), 2.0 ** -10 * step)).all()
+
+
+# few rows: through LDS, through registers, at odd elements
+@pytest.mark.parametrize("t", [F16, BF16])
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 33, 64])
+@pytest.mark.parametrize("N,K,rank,pad,shift,order", [
+    (256, 512, 16, 0, 0, "single"), (250, 2048, 8, 8, 0, "one"), (100, 333, 9, 1, 0, "single"), (65, 72, 64, 0, 1, "runs"),
+    (1000, 64, 1, 0, 0, "single"), (33, 8, 100, 0, 0, "single"),
+])
+def test_few_rows(hg, t, M, N, K, rank, pad, shift, order):
+    case(hg, M, N, K, rank, 5, t, order, pad=pad, shift=shift, bias=M % 2 == 0)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 16384, 4096), (16, 9000, 2048), (40, 8200, 256), (64, 8224, 512)])
+def test_few_rows_of_wide_weights(hg, M, N, K):
+    """32 rows of W in a workgroup."""
+    case(hg, M, N, K, 16, 8, BF16, "single")
+
+
+# 64×64 tiles, the same at any address, 128×128, slices, 256×256, with rows and columns that do not fill them
+@pytest.mark.parametrize("t", [F16, BF16])
+@pytest.mark.parametrize("M,N,K,rank,count,order,kw", [
+    (65, 512, 512, 16, 5, "single", {}), (333, 111, 777, 9, 5, "single", dict(name="silu", bias=True)),
+    (300, 260, 4000, 16, 3, "runs", dict(R=True, out=F32)), (700, 900, 640, 40, 4, "runs", dict(pad=8, apad=8)),
+    (600, 1000, 100, 7, 64, "single", dict(save=8)), (1030, 2060, 131, 32, 6, "runs", dict(pad=1, opad=3)),
+    (2048, 4096, 128, 17, 3, "runs", dict(bias=True, name="gelu")), (200, 300, 320, 256, 2, "single", {}),
+    (1000, 1000, 200, 16, 1, "one", dict(scales=False, save=16)), (512, 512, 64, 16, 3, "none", {}),
+])
+def test_tiles(hg, t, M, N, K, rank, count, order, kw):
+    case(hg, M, N, K, rank, count, t, order, **kw)
+
+
+@pytest.mark.parametrize("M,N,K,rank,count,order,kw", [
+    (4096, 4096, 64, 16, 4, "runs", {}), (3001, 5003, 128, 8, 300, "single", dict(out=F32)),
+    (4000, 4000, 200, 32, 3, "runs", dict(R=True, name="gelu_tanh", save=16)), (2500, 4400, 264, 64, 2, "one", {}),
+    (4096, 4096, 72, 24, 40, "single", dict(apad=1, shift=1)), (4100, 4200, 64, 16, 4, "none", dict(bias=True, save=8)),
+])
+@pytest.mark.parametrize("t", [F16, BF16])
+def test_large_tiles(hg, t, M, N, K, rank, count, order, kw):
+    case(hg, M, N, K, rank, count, t, order, **kw)
+
+
+@pytest.mark.parametrize("M,N,K,rank", [(7, 40, 0, 16), (5, 64, 64, 0), (0, 64, 64, 16), (5, 0, 64, 16), (1, 1, 1, 1)])
+def test_empty_and_smallest(hg, M, N, K, rank):
+    case(hg, M, N, K, rank, 3, order="single", bias=True)
+
+
+@pytest.mark.parametrize("M,N,K,rank", [(16, 256, 512, 16), (300, 256, 512, 16), (300, 256, 512, 9), (4096, 4096, 64, 16)])
+@pytest.mark.parametrize("t", [F16, BF16])
+def test_what_is_not_finite_stays_with_its_request(hg, t, M, N, K, rank):
+    """Neither a row of X nor an adapter's A or B that holds a NaN or an infinity changes other requests' rows, and its
+    own do not come out finite where it enters."""
+    X, W, A, B, s, which = operands(M, N, K, rank, 6, t, "single")
+    which[:] = torch.arange(M) % 5
+    which[M // 2] = 5
+    run = lambda: hg.linear_adapters(X.to(DEV), W.to(DEV), torch.empty(M, N, dtype=t, device=DEV), which.to(DEV),  # noqa: E731
+                                     A.to(DEV), B.to(DEV), scales=s.to(DEV)).cpu()
+    want = run()
+    X[3, 5] = float("nan")
+    A[1, 2 % rank, 3] = float("inf")
+    B[2, 7, rank - 1] = float("nan")
+    B[5, 11, 0] = float("inf")
+    got = run()
+    clean = (which != 1) & (which != 2) & (which != 5)
+    clean[3] = False
+    assert torch.equal(got[clean], want[clean])
+    assert got[3].isnan().all() and not got[which == 1].isfinite().any()
+    mine = got[which == 2]
+    assert mine[:, 7].isnan().all() and not got[which == 5][:, 11].isfinite().any()
+
+
+@pytest.mark.parametrize("M,N,K,rank", [(64, 256, 512, 16), (300, 256, 512, 16), (4096, 4096, 64, 16)])
+def test_a_row_does_not_depend_on_the_others(hg, M, N, K, rank):
+    """The same row beside other rows, in another place of its tile's adapters: the same bits."""
+    X, W, A, B, s, which = (x.to(DEV) if x is not None else None for x in operands(M, N, K, rank, 6, BF16, "single"))
+    X[M - 1], which[M - 1] = X[0], which[0].clamp(0, 5)
+    which[0] = which[M - 1]
+    Y = hg.linear_adapters(X, W, torch.empty(M, N, dtype=BF16, device=DEV), which, A, B, scales=s)
+    assert torch.equal(Y[0], Y[M - 1])
+    again = hg.linear_adapters(X, W, torch.empty(M, N, dtype=BF16, device=DEV), which, A, B, scales=s)
+    assert torch.equal(Y, again)
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 512, 512), (200, 512, 512), (4096, 4096, 64)])
+def test_graph(hg, M, N, K):
+    """Captured and replayed with other rows, adapters and work between the replays."""
+    X, W, A, B, s, which = (x.to(DEV) for x in operands(M, N, K, 16, 6, BF16, "runs"))
+    Y, eager = (torch.empty(M, N, dtype=BF16, device=DEV) for _ in range(2))
+    work = hg.linear_adapters_workspace(X, W, A)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        hg.linear_adapters(X, W, Y, which, A, B, scales=s, work=work)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hg.linear_adapters(X, W, Y, which, A, B, scales=s, work=work)
+    for i in range(4):
+        X.copy_(torch.randn(M, K, device=DEV))
+        which.copy_(torch.randint(-1, 6, (M,), device=DEV))
+        Y.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        hg.linear_adapters(X, W, eager, which, A, B, scales=s)
+        assert torch.equal(Y, eager), i
+
+
+def test_another_stream(hg):
+    X, W, A, B, s, which = (x.to(DEV) for x in operands(50, 300, 512, 16, 6, F16, "single"))
+    want = hg.linear_adapters(X, W, torch.empty(50, 300, dtype=F16, device=DEV), which, A, B, scales=s)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = hg.linear_adapters(X, W, torch.empty(50, 300, dtype=F16, device=DEV), which, A, B, scales=s)
+        torch.cuda.current_stream().synchronize()
+    assert torch.equal(got, want)
+
+
+def test_adapters_past_32_bits(hg):
+    """Adapters 2^31 elements apart."""
+    M, N, K, rank = 20, 64, 64, 8
+    X, W, A, B, s, which = operands(M, N, K, rank, 3, BF16, "single")
+    gap = (1 << 30) + 1000
+    big = torch.zeros(2 * gap + 4096, dtype=BF16, device=DEV)
+    a, b = big.as_strided((3, rank, K), (gap, K, 1)), big[1000:].as_strided((3, N, rank), (gap, rank, 1))
+    a.copy_(A)
+    b.copy_(B)
+    Y = torch.empty(M, N, dtype=BF16, device=DEV)
+    hg.linear_adapters(X.to(DEV), W.to(DEV), Y, which.to(DEV), a, b, scales=s.to(DEV))
+    y, _, ey, _ = expected(X, W, A, B, s, which, None, "none", None)
+    ref.check(Y, y, ey, "Y")
+
+
+def test_without_adapters_it_is_the_layer(hg):
+    for M in (5, 300):
+        X, W, A, B, s, which = (x.to(DEV) for x in operands(M, 200, 128, 16, 3, BF16, "none"))
+        want = hg.linear(X, W, torch.empty(M, 200, dtype=BF16, device=DEV))
+        for a, b, f in ((A, B, s), (A[:0], B[:0], s[:0]), (A[:, :0], B[:, :, :0], s)):
+            got = hg.linear_adapters(X, W, torch.empty(M, 200, dtype=BF16, device=DEV), which, a, b, scales=f)
+            assert torch.equal(got, want)
+
+
+def test_training_an_adapter_with_the_layer(hg):
+    """One adapter's product as two layers, and its gradients: what the header says an adapter is trained with."""
+    X, W, A, B, s, which = operands(300, 200, 256, 16, 1, F16, "one", scales=False)
+    x, w, a, b = (v.to(DEV) for v in (X, W, A[0], B[0]))
+    new = lambda *shape, t=F16: torch.empty(*shape, dtype=t, device=DEV)  # noqa: E731
+    t = hg.linear(x, a, new(300, 16))
+    y = hg.linear(t, b, new(300, 200, t=F32), residual=hg.linear(x, w, new(300, 200, t=F32)))
+    both = hg.linear_adapters(x, w, new(300, 200, t=F32), which.to(DEV), A.to(DEV), B.to(DEV))
+    ty = X.double() @ A[0].double().t()
+    # the two differ by the rounding of t to fp16 and by fp32 sums
+    lim = (ref.half(F16) * 1.01) * ty.abs() @ B[0].double().abs().t() + 2.0 ** -12
+    assert ((y - both).cpu().double().abs() <= lim).all()
+    dy = torch.randn(300, 200, generator=torch.Generator().manual_seed(1)).to(F16)
+    dt, db, _ = hg.linear_grad(dy.to(DEV), b, t, dX=new(300, 16), dW=new(200, 16, t=F32))
+    _, da, _ = hg.linear_grad(dt, a, x, dW=new(16, 256, t=F32))
+    gt = ref.grads(dy, B[0], t.cpu(), torch.zeros(300, 200), "none")
+    ref.check(dt, *gt["dX"], "dT")
+    ref.check(db, *gt["dW"], "dB")
+    ref.check(da, *ref.grads(dt.cpu(), A[0], X, torch.zeros(300, 16), "none")["dW"], "dA")
