@@ -532,3 +532,5 @@ from .layer import (ACT_GELU, ACT_GELU_TANH, ACT_SILU, E4M3_BLOCK, EXPORTS_LINEA
                     linear_workspace_size)
 from .adapters import (EXPORTS_ADAPTERS, linear_adapters, linear_adapters_workspace,  # noqa: E402,F401
                        linear_adapters_workspace_size)
+from .logits import (EXPORTS_LOGPROBS, logprobs, logprobs_grad, logprobs_workspace,  # noqa: E402,F401
+                       logprobs_workspace_size)
