@@ -534,3 +534,4 @@ from .adapters import (EXPORTS_ADAPTERS, linear_adapters, linear_adapters_worksp
                        linear_adapters_workspace_size)
 from .logits import (EXPORTS_LOGPROBS, logprobs, logprobs_grad, logprobs_workspace,  # noqa: E402,F401
                        logprobs_workspace_size)
+from .optimizer import EXPORTS_ADAMW, AdamWTensors, adamw, adamw_state, adamw_tensors  # noqa: E402,F401

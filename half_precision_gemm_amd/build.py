@@ -23,7 +23,8 @@ SOURCES = [os.path.join(CSRC, "hg_api.cpp"), os.path.join(CSRC, "hg_kernels.hip"
            os.path.join(CSRC, "hg_linear_tile.hip"), os.path.join(CSRC, "hg_linear_rowwise.hip"),
            os.path.join(CSRC, "hg_linear_loose.hip"), os.path.join(CSRC, "hg_linear_outer.hip"),
            os.path.join(CSRC, "hg_adapters_api.cpp"), os.path.join(CSRC, "hg_linear_shrink.hip"),
-           os.path.join(CSRC, "hg_logprobs_api.cpp"), os.path.join(CSRC, "hg_logprobs.hip")]
+           os.path.join(CSRC, "hg_logprobs_api.cpp"), os.path.join(CSRC, "hg_logprobs.hip"),
+           os.path.join(CSRC, "hg_adamw_api.cpp"), os.path.join(CSRC, "hg_adamw.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
