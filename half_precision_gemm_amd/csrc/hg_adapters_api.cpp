@@ -58,22 +58,38 @@ struct Beside {
                               span_of(l->A, (last * l->stride_a + (r - 1) * l->lda + K) * 2),
                               span_of(l->B, (last * l->stride_b + (N - 1) * l->ldb + r) * 2)});
     }
+    bool direct_rows() const
+    {
+        return direct(X, K) && l->lda % 8 == 0 && l->stride_a % 8 == 0 && l->lda <= 2 * (int64_t)HG_LINEAR_MAX_WIDTH &&
+               (reinterpret_cast<uintptr_t>(l->A) & 15) == 0;
+    }
     int check(const Span &y, const Span &z, const Span &zs) const
     {
         return meets(y) || meets(z) || meets(zs) ? -11 : HG_OK;
     }
     int most_tile() const { return most_tile_of(l->rank); }
     void *room(Arena &a) const { return a.take(any() ? M * width_of(l->rank) * 2 : 0); }
-    hipError_t begin(lin::Product &p, Arena &a, bool few, bool bf16, hipStream_t s) const
+    hipError_t begin(lin::Product &p, Arena &a, const LinearPlan &q, bool bf16, hipStream_t s) const
     {
         if (!any())
             return hipSuccess;
         void *T = room(a);
+        const bool few = q.cut.tile == 0;
+        // (see OwnSums of hg_linear_rowwise.hip)
+        if (few && q.direct && lin::weight_blocks(N, p.f.save == lin::kSave8) == 1 && M == 1 && l->rank <= lin::kOwnRank &&
+            (N + 15) / 16 <= hg::cu_count()) {
+            p.ad = {l->which, static_cast<const uint16_t *>(l->B), nullptr, l->stride_b, l->ldb, 0, (int32_t)l->count, l->rank};
+            p.own = static_cast<const uint16_t *>(l->A);
+            p.own_scales = l->scales;
+            p.own_stride = l->stride_a;
+            p.own_ld = l->lda;
+            return hipSuccess;
+        }
         const int64_t ldt = few ? up8(l->rank) : width_of(l->rank);
         p.ad = {l->which, static_cast<const uint16_t *>(l->B), T, l->stride_b, l->ldb, ldt, (int32_t)l->count, l->rank};
         return lin::launch_shrink({static_cast<const uint16_t *>(X->data), static_cast<const uint16_t *>(l->A), l->which,
                                    l->scales, T, X->ld, l->lda, l->stride_a, ldt, (int32_t)M, (int32_t)K,
-                                   (int32_t)l->count, l->rank, few},
+                                   (int32_t)l->count, l->rank, few, direct_rows()},
                                   bf16, s);
     }
 };

@@ -74,7 +74,14 @@ struct Product {
     float *P;
     Finish f;
     Adapters ad;
+    // The adapters' A (adapter g: rank×K at own + g·own_stride) and scales, where
+    // the product computes T by itself (one row, direct operands, rank <= kOwnRank,
+    // N <= 16 per CU, no Z in 8 bits), else null.
+    const uint16_t *own;
+    const float *own_scales;
+    int64_t own_stride, own_ld;
 };
+constexpr int kOwnRank = 16;
 
 // Blocks of 16 rows of W that a workgroup of those takes: two where that still
 // gives every CU one, and for a Z in 8 bits, whose blocks of 32 columns stay in
@@ -139,7 +146,8 @@ hipError_t launch_prepare(const Slope &g, const Copy &x, const Copy &w, bool bf1
 
 // T of Adapters from X (M×K, any address) and the adapters' A (adapter g: rank×K
 // at A + g·stride), with the adapters' scales (null: 1); rows without an adapter
-// are left alone.  wide: fp32, else two 16-bit numbers.
+// are left alone.  wide: fp32, else two 16-bit numbers.  direct: rows of X and A are
+// whole 16-byte pieces at 16-byte addresses, 32-bit offsets reach 64 of them.
 struct Shrink {
     const uint16_t *X, *A;
     const int64_t *which;
@@ -147,7 +155,7 @@ struct Shrink {
     void *T;
     int64_t ldx, lda, stride, ldt;
     int32_t M, K, count, rank;
-    bool wide;
+    bool wide, direct;
 };
 hipError_t launch_shrink(const Shrink &q, bool bf16, hipStream_t s);
 
@@ -830,12 +838,14 @@ __device__ __forceinline__ int adapter_of(const Adapters &a, int row, int rows)
     const int64_t g = row < rows ? a.which[row] : -1;
     return g >= 0 && g < a.count ? (int)g : -1;
 }
-// The least of the lanes' values, the same in all of them.
-__device__ __forceinline__ int least_of_wave(int v)
+// The least of the lanes' values, the same in all of them, where lanes 16 apart
+// hold the same.
+__device__ __forceinline__ int least_of_rows(int v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        v = min(v, __shfl_xor(v, d));
+    v = min(v, __builtin_amdgcn_mov_dpp(v, 0x128, 0xf, 0xf, true));         // of 16 lanes, turned by 8, 4, 2, 1
+    v = min(v, __builtin_amdgcn_mov_dpp(v, 0x124, 0xf, 0xf, true));
+    v = min(v, __builtin_amdgcn_mov_dpp(v, 0x122, 0xf, 0xf, true));
+    v = min(v, __builtin_amdgcn_mov_dpp(v, 0x121, 0xf, 0xf, true));
     return __builtin_amdgcn_readfirstlane(v);
 }
 
@@ -847,9 +857,50 @@ __device__ __forceinline__ int least_of_wave(int v)
 // time.  A block whose rows all have this adapter takes the products as they are;
 // one with other rows among them keeps those rows' sums (a choice by lane, not
 // zeros in T: an infinity or NaN of one request's adapter stays in its rows).
-// Rows past the last are not stored and may get anything.  With prompts one
-// after the other most waves take one turn, whose loads are one wait of memory;
-// rows of different adapters side by side cost a turn each.
+// Rows past the last are not stored and may get anything.  A turn is one wait of
+// memory; from kTurns adapters on, which rows of different requests side by side
+// bring, a lane takes the rows and columns whose sums it holds, each with its own
+// row's B, and no turns are taken (add_by_rows).
+constexpr int kTurns = 4;
+template <bool BF16, int TI, int TJ>
+__device__ __forceinline__ void add_by_rows(const Product &p, const int (&mine)[TI], int row0, int col0, int lane,
+                                            floatx4 (&acc)[TI][TJ])
+{
+    const Adapters &a = p.ad;
+    const int frow = lane & 15, fhi = lane >> 4, up = (a.rank + 7) / 8 * 8;
+    for (int k = 0; k < a.rank; k += 8) {
+        const int left = a.rank - k;
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+            if (mine[i] < 0)
+                continue;
+            const uint16_t *T = static_cast<const uint16_t *>(a.T) + (row0 + 16 * i + frow) * a.ldt + k;
+            const uint16_t *B = a.B + mine[i] * a.stride + k;
+            u32x4 b[TJ][4];
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    b[j][e] = load16x8(B + min(col0 + 16 * j + 4 * fhi + e, p.N - 1) * a.ldb, left);
+            float t[8], low[8];
+            load8<BF16>(T, 8, t);
+            load8<BF16>(T + up, 8, low);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                t[q] += low[q];
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const u32x4 w = b[j][e];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        acc[i][j][e] = __builtin_fmaf(t[q], widen<BF16>((uint16_t)(w[q >> 1] >> (16 * (q & 1)))),
+                                                      acc[i][j][e]);
+                }
+        }
+    }
+}
 template <bool BF16, int TI, int TJ>
 __device__ __forceinline__ void add_adapters(const Product &p, int row0, int col0, int lane, floatx4 (&acc)[TI][TJ])
 {
@@ -860,14 +911,22 @@ __device__ __forceinline__ void add_adapters(const Product &p, int row0, int col
 #pragma unroll
     for (int i = 0; i < TI; ++i)
         mine[i] = adapter_of(a, row0 + 16 * i + frow, p.M);
-    for (int g = -1;;) {
-        int next = 0x7fffffff;
+    constexpr int NONE_LEFT = 0x7fffffff;
+    auto after = [&](int g) __attribute__((always_inline)) {
+        int next = NONE_LEFT;
 #pragma unroll
         for (int i = 0; i < TI; ++i)
-            next = min(next, mine[i] > g ? mine[i] : 0x7fffffff);
-        g = least_of_wave(next);
-        if (g == 0x7fffffff)
-            return;
+            next = min(next, mine[i] > g ? mine[i] : NONE_LEFT);
+        return least_of_rows(next);
+    };
+    int many = 0;
+    for (int g = after(-1); g != NONE_LEFT && many < kTurns; g = after(g))
+        ++many;
+    if (many == kTurns) {
+        add_by_rows<BF16>(p, mine, row0, col0, lane, acc);
+        return;
+    }
+    for (int g = after(-1); g != NONE_LEFT; g = after(g)) {
         const uint16_t *B = a.B + g * a.stride;
         for (int s = 0; s < steps; ++s) {
             const int c = 4 * s + fhi, cb = c < chunks ? c : c - chunks;      // low halves meet the same B

@@ -392,8 +392,8 @@ struct Nothing {
     int most_tile() const { return 256; }
     void room(Arena &) const {}                                             // its part of the workspace
     bool meets(const Span &) const { return false; }
-    // What is launched first; few: the product goes row by row.
-    hipError_t begin(lin::Product &, Arena &, bool, bool, hipStream_t) const { return hipSuccess; }
+    // What is launched first.
+    hipError_t begin(lin::Product &, Arena &, const LinearPlan &, bool, hipStream_t) const { return hipSuccess; }
 };
 template <int kWorkArgument, class Beside>
 int linear_call(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W, const float *bias,
@@ -473,7 +473,7 @@ int linear_call(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, co
         return status_of(lin::launch_reduce(&p, nullptr, bf16, s));
     }
     set_cut(p, q.cut, room.p);
-    if (const hipError_t e = beside.begin(p, arena, q.cut.tile == 0, bf16, s))
+    if (const hipError_t e = beside.begin(p, arena, q, bf16, s))
         return status_of(e);
     lin::Copy cx{}, cw{};
     if (q.copy_x) {

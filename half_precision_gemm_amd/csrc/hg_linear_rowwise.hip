@@ -100,6 +100,112 @@ __device__ __forceinline__ void begin_sums(const Product &p, floatx4 (&acc)[MB][
     }
 }
 
+// The same for one row and a rank of at most 16 without a launch before: every
+// workgroup computes T by itself, from X and A in L2, while W comes.  Thread t
+// takes eight k of all 16 rows of A at once, whole lines of each.  The chain from
+// `which` to A, T and B is 5 us of waits, so W's first loads are requested before
+// it, T's sums are formed behind the first stage, and what they give is added when
+// the sum over W is done.  The registers that this takes leave a CU one workgroup,
+// and every workgroup reads all of A: taken where there is one for each CU
+// (1×4096×4096 10.5 us, with the launch before 12.6; 1×16384×4096 30.9 and 29.6;
+// 2×4096×4096 in the matrix core's layout 17.2 and 12.7).
+struct NoSums {
+    __device__ __forceinline__ NoSums(const Product &, int, int) {}
+};
+template <int NB, bool BF16>
+struct OwnSums {
+    const Product &p;
+    int lane, wave, g;
+    const uint16_t *A;
+    u32x4 xs, as[kOwnRank], b[NB][4];
+    float v[kOwnRank];
+
+    __device__ __forceinline__ OwnSums(const Product &p_, int wave_, int lane_) : p(p_), lane(lane_), wave(wave_)
+    {
+        g = adapter_of(p.ad, 0, 1);
+#pragma unroll
+        for (int r = 0; r < kOwnRank; ++r)
+            v[r] = 0.0f;
+    }
+    __device__ __forceinline__ void request(int k0)
+    {
+        const uint16_t *A = p.own + max(g, 0) * p.own_stride;
+        const int k = k0 + threadIdx.x * 8, at = min(k, p.K - 8);
+        xs = *reinterpret_cast<const u32x4 *>(p.A + at) & (k < p.K ? ~0u : 0u);
+#pragma unroll
+        for (int r = 0; r < kOwnRank; ++r)
+            as[r] = *reinterpret_cast<const u32x4_any *>(A + min(r, p.ad.rank - 1) * p.own_ld + at);
+    }
+    // T's sum of this wave, value r in lanes 4r .. 4r + 3.
+    __device__ __forceinline__ float sum()
+    {
+        for (int k0 = 0;;) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] = widen<BF16>((uint16_t)(xs[e >> 1] >> (16 * (e & 1))));
+#pragma unroll
+            for (int r = 0; r < kOwnRank; ++r)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[r] = __builtin_fmaf(widen<BF16>((uint16_t)(as[r][e >> 1] >> (16 * (e & 1)))), x[e], v[r]);
+            k0 += THREADS * 8;
+            if (k0 >= p.K)
+                break;
+            request(k0);
+        }
+        // halves of the values are handed to the other half of the lanes, four times
+#pragma unroll
+        for (int n = kOwnRank / 2, d = 32; n >= 1; n /= 2, d /= 2) {
+            const bool high = (lane & d) != 0;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float give = high ? v[i] : v[i + n], keep = high ? v[i + n] : v[i];
+                v[i] = keep + __shfl_xor(give, d);
+            }
+        }
+        v[0] += __shfl_xor(v[0], 2);
+        return v[0] + __shfl_xor(v[0], 1);
+    }
+    // Adds the adapter's terms, wave w those of values 8w .. of T, lanes of row 0 to the
+    // columns that they hold; scratch: LDS that nothing else uses meanwhile.
+    __device__ __forceinline__ void add(float t, floatx4 (&acc)[1][NB], int n0, float *scratch)
+    {
+        const Adapters &a = p.ad;
+        const int k = 8 * wave;
+        const bool mine = g >= 0 && (lane & 15) == 0 && k < a.rank;
+        if (mine) {
+            const uint16_t *B = a.B + g * a.stride + k;
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    b[j][e] = load16x8(B + min(n0 + 16 * j + 4 * (lane >> 4) + e, p.N - 1) * a.ldb, a.rank - k);
+        }
+        if ((lane & 3) == 0)
+            scratch[wave * kOwnRank + lane / 4] = t;
+        __syncthreads();
+        if (!mine)
+            return;
+        const float s = p.own_scales ? p.own_scales[g] : 1.0f;
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+            float w = 0.0f;
+#pragma unroll
+            for (int i = 0; i < WAVES; ++i)
+                w += scratch[i * kOwnRank + k + h];
+            w = k + h < a.rank ? s * w : 0.0f;                    // (A's last row stands for those behind it)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const u32x4 c = b[j][e];
+                    acc[0][j][e] = __builtin_fmaf(w, widen<BF16>((uint16_t)(c[h >> 1] >> (16 * (h & 1)))), acc[0][j][e]);
+                }
+        }
+    }
+};
+
 // NB blocks of 16 rows of W, MB blocks of 16 rows of X, at any address (ODD: odd
 // elements too) and of any length.  W goes from memory straight to registers in the matrix core's
 // operand layout (lane l: row l mod 16, 8 k from 8·(l div 16) on: one 16-byte
@@ -113,7 +219,7 @@ template <int NB, int MB, bool ODD>
 struct Pieces {
     Raw<ODD> w[NB][2], x[MB][2];
 };
-template <int NB, int MB, bool ODD, bool BF16, bool ADAPT>
+template <int NB, int MB, bool ODD, bool BF16, int ADAPT>
 __global__ void __launch_bounds__(THREADS, 1) linear_rowwise_kernel(const Product p)
 {
     constexpr int DEPTH = NB * 2 + MB * 2 <= 4 ? 4 : NB * 2 + MB * 2 <= 8 ? 2 : 1;
@@ -136,7 +242,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_rowwise_kernel(const Produc
 #pragma unroll
         for (int j = 0; j < NB; ++j)
             acc[i][j] = floatx4{0, 0, 0, 0};
-    if constexpr (ADAPT)
+    if constexpr (ADAPT == 1)
         begin_sums<NB, MB, BF16>(p, acc, n0, wave, lane);
     using Piece = Pieces<NB, MB, ODD>;
     auto load = [&](int piece, Piece &q) __attribute__((always_inline)) {
@@ -239,7 +345,7 @@ constexpr int kStreamSlot = 16 * (NB + MB) * SK * 2;
 template <int NB, int MB>
 constexpr int kStreamSlots = (NB * MB <= 2 ? 80 : 160) * 1024 / kStreamSlot<NB, MB>;
 
-template <int NB, int MB, bool BF16, bool ADAPT>
+template <int NB, int MB, bool BF16, int ADAPT>
 __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const Product p)
 {
     constexpr int NS = kStreamSlots<NB, MB>, SLOT = kStreamSlot<NB, MB>;
@@ -294,14 +400,23 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const Product
 #pragma unroll
         for (int j = 0; j < NB; ++j)
             acc[i][j] = floatx4{0, 0, 0, 0};
-    if constexpr (ADAPT)
-        begin_sums<NB, MB, BF16>(p, acc, n0, wave, lane);
+    auto fill = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < NS - 1; ++s)
-        issue(s);
+        for (int s = 0; s < NS - 1; ++s)
+            issue(s);
+    };
+    if constexpr (ADAPT == 1)
+        begin_sums<NB, MB, BF16>(p, acc, n0, wave, lane);
+    fill();
+    typename std::conditional<ADAPT == 2, OwnSums<NB, BF16>, NoSums>::type own(p, wave, lane);
+    float own_t = 0.0f;
+    if constexpr (ADAPT == 2)
+        own.request(0);
     // Stage kt has landed, and every wave has read stage kt-1, whose slot takes
     // the stage NS-1 ahead.
     for (int kt = 0; kt < nk; ++kt) {
+        // (OwnSums' loads are younger than the first stages': these waits are for
+        // them too)
         wait_vmcnt<(NS - 2) * L>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
@@ -323,17 +438,27 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const Product
 #pragma unroll
             for (int j = 0; j < NB; ++j)
                 acc[i][j] = mfma_16x16x32<BF16>(w[j], x[i], acc[i][j]);
+        if constexpr (ADAPT == 2) {
+            if (kt == 0)
+                own_t = own.sum();
+        }
     }
     wait_vmcnt<0>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    if constexpr (ADAPT == 2)
+        own.add(own_t, acc, n0, reinterpret_cast<float *>(smem + WAVES * NB * 1024));
     finish_sums<NB, MB, BF16>(p, reinterpret_cast<float(*)[MB * 16][NB * 16]>(smem), acc, n0, wave, lane);
 }
 
-template <int NB, int MB, bool BF16, bool ADAPT>
+template <int NB, int MB, bool BF16, int ADAPT>
 hipError_t launch_one(const Product &p, bool stream, bool odd, hipStream_t s)
 {
+    if constexpr (ADAPT == 2)
+        return stream ? start(linear_stream_kernel<NB, MB, BF16, ADAPT>, (p.N + 16 * NB - 1) / (16 * NB), THREADS, s, p)
+                      : hipErrorInvalidConfiguration;
+    else
     return start(stream ? linear_stream_kernel<NB, MB, BF16, ADAPT>
                  : odd  ? linear_rowwise_kernel<NB, MB, true, BF16, ADAPT>
                         : linear_rowwise_kernel<NB, MB, false, BF16, ADAPT>,
@@ -343,8 +468,13 @@ hipError_t launch_one(const Product &p, bool stream, bool odd, hipStream_t s)
 template <int NB, int MB, bool BF16>
 hipError_t launch(const Product &p, bool stream, bool odd, hipStream_t s)
 {
-    return p.ad.B != nullptr ? launch_one<NB, MB, BF16, true>(p, stream, odd, s)
-                             : launch_one<NB, MB, BF16, false>(p, stream, odd, s);
+    if (p.own != nullptr) {
+        if constexpr (NB == 1 && MB == 1)
+            return launch_one<NB, MB, BF16, 2>(p, stream, odd, s);
+        return hipErrorInvalidConfiguration;
+    }
+    return p.ad.B != nullptr ? launch_one<NB, MB, BF16, 1>(p, stream, odd, s)
+                             : launch_one<NB, MB, BF16, 0>(p, stream, odd, s);
 }
 
 template <int NB, bool BF16>

@@ -5,13 +5,22 @@
 // A row costs 2·rank flops per element of X it reads, so this is the reading of
 // X and of the adapters in use.
 //
-//  * Few rows (shrink_rows_kernel): a workgroup per row and quarter of 16 of the
-//    rank, fp32 sums of a wide load's products; each row reads its adapter
-//    whatever the others' are, from L2 where they share it.
-//  * More (shrink_tile_kernel): 16 rows of X and 16 to 64 of the rank per
-//    workgroup on the matrix cores, the sum split over its waves; one turn for
-//    every adapter among the 16 rows, of which each row keeps its own's.
+//  * Few rows (shrink_rows_kernel): a workgroup per row and four values of T;
+//    each row reads its adapter whatever the others' are, from L2 where they
+//    share it.
+//  * More: 16 rows of X and 16 to 64 of the rank per workgroup on the matrix
+//    cores, the sum split over its eight waves; one turn for every adapter among
+//    the 16 rows, of which each row keeps its own's.  Where rows are few enough to
+//    leave CUs idle, several workgroups share a block's adapters (slots): most of
+//    them end at once where prompts lie one after the other, and rows of different
+//    adapters side by side are taken in parallel.
+//    shrink_stream_kernel takes X and A through a ring in LDS, 512 bytes of a row
+//    per load, shrink_tile_kernel straight into registers, at any address.
 #include "hg_linear.h"
+
+extern "C" __device__ void hg_lin_shrink_load_lds(hg::lin::i32x4 rsrc, hg::lin::lds_u32 *lds, int size, int voffset,
+                                                  int soffset, int offset,
+                                                  int aux) __asm("llvm.amdgcn.raw.buffer.load.lds");
 
 namespace hg {
 namespace lin {
@@ -97,12 +106,54 @@ __global__ void __launch_bounds__(RT) shrink_rows_kernel(const Shrink q, int par
         store_zeros(q, row, threadIdx.x, RT);
 }
 
-constexpr int TW = 8, TT = TW * 64;                               // waves and threads of shrink_tile_kernel
+constexpr int TW = 8, TT = TW * 64;                               // waves and threads of a block's workgroup
 
-// RB blocks of 16 of the rank, from 16·RB·blockIdx.y on; the rows' blocks of 16
-// are walked.
+// A workgroup's place: blocks of 16 rows, 16·RB of the rank, one of `slots` among
+// the block's workgroups.
+struct Place {
+    int blocks, slots;
+};
+// f(adapter) for this workgroup's adapters of a block, in ascending order; `mine`:
+// the adapter of the lane's row.
+template <class F>
+__device__ __forceinline__ void for_adapters(int mine, int slot, int slots, F &&f)
+{
+    int n = 0;
+    for (int g = -1;; ++n) {
+        g = least_of_rows(mine > g ? mine : 0x7fffffff);
+        if (g == 0x7fffffff)
+            return;
+        if (n % slots == slot)
+            f(g);
+    }
+}
+// The waves' sums of a block's values of T, added in order and stored in the rows
+// that have adapter g.
 template <int RB, bool BF16>
-__global__ void __launch_bounds__(TT) shrink_tile_kernel(const Shrink q, int blocks)
+__device__ __forceinline__ void end_turn(const Shrink &q, float (*part)[16][RB * 16], const floatx4 (&acc)[RB], int row0,
+                                         int r0, int g, int wave, int lane)
+{
+    const int frow = lane & 15, fhi = lane >> 4;
+    const Adapters who{q.which, nullptr, nullptr, 0, 0, 0, q.count, q.rank};
+    // (a lane holds values 4·fhi .. +3 of 16 of row frow)
+#pragma unroll
+    for (int j = 0; j < RB; ++j)
+        *reinterpret_cast<floatx4 *>(&part[wave][frow][16 * j + 4 * fhi]) = acc[j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * RB * 16; i += TT) {
+        const int r = i / (RB * 16), k = i % (RB * 16);
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < TW; ++w)
+            t += part[w][r][k];
+        if (r0 + k < q.rank && adapter_of(who, row0 + r, q.M) == g)
+            store_t<BF16>(q, row0 + r, r0 + k, q.scales ? q.scales[g] * t : t);
+    }
+    __syncthreads();
+}
+
+template <int RB, bool BF16>
+__global__ void __launch_bounds__(TT) shrink_tile_kernel(const Shrink q, const Place w)
 {
     __shared__ __attribute__((aligned(16))) float part[TW][16][RB * 16];
     const int lane = threadIdx.x & 63;
@@ -110,13 +161,10 @@ __global__ void __launch_bounds__(TT) shrink_tile_kernel(const Shrink q, int blo
     const int frow = lane & 15, fhi = lane >> 4;
     const int r0 = blockIdx.y * (RB * 16);
     const Adapters who{q.which, nullptr, nullptr, 0, 0, 0, q.count, q.rank};
-    for (int block = blockIdx.x; block < blocks; block += gridDim.x) {
+    for (int block = blockIdx.x; block < w.blocks; block += gridDim.x) {
         const int row0 = block * 16, mine = adapter_of(who, row0 + frow, q.M);
         const uint16_t *x = q.X + min(row0 + frow, q.M - 1) * q.ldx + 8 * fhi;
-        for (int g = -1;;) {
-            g = least_of_wave(mine > g ? mine : 0x7fffffff);
-            if (g == 0x7fffffff)
-                break;
+        for_adapters(mine, blockIdx.z, w.slots, [&](int g) __attribute__((always_inline)) {
             const uint16_t *a[RB];
 #pragma unroll
             for (int j = 0; j < RB; ++j)
@@ -146,7 +194,8 @@ __global__ void __launch_bounds__(TT) shrink_tile_kernel(const Shrink q, int blo
                         acc[j] = mfma_16x16x32<BF16>(as[s][j], xs[s], acc[j]);
             };
             auto plain = [](const uint16_t *p, int) __attribute__((always_inline)) {
-                return *reinterpret_cast<const u32x4_any *>(p);
+                const u32x4 v = *reinterpret_cast<const u32x4_any *>(p);
+                return v;
             };
             int piece = wave;
             for (; piece + (D - 1) * TW < whole; piece += D * TW) {
@@ -158,26 +207,100 @@ __global__ void __launch_bounds__(TT) shrink_tile_kernel(const Shrink q, int blo
                 step(piece, plain);
             if (q.K % 64 != 0 && whole % TW == wave)
                 step(whole, [](const uint16_t *p, int n) __attribute__((always_inline)) { return load16x8(p, n); });
-            // (a lane holds values 4·fhi .. +3 of 16 of row frow)
-#pragma unroll
-            for (int j = 0; j < RB; ++j)
-                *reinterpret_cast<floatx4 *>(&part[wave][frow][16 * j + 4 * fhi]) = acc[j];
-            __syncthreads();
-            for (int i = threadIdx.x; i < 16 * RB * 16; i += TT) {
-                const int r = i / (RB * 16), k = i % (RB * 16);
-                float t = 0.0f;
-#pragma unroll
-                for (int w = 0; w < TW; ++w)
-                    t += part[w][r][k];
-                if (r0 + k < q.rank && adapter_of(who, row0 + r, q.M) == g)
-                    store_t<BF16>(q, row0 + r, r0 + k, q.scales ? q.scales[g] * t : t);
-            }
-            __syncthreads();
-        }
-        if (blockIdx.y == 0)
+            end_turn<RB, BF16>(q, part, acc, row0, r0, g, wave, lane);
+        });
+        if (blockIdx.y == 0 && blockIdx.z == 0)
             for (int r = wave; r < 16; r += TW)
                 if (row0 + r < q.M)
                     store_zeros(q, row0 + r, lane, 64);
+    }
+}
+
+// The same for operands that direct loads take (rows of whole 16-byte pieces at
+// 16-byte addresses), as linear_stream_kernel of hg_linear_rowwise.hip: stages of
+// 256 k, 32 for each wave, workgroups beginning at different places of the sum.
+constexpr int SK = 256;                                           // k per stage
+template <int RB>
+constexpr int kShrinkSlot = 16 * (1 + RB) * SK * 2;
+template <int RB>
+constexpr int kShrinkSlots = 80 * 1024 / kShrinkSlot<RB> < 3 ? 3 : 80 * 1024 / kShrinkSlot<RB>;
+
+template <int RB, bool BF16>
+__global__ void __launch_bounds__(TT) shrink_stream_kernel(const Shrink q, const Place w)
+{
+    constexpr int NS = kShrinkSlots<RB>, SLOT = kShrinkSlot<RB>;
+    constexpr int ROW = SK * 2, CH = ROW / 16, RPI = 64 / CH, L = 1 + RB;     // bytes and chunks per row, rows per load
+    static_assert(SK == TW * 32 && TW * RPI == 16 && NS >= 3 && (NS - 2) * L <= 63 && TW * RB * 1024 <= NS * SLOT, "");
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[NS * SLOT];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int frow = lane & 15, fhi = lane >> 4, K = q.K;
+    const int r0 = blockIdx.y * (RB * 16), ranks = min(q.rank - r0, RB * 16);
+    const uint32_t lds_base = (uint32_t)reinterpret_cast<uintptr_t>(smem);
+    const int nk = (K + SK - 1) / SK;
+    const Adapters who{q.which, nullptr, nullptr, 0, 0, 0, q.count, q.rank};
+    const int r = wave * RPI + lane / CH, ck = ((lane % CH) ^ (r & 15)) * 8;      // this lane's row of 16 and first k
+    for (int block = blockIdx.x; block < w.blocks; block += gridDim.x) {
+        const int row0 = block * 16, rows = min(q.M - row0, 16), mine = adapter_of(who, row0 + frow, q.M);
+        const i32x4 rx = buffer_of(reinterpret_cast<uint64_t>(q.X) + (uint64_t)(row0 * q.ldx) * 2,
+                                   (uint32_t)(rows - 1) * (uint32_t)q.ldx * 2 + (uint32_t)K * 2);
+        const uint32_t ox = r < rows ? (uint32_t)r * (uint32_t)q.ldx * 2 + ck * 2 : kOutside;
+        for_adapters(mine, blockIdx.z, w.slots, [&](int g) __attribute__((always_inline)) {
+            const i32x4 ra = buffer_of(reinterpret_cast<uint64_t>(q.A) + (uint64_t)(g * q.stride + r0 * q.lda) * 2,
+                                       (uint32_t)(ranks - 1) * (uint32_t)q.lda * 2 + (uint32_t)K * 2);
+            int at = (int)(((block >> 3) + (block & 7) * (unsigned)nk / 8) % (unsigned)nk);
+            auto issue = [&](int kt) __attribute__((always_inline)) {
+                const uint32_t slot = lds_base + (kt % NS) * SLOT + wave * 1024;
+                const int k0 = at * SK;
+                const bool in = kt < nk && ck + k0 < K;
+                at = at + 1 == nk ? 0 : at + 1;
+                hg_lin_shrink_load_lds(rx, reinterpret_cast<lds_u32 *>((uintptr_t)slot), 16,
+                                       (int)(in ? ox + (uint32_t)k0 * 2 : kOutside), 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < RB; ++j) {
+                    const uint32_t o = (uint32_t)(16 * j + r) * (uint32_t)q.lda * 2 + ck * 2 + (uint32_t)k0 * 2;
+                    hg_lin_shrink_load_lds(ra, reinterpret_cast<lds_u32 *>((uintptr_t)(slot + (1 + j) * (16 * ROW))), 16,
+                                           (int)(in && 16 * j + r < ranks ? o : kOutside), 0, 0, 0);
+                }
+            };
+            floatx4 acc[RB];
+#pragma unroll
+            for (int j = 0; j < RB; ++j)
+                acc[j] = floatx4{0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < NS - 1; ++s)
+                issue(s);
+            // Stage kt has landed, and every wave has read stage kt-1, whose slot
+            // takes the stage NS-1 ahead.
+            for (int kt = 0; kt < nk; ++kt) {
+                wait_vmcnt<(NS - 2) * L>();
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+                __atomic_signal_fence(__ATOMIC_SEQ_CST);
+                const unsigned char *slot = smem + (kt % NS) * SLOT;
+                const int c = ((wave * 4 + fhi) ^ frow) * 16;
+                half8 x, a[RB];
+                x = *reinterpret_cast<const half8 *>(slot + frow * ROW + c);
+#pragma unroll
+                for (int j = 0; j < RB; ++j)
+                    a[j] = *reinterpret_cast<const half8 *>(slot + (16 * (1 + j) + frow) * ROW + c);
+                issue(kt + NS - 1);
+                wait_lgkmcnt<0>();
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < RB; ++j)
+                    acc[j] = mfma_16x16x32<BF16>(a[j], x, acc[j]);
+            }
+            // the ring's last loads (zero fills) and everyone's reads are done
+            wait_vmcnt<0>();
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            __atomic_signal_fence(__ATOMIC_SEQ_CST);
+            end_turn<RB, BF16>(q, reinterpret_cast<float(*)[16][RB * 16]>(smem), acc, row0, r0, g, wave, lane);
+        });
+        if (blockIdx.y == 0 && blockIdx.z == 0)
+            for (int i = wave; i < rows; i += TW)
+                store_zeros(q, row0 + i, lane, 64);
     }
 }
 
@@ -187,14 +310,21 @@ hipError_t shrink(const Shrink &q, hipStream_t s)
     const int parts = (q.rank + PER - 1) / PER;
     if (q.M <= kFewRows)
         return start(shrink_rows_kernel<BF16>, (int64_t)q.M * parts, RT, s, q, parts);
-    const int64_t blocks = ((int64_t)q.M + 15) / 16, grid = blocks < (1 << 20) ? blocks : 1 << 20;
-    const int rb = (q.rank + 15) / 16, per = rb > 2 ? 4 : rb;
+    const int64_t blocks = ((int64_t)q.M + 15) / 16, grid = blocks < (1 << 17) ? blocks : 1 << 17;
+    const int rb = (q.rank + 15) / 16, per = rb > 2 ? 4 : rb, ranks = (rb + per - 1) / per;
+    // four workgroups per CU, at most one per row of a block
+    int64_t slots = 4 * (int64_t)cu_count() / (blocks * ranks);
+    slots = slots < 1 ? 1 : slots > 16 ? 16 : slots;
+    const Place w{(int)blocks, (int)slots};
     auto go = [&](auto kernel) {
-        const int n = (int)blocks;
-        void *args[] = {const_cast<Shrink *>(&q), const_cast<int *>(&n)};
-        return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3((unsigned)grid, (unsigned)((rb + per - 1) / per)),
-                               dim3(TT), args, 0, s);
+        void *args[] = {const_cast<Shrink *>(&q), const_cast<Place *>(&w)};
+        return hipLaunchKernel(reinterpret_cast<const void *>(kernel),
+                               dim3((unsigned)grid, (unsigned)ranks, (unsigned)slots), dim3(TT), args, 0, s);
     };
+    if (q.direct)
+        return per == 1   ? go(shrink_stream_kernel<1, BF16>)
+               : per == 2 ? go(shrink_stream_kernel<2, BF16>)
+                          : go(shrink_stream_kernel<4, BF16>);
     return per == 1 ? go(shrink_tile_kernel<1, BF16>) : per == 2 ? go(shrink_tile_kernel<2, BF16>) : go(shrink_tile_kernel<4, BF16>);
 }
 

@@ -84,20 +84,42 @@ __device__ __forceinline__ void put(const floatx4 (&blk)[T], uint32_t stg, int l
 // Whether one of eight 16-bit numbers is infinite or NaN: its exponent is all
 // ones, so that its magnitude plus the exponent's last place carries to the sign.
 template <bool BF16>
-__device__ __forceinline__ bool not_finite(const half8 &v)
+__device__ __forceinline__ bool not_finite(const u32x4 &v)
 {
     constexpr uint32_t one = BF16 ? 0x00800080u : 0x04000400u;
-    const u32x4 w = (__builtin_bit_cast(u32x4, v) & 0x7fff7fffu) + one;
+    const u32x4 w = (v & 0x7fff7fffu) + one;
     return ((w[0] | w[1] | w[2] | w[3]) & 0x80008000u) != 0;
+}
+
+// A matrix instruction whose sums stay in their accumulation registers: left to
+// the compiler, a second place that uses all 64 blocks moves half of them to
+// vector registers and back in every turn of the K loop (376 moves, 8192×4096×4096
+// 210 -> 320 us).  The compiler does not see what it waits for: a block comes up
+// again 64 instructions later at the earliest, the K loop's other operands come
+// from LDS, whose waits it does see, and elsewhere (WAIT) the instruction waits for
+// operands that the one before wrote.  Around either place there are waits for the
+// blocks themselves.
+template <bool BF16, bool WAIT>
+__device__ __forceinline__ void multiply_in_place(const half8 &a, const half8 &b, floatx4 &c)
+{
+    if constexpr (WAIT && BF16)
+        __asm__ volatile("s_nop 3\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    else if constexpr (WAIT)
+        __asm__ volatile("s_nop 3\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    else if constexpr (BF16)
+        __asm__ volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    else
+        __asm__ volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
 
 // The adapters' terms of a wave's 64 blocks (hg_linear.h), ranks that are a
 // multiple of 8.  Accumulators that a choice or a branch touches leave their
 // registers (add_adapters() spills a thousand of them here), so this is straight
 // code: one more 32-wide step of the K loop for every adapter among the wave's 128
-// rows, T zero in the rows of others.  So that zero times an infinity or NaN of
-// this adapter's B does not reach those rows, eight numbers with one among them
-// count as zeros, and the adapter's own rows get a NaN from T instead.
+// rows, T zero in the rows of others, the next adapter's B requested under it.  So
+// that zero times an infinity or NaN of this adapter's B does not reach those rows,
+// eight numbers with one among them count as zeros, and the adapter's own rows get
+// a NaN from T instead.
 template <bool BF16>
 __device__ __forceinline__ void add_adapters_straight(const Product &p, int row0, int col0, int lane, floatx4 (&acc)[T][T])
 {
@@ -108,42 +130,54 @@ __device__ __forceinline__ void add_adapters_straight(const Product &p, int row0
 #pragma unroll
     for (int i = 0; i < T; ++i)
         mine[i] = adapter_of(a, row0 + 16 * i + frow, p.M);
-    const uint16_t *rows = static_cast<const uint16_t *>(a.T);
-    for (int g = -1;;) {
-        int next = 0x7fffffff;
+    constexpr int NONE_LEFT = 0x7fffffff;
+    auto after = [&](int g) __attribute__((always_inline)) {
+        int next = NONE_LEFT;
 #pragma unroll
         for (int i = 0; i < T; ++i)
-            next = min(next, mine[i] > g ? mine[i] : 0x7fffffff);
-        g = least_of_wave(next);
-        if (g == 0x7fffffff)
-            return;
-        for (int s = 0; s < steps; ++s) {
-            const int c = 4 * s + fhi, cb = c < chunks ? c : c < 2 * chunks ? c - chunks : 0;
+            next = min(next, mine[i] > g ? mine[i] : NONE_LEFT);
+        return least_of_rows(next);
+    };
+    const int first = after(-1);
+    if (first == NONE_LEFT)
+        return;
+    for (int s = 0; s < steps; ++s) {
+        const int c = 4 * s + fhi, cb = c < chunks ? c : c < 2 * chunks ? c - chunks : 0;
+        u32x4 b[T], ahead[T], t[T];
+        auto request = [&](int g) __attribute__((always_inline)) {
             const uint16_t *B = a.B + g * a.stride + 8 * cb;
-            half8 b[T], t[T];
 #pragma unroll
             for (int j = 0; j < T; ++j)
-                b[j] = __builtin_bit_cast(half8, *reinterpret_cast<const u32x4_any *>(B + min(col0 + 16 * j + frow, p.N - 1) * a.ldb));
+                ahead[j] = *reinterpret_cast<const u32x4_any *>(B + min(col0 + 16 * j + frow, p.N - 1) * a.ldb);
+        };
+        request(first);
 #pragma unroll
-            for (int i = 0; i < T; ++i)
-                t[i] = *reinterpret_cast<const half8 *>(rows + min(row0 + 16 * i + frow, p.M - 1) * a.ldt + 8 * c);
+        for (int i = 0; i < T; ++i)
+            t[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.T) +
+                                                    min(row0 + 16 * i + frow, p.M - 1) * a.ldt + 8 * c);
+        int g = first, next;
+        do {
             bool bad = false;
 #pragma unroll
             for (int j = 0; j < T; ++j) {
+                b[j] = ahead[j];
                 const bool x = not_finite<BF16>(b[j]);
                 bad |= x;
-                b[j] = __builtin_bit_cast(half8, __builtin_bit_cast(u32x4, b[j]) & (x ? 0u : ~0u));
+                b[j] &= x ? 0u : ~0u;
             }
+            next = after(g);
+            if (next != NONE_LEFT)
+                request(next);
             const uint32_t nan = __builtin_amdgcn_ballot_w64(bad) != 0 ? 0x7fff7fffu : 0u;
 #pragma unroll
-            for (int i = 0; i < T; ++i)
-                t[i] = __builtin_bit_cast(half8, (__builtin_bit_cast(u32x4, t[i]) | nan) & (mine[i] == g ? ~0u : 0u));
+            for (int i = 0; i < T; ++i) {
+                const half8 own = __builtin_bit_cast(half8, (t[i] | nan) & (mine[i] == g ? ~0u : 0u));
 #pragma unroll
-            for (int j = 0; j < T; ++j)
-#pragma unroll
-                for (int i = 0; i < T; ++i)
-                    acc[i][j] = mfma_16x16x32<BF16>(b[j], t[i], acc[i][j]);
-        }
+                for (int j = 0; j < T; ++j)
+                    multiply_in_place<BF16, true>(__builtin_bit_cast(half8, b[j]), own, acc[i][j]);
+            }
+            g = next;
+        } while (g != NONE_LEFT);
     }
 }
 
@@ -227,6 +261,14 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
 #pragma unroll
             for (int j = 0; j < T; ++j)
                 acc[i][j] = floatx4{0, 0, 0, 0};
+        if constexpr (ADAPT) {
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+#pragma unroll
+                for (int j = 0; j < T; ++j)
+                    __asm__ volatile("" : "+a"(acc[i][j]));
+            __asm__ volatile("s_nop 7");
+        }
         int as = 0, bs = 0;
         for (int kt = 0; kt < t.nk; ++kt) {
             const int an = as == NSA - 1 ? 0 : as + 1, a2 = an == NSA - 1 ? 0 : an + 1, bn = bs ^ 1;
@@ -248,7 +290,10 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
                     // A blocks in snake order: consecutive instructions share
                     // an operand, which draws less power
                     constexpr int j = k / TQ, a = (j & 1) ? TQ - 1 - k % TQ : k % TQ;
-                    acc[h * TQ + a][j] = mfma_16x16x32<BF16>(fb[s][j], fa[h][a], acc[h * TQ + a][j]);
+                    if constexpr (ADAPT)
+                        multiply_in_place<BF16, false>(fb[s][j], fa[h][a], acc[h * TQ + a][j]);
+                    else
+                        acc[h * TQ + a][j] = mfma_16x16x32<BF16>(fb[s][j], fa[h][a], acc[h * TQ + a][j]);
                     constexpr int op = sched(q, k);
                     if constexpr (op >= LD) {
                         if constexpr (q < 2)
@@ -268,6 +313,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
             bs = bn;
         }
         if constexpr (ADAPT) {
+            // the K loop's last results are in their registers
+            __asm__ volatile("s_nop 15\n\ts_nop 15");
             if (t.kt0 == 0)
                 add_adapters_straight<BF16>(p, t.m0 + wm * WT, t.n0 + wn * WT, lane, acc);
         }
