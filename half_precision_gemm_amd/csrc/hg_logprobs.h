@@ -13,9 +13,10 @@ constexpr int kThreads = 256;
 constexpr int kGroup = 8;                 // neighbouring logits that one lane loads together
 constexpr int kMostParts = 64;            // pieces of a row
 
-// A piece of a row: `per` groups, `groups` (1, 2, 4 or 8) for each thread.
+// A row's parts: `per` groups each, `groups` (1, 2, 4 or 8) for a lane of `waves` (1
+// or 4) waves.
 struct Parts {
-    int32_t groups, parts, per;
+    int32_t waves, groups, parts, per;
 };
 
 // What a piece leaves for its row, 16 bytes and `top` keys.

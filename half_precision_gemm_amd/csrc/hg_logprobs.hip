@@ -15,12 +15,19 @@
 // relative to its waves' maxima and are brought to one reference as they are
 // joined, always in the same order.
 //
-// The most probable k of a part: a threshold that at least k of the lanes' maxima
-// reach is found by bisection over their bits (counted with ballots), so k
-// elements reach it and only lanes counted can hold others that do: at most
-// kLanes·64 candidates, ordinarily k and a few.  They are ordered by (logit,
-// lower number first), each counting the candidates before it.  Equal maxima are
-// told apart by where their group of eight lies, in the same order.
+// The most probable k of a part: the lanes fall into 32 or 64 sets, at least k; the
+// k-th largest of the sets' maxima is reached by an element of k sets, so it is a
+// threshold that the k largest reach, and few others where large logits are
+// anywhere (k = 5 of 32 sets: 5.4 on average, 20 of 64: 24).  Only whole groups of
+// eight logits are compared with it where they lie, in registers; the few that reach
+// it go to LDS, and their logits that do are ordered there by (logit, lower number
+// first), each counting those before it.  Where there is no room for what reaches
+// it (few tokens allowed, equal logits), a threshold is found that at least k and at
+// most k + kSpare lanes' maxima reach, by bisection over their bits (counted with
+// ballots); equal maxima are told apart by where their group lies, in the same
+// order.  Then only those lanes can hold candidates, at most kLanes·64.  Measured,
+// 8192×50264 bf16, us, without the most probable 152: bisection for all k = 5 304, k
+// = 32 356; the least of 8 (32) sets' maxima 222, 304; as it is 215, 245.
 //
 // Groups of eight logits lie at multiples of 16 bytes (32 of fp32) in memory
 // whatever the row's address is, so every load is a whole one; what a row's first
@@ -41,7 +48,7 @@ using lin::u32x4;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr float kFar = -200.0f;                   // 2^kFar is 0 in fp32, and 0·kFar is 0
-constexpr int kSpare = 8, kLanes = 32 + kSpare;   // lanes that may hold candidates
+constexpr int kSpare = 8, kLanes = 32 + kSpare;   // lanes that may hold candidates after a bisection
 static_assert(HG_BF16 == 2 && HG_F16 == 0 && HG_F32 == 1, "");
 
 template <int TYPE>
@@ -66,6 +73,13 @@ __device__ __forceinline__ float without_nan(float v) { return __builtin_fmaxf(v
 template <int TYPE>
 struct Group {
     u32x4 w[kSize<TYPE> / 2];
+    // At `at` bytes of a buffer (an offset past its end: zeros).
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int at)
+    {
+#pragma unroll
+        for (int i = 0; i < kSize<TYPE> / 2; ++i)
+            w[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at + 16 * i, 0, 0));
+    }
     __device__ __forceinline__ void load(const char *p)
     {
 #pragma unroll
@@ -80,6 +94,16 @@ struct Group {
             return __builtin_bit_cast(float, u);
         else
             return lin::widen<TYPE == HG_BF16>((uint16_t)(u >> (16 * (e & 1))));
+    }
+    // The same where e is the lane's own.
+    __device__ __forceinline__ float any(int e) const
+    {
+        typename std::conditional<TYPE == HG_F32, float, uint16_t>::type v;
+        __builtin_memcpy(&v, reinterpret_cast<const char *>(w) + e * sizeof v, sizeof v);
+        if constexpr (TYPE == HG_F32)
+            return v;
+        else
+            return lin::widen<TYPE == HG_BF16>(v);
     }
     // -inf outside elements 0 .. V-1, the group's first being `first`.
     __device__ __forceinline__ void cut(int first, int V)
@@ -106,19 +130,74 @@ __device__ __forceinline__ const char *first_group(const void *X, int64_t ld, in
     return p - head * kSize<TYPE>;
 }
 
+// f of the lanes' values and the same in all lanes: neighbours, pairs, halves of
+// eight and of sixteen by DPP, the rows by swaps.  `steps`: the first so many, for
+// groups of 2^steps lanes.
+template <int steps, class T, class F>
+__device__ __forceinline__ T fold(T v, F f)
+{
+    auto moved = [&](auto c) __attribute__((always_inline)) {
+        const int w = __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), decltype(c)::value, 0xf, 0xf, true);
+        v = f(v, __builtin_bit_cast(T, w));
+    };
+    if constexpr (steps > 0)
+        moved(std::integral_constant<int, 0xb1>{});               // quad_perm 1 0 3 2
+    if constexpr (steps > 1)
+        moved(std::integral_constant<int, 0x4e>{});               // quad_perm 2 3 0 1
+    if constexpr (steps > 2)
+        moved(std::integral_constant<int, 0x141>{});              // row_half_mirror
+    if constexpr (steps > 3)
+        moved(std::integral_constant<int, 0x140>{});              // row_mirror
+    if constexpr (steps > 4) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, v);
+        const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        const uint32_t x = r[0], y = r[1];
+        v = f(__builtin_bit_cast(T, x), __builtin_bit_cast(T, y));
+    }
+    if constexpr (steps > 5) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, v);
+        const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        const uint32_t x = r[0], y = r[1];
+        v = f(__builtin_bit_cast(T, x), __builtin_bit_cast(T, y));
+    }
+    return v;
+}
 __device__ __forceinline__ float max_of_wave(float v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        v = __builtin_fmaxf(v, __shfl_xor(v, d));
-    return v;
+    return fold<6>(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
 }
 __device__ __forceinline__ float sum_of_wave(float v)
 {
+    return fold<6>(v, [](float a, float b) { return a + b; });
+}
+// The k-th largest of `sets` (32 or 64, at least k) numbers in LDS, equal ones counted
+// as often as they are there; the same in all lanes.  Every lane counts what is
+// larger than one of them (of 32, half a wave counts among either half).
+__device__ __forceinline__ uint32_t kth_largest(const uint32_t *numbers, int sets, int k)
+{
+    const int lane = threadIdx.x & 63;
+    const uint32_t mine = numbers[lane & (sets - 1)];
+    const uint32_t *from = numbers + (sets == 32 ? lane >> 5 << 4 : 0);
+    int larger = 0;
+#pragma clang loop unroll(disable)
+    for (int i = 0; i < (sets == 32 ? 16 : 64); i += 16) {
+        u32x4 w[4];
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        v += __shfl_xor(v, d);
-    return v;
+        for (int j = 0; j < 4; ++j)
+            w[j] = *reinterpret_cast<const u32x4 *>(from + i + 4 * j);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                larger += w[j][e] > mine;
+    }
+    if (sets == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap((uint32_t)larger, (uint32_t)larger, false, false);
+        larger = (int)(r[0] + r[1]);
+    }
+    // the least of those that fewer than k are larger than
+    const uint32_t v = larger < k ? mine : 0xffffffffu;
+    return fold<6>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
 }
 
 // Sums relative to `from` added to ones relative to `to` >= from: sum = Σ 2^d,
@@ -218,46 +297,77 @@ __device__ __forceinline__ void put_top(const Forward &f, int64_t row, const Row
         f.top_logp[at] = r.logp(unordered((uint32_t)(key >> 32)), f.scale);
 }
 
-template <int GR, int TYPE, bool TOP>
-__global__ void __launch_bounds__(kThreads) part_kernel(const Forward f)
+// How many of n keys are larger.  Several are read together: one by one each costs
+// LDS' latency.  (What lies behind the last is read, up to a multiple of 8, and not
+// counted.)
+__device__ __forceinline__ int larger(const uint64_t *keys, int n, uint64_t key)
 {
-    constexpr int WAVES = kThreads / 64, MOST = kLanes * GR * kGroup;
+    int count = 0;
+    for (int j = 0; j < n; j += 8) {
+        uint64_t k[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            k[e] = keys[j + e];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            count += j + e < n && k[e] > key;
+    }
+    return count;
+}
+
+// WAVES: of the workgroup; GR: groups of a lane.
+template <int WAVES, int GR, int TYPE, bool TOP>
+__global__ void __launch_bounds__(WAVES * 64, GR == 8 ? (TYPE == HG_F32 ? 4 : 5) : 6) part_kernel(const Forward f, int rows_on, int parts_on)
+{
+    constexpr int THREADS = WAVES * 64, LANES = kLanes < THREADS ? kLanes : THREADS;
+    constexpr int kFew = WAVES == 1 ? 96 : 192, MOST = LANES * GR * kGroup;
     __shared__ float wave_sums[WAVES][3];
-    __shared__ uint32_t best_hi[TOP ? kThreads : 1], best_lo[TOP ? kThreads : 1];
-    __shared__ uint64_t found[TOP ? MOST : 1];
-    __shared__ int count;
+    __shared__ __attribute__((aligned(16))) uint32_t sets[TOP ? 64 : 4];
+    __shared__ uint32_t best_hi[TOP ? THREADS : 1], best_lo[TOP ? THREADS : 1];
+    __shared__ Group<TYPE> few[TOP ? kFew : 1];
+    __shared__ int few_at[TOP ? kFew : 1];
+    __shared__ uint64_t found[TOP ? MOST + 8 : 1];
+    __shared__ int count, all;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t items = f.M * f.parts.parts;
     const float c = f.scale * kLog2e;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int64_t row = item / f.parts.parts;
-        const int part = (int)(item - row * f.parts.parts);
+    const int parts = f.parts.parts;
+    int part = blockIdx.x % (unsigned)parts;
+    for (int64_t row = blockIdx.x / (unsigned)parts; row < f.M; row += rows_on, part += parts_on) {
+        if (part >= parts) {
+            part -= parts;
+            if (++row >= f.M)
+                break;
+        }
+        const int64_t item = row * parts + part;
         int head;
         const char *p = first_group<TYPE>(f.X, f.ldx, row, head);
         const int groups = (head + f.V + kGroup - 1) / kGroup;               // of the row
         const int g0 = part * f.parts.per, n = min(groups - g0, f.parts.per);       // this part's
         Group<TYPE> x[GR];
-        // Groups past the last are loaded as the last and not looked at; of a whole
-        // wave none are.
-        auto any = [&](int i) { return i * kThreads + wave * 64 < n; };
+        const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<char *>(p) + (int64_t)g0 * (kGroup * kSize<TYPE>), 0, max(n, 0) * (kGroup * kSize<TYPE>), 0x00020000);
+        // Groups past the part's last are zeros, then -inf; of a whole wave none are
+        // looked at.
+        auto any = [&](int i) { return i * THREADS + wave * 64 < n; };
 #pragma unroll
         for (int i = 0; i < GR; ++i)
             if (any(i))
-                x[i].load(p + (int64_t)(g0 + min(i * kThreads + (int)threadIdx.x, n - 1)) * (kGroup * kSize<TYPE>));
-        float best = -__builtin_inff();
-        int best_at = g0 + threadIdx.x;
+                x[i].load(buffer, (i * THREADS + threadIdx.x) * (kGroup * kSize<TYPE>));
+        // groups 1 .. of the row that are whole, up to this part's last
+        const unsigned whole_groups = (unsigned)max(min(g0 + n, groups - 1) - 1, 0);
+        float best = -__builtin_inff(), of_group[GR];
 #pragma unroll
         for (int i = 0; i < GR; ++i) {
             if (!any(i))
                 continue;
-            const int at = i * kThreads + threadIdx.x, first = (g0 + at) * kGroup - head;
-            if (first < 0 || first + kGroup > f.V || at >= n)
-                x[i].cut(at < n ? first : f.V, f.V);
+            const int at = i * THREADS + threadIdx.x;
+            if ((unsigned)(g0 + at - 1) >= whole_groups)
+                x[i].cut(at < n ? (g0 + at) * kGroup - head : f.V, f.V);
             float m = x[i].at(0);
 #pragma unroll
             for (int e = 1; e < 8; ++e)
                 m = __builtin_fmaxf(m, x[i].at(e));
-            best_at = m > best ? g0 + at : best_at;
+            of_group[i] = m;
             best = __builtin_fmaxf(best, m);
         }
         const float m = max_of_wave(best), zero = m == -__builtin_inff() ? 0.0f : m;
@@ -275,65 +385,126 @@ __global__ void __launch_bounds__(kThreads) part_kernel(const Forward f)
         }
         sum = sum_of_wave(sum);
         weighted = sum_of_wave(weighted);
+        const int nsets = f.top > 16 ? 64 : 32;
+        if constexpr (TOP) {
+            const auto most = [](float a, float b) { return __builtin_fmaxf(a, b); };
+            const int each = THREADS / nsets;                                 // lanes of a set: 1, 2, 4 or 8
+            float set = best;
+            if constexpr (WAVES == 1)
+                set = each == 2 ? fold<1>(best, most) : best;
+            else
+                set = each == 8 ? fold<3>(best, most) : fold<2>(best, most);
+            if ((threadIdx.x & (each - 1)) == 0)
+                sets[threadIdx.x / each] = ordered(set);
+            if (threadIdx.x == 0)
+                count = all = 0;
+        }
         if (lane == 0) {
             wave_sums[wave][0] = m;
             wave_sums[wave][1] = sum;
             wave_sums[wave][2] = weighted;
-        }
-        if constexpr (TOP) {
-            best_hi[threadIdx.x] = (int)threadIdx.x < n ? ordered(best) >> kLowBit<TYPE> : 0;
-            best_lo[threadIdx.x] = ~(uint32_t)best_at;
-            if (threadIdx.x == 0)
-                count = 0;
         }
         __syncthreads();
         float largest = wave_sums[0][0], s = 0.0f, t = 0.0f;
 #pragma unroll
         for (int i = 1; i < WAVES; ++i)
             largest = __builtin_fmaxf(largest, wave_sums[i][0]);
-        const float to = largest == -__builtin_inff() ? 0.0f : largest;
-#pragma unroll
-        for (int i = 0; i < WAVES; ++i)
-            join(wave_sums[i][0], wave_sums[i][1], wave_sums[i][2], to, c, s, t);
         const bool whole = f.parts.parts == 1;
         Row r{};
-        if (whole)
-            r = finish<TYPE>(f, row, largest, s, t, threadIdx.x == 0);
-        else if (threadIdx.x == 0)
-            f.partials[item] = {largest, s, t, 0.0f};
-        if constexpr (TOP) {
-            uint32_t hi[WAVES], lo[WAVES], least, lowest;
+        if (whole || wave == 0) {
+            const float to = largest == -__builtin_inff() ? 0.0f : largest;
 #pragma unroll
-            for (int i = 0; i < WAVES; ++i) {
-                hi[i] = best_hi[i * 64 + lane];
-                lo[i] = best_lo[i * 64 + lane];
-            }
-            threshold<WAVES>(hi, lo, 32 - kLowBit<TYPE>, f.top, f.top + kSpare, least, lowest);
-            uint64_t *keys = f.keys + item * f.top;
-            // the lanes with candidates look for them
-            const uint32_t mine = (int)threadIdx.x < n ? ordered(best) >> kLowBit<TYPE> : 0;
-            if (mine > least || (mine == least && ~(uint32_t)best_at >= lowest)) {
+            for (int i = 0; i < WAVES; ++i)
+                join(wave_sums[i][0], wave_sums[i][1], wave_sums[i][2], to, c, s, t);
+            if (whole)
+                r = finish<TYPE>(f, row, largest, s, t, threadIdx.x == 0);
+            else if (threadIdx.x == 0)
+                f.partials[item] = {largest, s, t, 0.0f};
+        }
+        if constexpr (TOP) {
+            const int end = min((g0 + n) * kGroup - head, f.V);               // of this part's logits
+            // v's key, and its place among the candidates
+            auto put = [&](float v, int at) __attribute__((always_inline)) {
+                const int place = atomicAdd(&all, 1);
+                if (place < MOST)
+                    found[place] = (uint64_t)ordered(without_nan(v)) << 32 | ~(uint32_t)at;
+            };
+            const float reach = unordered(kth_largest(sets, nsets, f.top));
+            // Groups that reach it go to LDS (a lane's to places that one atomic operation
+            // has taken), where their logits are looked at by a thread each.  (A NaN
+            // never is below anything: it comes along, and goes to the end of the order.)
+            int mine = 0;
+#pragma unroll
+            for (int i = 0; i < GR; ++i)
+                if (any(i))
+                    mine += !(of_group[i] < reach);
+            if (mine > 0) {
+                int place = atomicAdd(&count, mine);
 #pragma unroll
                 for (int i = 0; i < GR; ++i) {
-                    const int at = i * kThreads + threadIdx.x, first = (g0 + at) * kGroup - head;
-                    if (at >= n)
+                    if (!any(i) || of_group[i] < reach)
                         continue;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t u = ordered(without_nan(x[i].at(e))), h = u >> kLowBit<TYPE>;
-                        const bool in = (unsigned)(first + e) < (unsigned)f.V;
-                        if (in && (h > least || (h == least && ~(uint32_t)(g0 + at) >= lowest)))
-                            found[atomicAdd(&count, 1)] = (uint64_t)u << 32 | ~(uint32_t)(first + e);
+                    if (place < kFew) {
+                        few[place] = x[i];
+                        few_at[place] = g0 + i * THREADS + threadIdx.x;
                     }
+                    ++place;
                 }
             }
             __syncthreads();
-            const int all = count;
-            for (int i = threadIdx.x; i < all; i += kThreads) {
+            const int left = count;
+            if (left <= kFew) {
+                for (int i = threadIdx.x; i < left * kGroup; i += THREADS) {
+                    const int at = few_at[i / kGroup] * kGroup - head + i % kGroup;
+                    const float v = few[i / kGroup].any(i % kGroup);
+                    if (!(v < reach) && at >= 0 && at < end)
+                        put(v, at);
+                }
+                __syncthreads();
+            }
+            if (left > kFew || all > MOST) {
+                int best_at = g0 + threadIdx.x;                               // the first group with the lane's maximum
+                float top = -__builtin_inff();
+#pragma unroll
+                for (int i = 0; i < GR; ++i) {
+                    if (!any(i))
+                        continue;
+                    best_at = of_group[i] > top ? g0 + i * THREADS + threadIdx.x : best_at;
+                    top = __builtin_fmaxf(top, of_group[i]);
+                }
+                best_hi[threadIdx.x] = (int)threadIdx.x < n ? ordered(best) >> kLowBit<TYPE> : 0;
+                best_lo[threadIdx.x] = ~(uint32_t)best_at;
+                __syncthreads();                  // (everyone has seen `all`)
+                if (threadIdx.x == 0)
+                    all = 0;
+                uint32_t hi[WAVES], lo[WAVES], least, lowest;
+#pragma unroll
+                for (int i = 0; i < WAVES; ++i) {
+                    hi[i] = best_hi[i * 64 + lane];
+                    lo[i] = best_lo[i * 64 + lane];
+                }
+                threshold<WAVES>(hi, lo, 32 - kLowBit<TYPE>, f.top, min(f.top + kSpare, LANES), least, lowest);
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < GR; ++i) {
+                    const int at = i * THREADS + threadIdx.x, first = (g0 + at) * kGroup - head;
+                    if (!any(i) || at >= n || ordered(without_nan(of_group[i])) >> kLowBit<TYPE> < least)
+                        continue;
+                    const bool ties = ~(uint32_t)(g0 + at) >= lowest;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t h = ordered(without_nan(x[i].at(e))) >> kLowBit<TYPE>;
+                        if ((h > least || (h == least && ties)) && first + e >= 0 && first + e < end)
+                            put(x[i].at(e), first + e);
+                    }
+                }
+                __syncthreads();
+            }
+            uint64_t *keys = f.keys + item * f.top;
+            const int candidates = all;
+            for (int i = threadIdx.x; i < candidates; i += THREADS) {
                 const uint64_t key = found[i];
-                int place = 0;
-                for (int j = 0; j < all; ++j)
-                    place += found[j] > key;
+                const int place = larger(found, candidates, key);
                 if (place < f.top) {
                     if (whole)
                         put_top(f, row, r, place, key);
@@ -342,7 +513,7 @@ __global__ void __launch_bounds__(kThreads) part_kernel(const Forward f)
                 }
             }
             if (!whole)                           // fewer elements than `top`
-                for (int i = all + threadIdx.x; i < f.top; i += kThreads)
+                for (int i = candidates + threadIdx.x; i < f.top; i += THREADS)
                     keys[i] = 0;
         }
         __syncthreads();
@@ -353,7 +524,8 @@ __global__ void __launch_bounds__(kThreads) part_kernel(const Forward f)
 template <int E, int TYPE>
 __global__ void __launch_bounds__(kThreads) join_kernel(const Forward f)
 {
-    __shared__ uint64_t found[kThreads / 64][64];
+    __shared__ uint64_t found[kThreads / 64][64 + 8];
+    __shared__ __attribute__((aligned(16))) uint32_t sets[kThreads / 64][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, parts = f.parts.parts;
     const float c = f.scale * kLog2e;
     for (int64_t row = (int64_t)blockIdx.x * (kThreads / 64) + wave; row < f.M; row += (int64_t)gridDim.x * (kThreads / 64)) {
@@ -377,12 +549,35 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Forward f)
             hi[i] = (uint32_t)(k >> 32);
             lo[i] = (uint32_t)k;
         }
-        // the keys are all different, so that at most 64 are left
-        threshold<E>(hi, lo, 32, f.top, 64, least, lowest);
+        // What the largest keys of `top` lanes reach; if that is more than 64 keys,
+        // what a threshold leaves: they are all different.
+        auto reaching = [&](int i) __attribute__((always_inline)) {
+            return hi[i] != 0 && (hi[i] > least || (hi[i] == least && lo[i] >= lowest));
+        };
+        auto count = [&]() __attribute__((always_inline)) {
+            int c = 0;
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                c += __builtin_popcountll(__builtin_amdgcn_ballot_w64(reaching(i)));
+            return c;
+        };
+        least = lowest = 0;
+        if constexpr (E > 1) {
+            uint32_t most = hi[0];
+#pragma unroll
+            for (int i = 1; i < E; ++i)
+                most = max(most, hi[i]);
+            sets[wave][lane] = most;
+            __atomic_signal_fence(__ATOMIC_SEQ_CST);
+            least = kth_largest(sets[wave], 64, f.top);
+            __atomic_signal_fence(__ATOMIC_SEQ_CST);
+            if (count() > 64)
+                threshold<E>(hi, lo, 32, f.top, 64, least, lowest);
+        }
         int n = 0;
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            const bool in = hi[i] != 0 && (hi[i] > least || (hi[i] == least && lo[i] >= lowest));
+            const bool in = reaching(i);
             const uint64_t who = __builtin_amdgcn_ballot_w64(in);
             if (in)
                 found[wave][n + __builtin_popcountll(who & ((1ull << lane) - 1))] = (uint64_t)hi[i] << 32 | lo[i];
@@ -392,9 +587,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Forward f)
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
         if (lane < n) {
             const uint64_t key = found[wave][lane];
-            int place = 0;
-            for (int j = 0; j < n; ++j)
-                place += found[wave][j] > key;
+            const int place = larger(found[wave], n, key);
             if (place < f.top)
                 put_top(f, row, r, place, key);
         }
@@ -481,25 +674,34 @@ __global__ void __launch_bounds__(kThreads) gradient_kernel(const Backward b, in
 
 int64_t grid_of(int64_t items) { return items < (1 << 22) ? items : 1 << 22; }
 
-template <int GR, int TYPE>
+template <int WAVES, int GR, int TYPE>
 hipError_t parts(const Forward &f, hipStream_t s)
 {
-    return start(f.top > 0 ? part_kernel<GR, TYPE, true> : part_kernel<GR, TYPE, false>, grid_of(f.M * f.parts.parts),
-                 kThreads, s, f);
+    const int64_t grid = grid_of(f.M * f.parts.parts);
+    return start(f.top > 0 ? part_kernel<WAVES, GR, TYPE, true> : part_kernel<WAVES, GR, TYPE, false>, grid, WAVES * 64, s, f,
+                 (int)(grid / f.parts.parts), (int)(grid % f.parts.parts));
+}
+template <int WAVES, int TYPE>
+hipError_t parts(const Forward &f, hipStream_t s)
+{
+    return f.parts.groups == 1   ? parts<WAVES, 1, TYPE>(f, s)
+           : f.parts.groups == 2 ? parts<WAVES, 2, TYPE>(f, s)
+           : f.parts.groups == 4 ? parts<WAVES, 4, TYPE>(f, s)
+                                 : parts<WAVES, 8, TYPE>(f, s);
 }
 template <int TYPE>
 hipError_t forward(const Forward &f, hipStream_t s)
 {
-    const hipError_t e = f.parts.groups == 1   ? parts<1, TYPE>(f, s)
-                         : f.parts.groups == 2 ? parts<2, TYPE>(f, s)
-                         : f.parts.groups == 4 ? parts<4, TYPE>(f, s)
-                                               : parts<8, TYPE>(f, s);
+    const hipError_t e = f.parts.waves == 1 ? parts<1, TYPE>(f, s) : parts<4, TYPE>(f, s);
     if (e != hipSuccess || f.parts.parts == 1)
         return e;
     const int keys = f.parts.parts * f.top;
     if (f.parts.parts > 128 || keys > 33 * 64)
         return hipErrorInvalidConfiguration;
-    return start(keys <= 64 ? join_kernel<1, TYPE> : keys <= 256 ? join_kernel<4, TYPE> : join_kernel<33, TYPE>,
+    return start(keys <= 64    ? join_kernel<1, TYPE>
+                 : keys <= 256 ? join_kernel<4, TYPE>
+                 : keys <= 512 ? join_kernel<8, TYPE>
+                               : join_kernel<33, TYPE>,
                  grid_of((f.M + kThreads / 64 - 1) / (kThreads / 64)), kThreads, s, f);
 }
 template <int TYPE>

@@ -19,18 +19,23 @@ namespace probs = hg::probs;
 bool is_logits(int type) { return type == HG_F16 || type == HG_BF16 || type == HG_F32; }
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Pieces that rows are cut into: as long as they come (16384 logits, a load of
-// 16 bytes or two for each of a lane's eight groups) if that gives every CU two,
-// else shorter ones, down to 2048.
+// Parts that rows are cut into: as long as they come (16384 logits, a load of 16
+// bytes or two for each of a lane's eight groups) if that gives every CU two, else
+// shorter ones, down to 2048.  Rows of up to 4096 logits go to a wave each.
 probs::Parts parts_of(int64_t M, int64_t V)
 {
     const int64_t groups = (V + 2 * probs::kGroup - 2) / probs::kGroup;       // wherever in one a row begins
     int64_t per = 8;
+    if (groups <= 8 * 64) {
+        while (per > 1 && groups <= per / 2 * 64)
+            per /= 2;
+        return {1, (int32_t)per, 1, (int32_t)groups};
+    }
     auto parts = [&](int64_t g) { return (groups + g * probs::kThreads - 1) / (g * probs::kThreads); };
     while (per > 1 && (parts(per / 2) == 1 || (M * parts(per) < 2 * hg::cu_count() && parts(per / 2) <= probs::kMostParts)))
         per /= 2;
     const int64_t n = parts(per);
-    return {(int32_t)per, (int32_t)n, (int32_t)((groups + n - 1) / n)};
+    return {4, (int32_t)per, (int32_t)n, (int32_t)((groups + n - 1) / n)};
 }
 
 int check(int64_t M, int64_t V)
