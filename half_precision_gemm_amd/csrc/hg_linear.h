@@ -838,6 +838,72 @@ __device__ __forceinline__ int adapter_of(const Adapters &a, int row, int rows)
     const int64_t g = row < rows ? a.which[row] : -1;
     return g >= 0 && g < a.count ? (int)g : -1;
 }
+// Elements k .. k + 7 of row `row` of an adapter's B (cols rows of `rank`), zeros
+// behind the rank.  What follows a row in memory is loaded with it and cut off, but
+// for the last rows, behind which nothing may be: those element by element.
+__device__ __forceinline__ u32x4 load_b(const Adapters &a, const uint16_t *B, int row, int cols, int k)
+{
+    const int n = a.rank - k;
+    const int64_t at = row * a.ldb + k;
+    u32x4 w = {0, 0, 0, 0};
+    if (n >= 8 || at + 8 <= (cols - 1) * a.ldb + a.rank) {
+        w = *reinterpret_cast<const u32x4_any *>(B + at);
+    } else {
+#pragma clang loop unroll(disable)
+        for (int e = 0; e < n; ++e) {
+            const uint32_t u = (uint32_t)B[at + e] << (16 * (e & 1));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] |= e >> 1 == j ? u : 0u;
+        }
+    }
+    if (n < 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] &= n >= 2 * e + 2 ? ~0u : n == 2 * e + 1 ? 0xffffu : 0u;
+    }
+    return w;
+}
+// acc[j][e] += Σ T(k)·B(col0 + 16j + e, k) over k .. k + 7 of the rank: a lane's
+// columns of one row, whose T is `eight` (of k .. k + 7) or `one` (of a k), and whose
+// adapter's B is B.  A last piece of less than eight goes one by one: loads that may
+// be whole or not fill the instruction cache with both (333×1111×777, rank 9, 20 us
+// of 27).
+template <bool BF16, int TJ, class EIGHT, class ONE>
+__device__ __forceinline__ void add_eight(const Product &p, const uint16_t *B, int col0, int k, floatx4 (&acc)[TJ],
+                                          EIGHT &&eight, ONE &&one)
+{
+    const Adapters &a = p.ad;
+    if (k + 8 <= a.rank) {
+        u32x4 b[TJ][4];
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                b[j][e] = *reinterpret_cast<const u32x4_any *>(B + min(col0 + 16 * j + e, p.N - 1) * a.ldb + k);
+        float t[8];
+        eight(t);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const u32x4 w = b[j][e];
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    acc[j][e] = __builtin_fmaf(t[q], widen<BF16>((uint16_t)(w[q >> 1] >> (16 * (q & 1)))), acc[j][e]);
+            }
+    } else {
+#pragma clang loop unroll(disable)
+        for (int r = k; r < a.rank; ++r) {
+            const float t = one(r);
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[j][e] = __builtin_fmaf(t, widen<BF16>(B[min(col0 + 16 * j + e, p.N - 1) * a.ldb + r]), acc[j][e]);
+        }
+    }
+}
 // The least of the lanes' values, the same in all of them, where lanes 16 apart
 // hold the same.
 __device__ __forceinline__ int least_of_rows(int v)
@@ -869,35 +935,22 @@ __device__ __forceinline__ void add_by_rows(const Product &p, const int (&mine)[
     const Adapters &a = p.ad;
     const int frow = lane & 15, fhi = lane >> 4, up = (a.rank + 7) / 8 * 8;
     for (int k = 0; k < a.rank; k += 8) {
-        const int left = a.rank - k;
 #pragma unroll
         for (int i = 0; i < TI; ++i) {
             if (mine[i] < 0)
                 continue;
-            const uint16_t *T = static_cast<const uint16_t *>(a.T) + (row0 + 16 * i + frow) * a.ldt + k;
-            const uint16_t *B = a.B + mine[i] * a.stride + k;
-            u32x4 b[TJ][4];
-#pragma unroll
-            for (int j = 0; j < TJ; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    b[j][e] = load16x8(B + min(col0 + 16 * j + 4 * fhi + e, p.N - 1) * a.ldb, left);
-            float t[8], low[8];
-            load8<BF16>(T, 8, t);
-            load8<BF16>(T + up, 8, low);
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                t[q] += low[q];
-#pragma unroll
-            for (int j = 0; j < TJ; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const u32x4 w = b[j][e];
+            const uint16_t *T = static_cast<const uint16_t *>(a.T) + (row0 + 16 * i + frow) * a.ldt;
+            add_eight<BF16>(
+                p, a.B + mine[i] * a.stride, col0 + 4 * fhi, k, acc[i],
+                [&](float (&t)[8]) __attribute__((always_inline)) {
+                    float low[8];
+                    load8<BF16>(T + k, 8, t);
+                    load8<BF16>(T + up + k, 8, low);
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        acc[i][j][e] = __builtin_fmaf(t[q], widen<BF16>((uint16_t)(w[q >> 1] >> (16 * (q & 1)))),
-                                                      acc[i][j][e]);
-                }
+                        t[q] += low[q];
+                },
+                [&](int r) __attribute__((always_inline)) { return widen<BF16>(T[r]) + widen<BF16>(T[up + r]); });
         }
     }
 }
@@ -929,12 +982,12 @@ __device__ __forceinline__ void add_adapters(const Product &p, int row0, int col
     for (int g = after(-1); g != NONE_LEFT; g = after(g)) {
         const uint16_t *B = a.B + g * a.stride;
         for (int s = 0; s < steps; ++s) {
-            const int c = 4 * s + fhi, cb = c < chunks ? c : c - chunks;      // low halves meet the same B
-            const int left = c < 2 * chunks ? a.rank - 8 * cb : 0;
+            // low halves meet the same B, the zeros behind them its first eight
+            const int c = 4 * s + fhi, cb = c < chunks ? c : c < 2 * chunks ? c - chunks : 0;
             half8 b[TJ], t[TI];
 #pragma unroll
             for (int j = 0; j < TJ; ++j)
-                b[j] = __builtin_bit_cast(half8, load16x8(B + min(col0 + 16 * j + frow, p.N - 1) * a.ldb + 8 * cb, left));
+                b[j] = __builtin_bit_cast(half8, load_b(a, B, min(col0 + 16 * j + frow, p.N - 1), p.N, 8 * cb));
 #pragma unroll
             for (int i = 0; i < TI; ++i)
                 t[i] = *reinterpret_cast<const half8 *>(static_cast<const uint16_t *>(a.T) +

@@ -59,10 +59,10 @@ __device__ __forceinline__ void finish_sums(const Product &p, float (*part)[MB *
 }
 
 // Where a workgroup's sums begin: at what the rows' adapters add (hg_linear.h,
-// Adapters), or at zero.  Wave w takes the rank's eighths w, w + 8, ..: a lane the
-// columns and rows whose sums it holds, with T in fp32 and eight of B in one load
-// for each of them, so that 64 rows of 64 adapters cost what those of one do, and
-// no more than one wait of memory for B up to a rank of 64.
+// Adapters), or at zero.  The waves share the rank's eighths and the blocks of 16
+// rows: a lane takes the columns and rows whose sums it holds, with T in fp32 and
+// eight of B in one load for each of them, so that 64 rows of 64 adapters cost what
+// those of one do.
 template <int NB, int MB, bool BF16>
 __device__ __forceinline__ void begin_sums(const Product &p, floatx4 (&acc)[MB][NB], int n0, int wave, int lane)
 {
@@ -72,30 +72,24 @@ __device__ __forceinline__ void begin_sums(const Product &p, floatx4 (&acc)[MB][
 #pragma unroll
     for (int i = 0; i < MB; ++i)
         mine[i] = adapter_of(a, 16 * i + frow, p.M);
-    for (int k = 8 * wave; k < a.rank; k += 8 * WAVES) {
-        const int left = a.rank - k;
+    // `split` waves share an eighth, each every split-th block of rows
+    const int chunks = (a.rank + 7) / 8, split = chunks >= WAVES ? 1 : chunks > 2 ? 2 : 4;
+    for (int k = wave / split * 8; k < a.rank; k += 8 * WAVES / split) {
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
-            if (mine[i] < 0)
+            if ((i & (split - 1)) != (wave & (split - 1)) || mine[i] < 0)
                 continue;
-            const float *T = static_cast<const float *>(a.T) + (16 * i + frow) * a.ldt + k;
-            const floatx4 lo = *reinterpret_cast<const floatx4 *>(T), hi = *reinterpret_cast<const floatx4 *>(T + 4);
-            const uint16_t *B = a.B + mine[i] * a.stride + k;
-            u32x4 b[NB][4];
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    b[j][e] = load16x8(B + min(n0 + 16 * j + 4 * fhi + e, p.N - 1) * a.ldb, left);
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
+            const float *T = static_cast<const float *>(a.T) + (16 * i + frow) * a.ldt;
+            add_eight<BF16>(
+                p, a.B + mine[i] * a.stride, n0 + 4 * fhi, k, acc[i],
+                [&](float (&t)[8]) __attribute__((always_inline)) {
+                    const floatx4 lo = *reinterpret_cast<const floatx4 *>(T + k);
+                    const floatx4 hi = *reinterpret_cast<const floatx4 *>(T + k + 4);
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        acc[i][j][e] = __builtin_fmaf(q < 4 ? lo[q] : hi[q - 4],
-                                                      widen<BF16>((uint16_t)(b[j][e][q >> 1] >> (16 * (q & 1)))),
-                                                      acc[i][j][e]);
+                        t[q] = q < 4 ? lo[q] : hi[q - 4];
+                },
+                [&](int r) __attribute__((always_inline)) { return T[r]; });
         }
     }
 }
@@ -117,7 +111,7 @@ struct OwnSums {
     const Product &p;
     int lane, wave, g;
     const uint16_t *A;
-    u32x4 xs, as[kOwnRank], b[NB][4];
+    u32x4 xs, as[kOwnRank];
     float v[kOwnRank];
 
     __device__ __forceinline__ OwnSums(const Product &p_, int wave_, int lane_) : p(p_), lane(lane_), wave(wave_)
@@ -171,38 +165,28 @@ struct OwnSums {
     // columns that they hold; scratch: LDS that nothing else uses meanwhile.
     __device__ __forceinline__ void add(float t, floatx4 (&acc)[1][NB], int n0, float *scratch)
     {
-        const Adapters &a = p.ad;
-        const int k = 8 * wave;
-        const bool mine = g >= 0 && (lane & 15) == 0 && k < a.rank;
-        if (mine) {
-            const uint16_t *B = a.B + g * a.stride + k;
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    b[j][e] = load16x8(B + min(n0 + 16 * j + 4 * (lane >> 4) + e, p.N - 1) * a.ldb, a.rank - k);
-        }
         if ((lane & 3) == 0)
             scratch[wave * kOwnRank + lane / 4] = t;
         __syncthreads();
-        if (!mine)
+        const int k = 8 * wave;
+        if (g < 0 || (lane & 15) != 0 || k >= p.ad.rank)
             return;
         const float s = p.own_scales ? p.own_scales[g] : 1.0f;
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
+        const auto one = [&](int r) __attribute__((always_inline)) {
             float w = 0.0f;
 #pragma unroll
             for (int i = 0; i < WAVES; ++i)
-                w += scratch[i * kOwnRank + k + h];
-            w = k + h < a.rank ? s * w : 0.0f;                    // (A's last row stands for those behind it)
+                w += scratch[i * kOwnRank + r];
+            return s * w;
+        };
+        add_eight<BF16>(
+            p, p.ad.B + g * p.ad.stride, n0 + 4 * (lane >> 4), k, acc[0],
+            [&](float (&v)[8]) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const u32x4 c = b[j][e];
-                    acc[0][j][e] = __builtin_fmaf(w, widen<BF16>((uint16_t)(c[h >> 1] >> (16 * (h & 1)))), acc[0][j][e]);
-                }
-        }
+                for (int h = 0; h < 8; ++h)
+                    v[h] = one(k + h);
+            },
+            one);
     }
 };
 
@@ -405,9 +389,11 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const Product
         for (int s = 0; s < NS - 1; ++s)
             issue(s);
     };
+    // (The adapters' loads are younger than the first stages': those come while
+    // these are on their way.)
+    fill();
     if constexpr (ADAPT == 1)
         begin_sums<NB, MB, BF16>(p, acc, n0, wave, lane);
-    fill();
     typename std::conditional<ADAPT == 2, OwnSums<NB, BF16>, NoSums>::type own(p, wave, lane);
     float own_t = 0.0f;
     if constexpr (ADAPT == 2)

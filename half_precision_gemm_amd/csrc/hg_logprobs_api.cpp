@@ -2,7 +2,6 @@
 // include/hgemm_logprobs.h.
 #include "hgemm_logprobs.h"
 
-#include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -79,7 +78,7 @@ int hg_logprobs(int64_t M, int64_t V, const hg_matrix *X, float scale, const int
         return e;
     if (X == nullptr || !is_logits(X->type) || !valid(X, M, V))
         return -3;
-    if (!(scale > 0.0f) || !isfinite(scale))
+    if (!(scale > 0.0f && scale <= HG_LOGPROBS_MAX_SCALE))
         return -4;
     if (!aligned(tokens, 8) || (logp != nullptr && tokens == nullptr))
         return -5;
@@ -148,7 +147,7 @@ int hg_logprobs_grad(int64_t M, int64_t V, const hg_matrix *X, float scale, cons
         return e;
     if (X == nullptr || !is_logits(X->type) || !valid(X, M, V))
         return -3;
-    if (!(scale > 0.0f) || !isfinite(scale))
+    if (!(scale > 0.0f && scale <= HG_LOGPROBS_MAX_SCALE))
         return -4;
     if (!aligned(tokens, 8) || (dlogp != nullptr && tokens == nullptr))
         return -5;

@@ -20,9 +20,10 @@
 extern "C" {
 #endif
 
-/* Largest number of logits in a row, and of the most probable tokens. */
+/* Largest number of logits in a row, of the most probable tokens, and scale. */
 #define HG_LOGPROBS_MAX_VOCABULARY (1 << 20)
 #define HG_LOGPROBS_MAX_TOP 32
+#define HG_LOGPROBS_MAX_SCALE 1e30f
 
 /*
  * hg_logprobs — one pass over the logits.
@@ -30,7 +31,7 @@ extern "C" {
  *  1 M           : rows, at most HG_LINEAR_MAX_ROWS.
  *  2 V           : logits in a row, at least 1.
  *  3 X           : M×V, HG_F16, HG_BF16 or HG_F32.
- *  4 scale       : finite and above 0 (1 / temperature).
+ *  4 scale       : above 0, at most HG_LOGPROBS_MAX_SCALE (1 / temperature).
  *  5 tokens      : M values, or NULL; outside 0 .. V-1: none.
  *  6 logp        : M fp32 values log p[token], 0 where there is none, or NULL
  *                  (with tokens NULL it must be).

@@ -52,7 +52,7 @@ LONG = dict(V=40000, X=(P[0], 40000))                # several parts: a workspac
     (dict(M=-1), -1), (dict(M=(1 << 30) + 1), -1), (dict(V=0), -2), (dict(V=(1 << 20) + 1), -2), (dict(X=NULL), -3),
     (dict(X=(P[0], 99)), -3), (dict(X=(P[0], 100, E4M3)), -3), (dict(X=(P[0] + 1, 100)), -3),
     (dict(X=(P[0] + 2, 100, F32)), -3), (dict(X=(None, 100)), -3), (dict(scale=0.0), -4), (dict(scale=-1.0), -4),
-    (dict(scale=INF), -4), (dict(scale=float("nan")), -4), (dict(tokens=None), -5), (dict(tokens=P[1] + 4), -5),
+    (dict(scale=INF), -4), (dict(scale=float("nan")), -4), (dict(scale=1.1e30), -4), (dict(tokens=None), -5), (dict(tokens=P[1] + 4), -5),
     (dict(logp=P[2] + 2), -6), (dict(entropy=P[3] + 1), -7), (dict(stats=P[4] + 2), -8), (dict(top=-1), -9),
     (dict(top=33), -9), (dict(top=5, V=4), -9), (dict(ids=P[5] + 4), -10), (dict(tl=P[6] + 2), -11),
     (dict(logp=P[0] + 4), -6), (dict(logp=P[1]), -6), (dict(entropy=P[2] + 12), -7), (dict(stats=P[3] + 8), -8),
