@@ -864,45 +864,48 @@ __device__ __forceinline__ u32x4 load_b(const Adapters &a, const uint16_t *B, in
     }
     return w;
 }
-// acc[j][e] += Σ T(k)·B(col0 + 16j + e, k) over k .. k + 7 of the rank: a lane's
-// columns of one row, whose T is `eight` (of k .. k + 7) or `one` (of a k), and whose
-// adapter's B is B.  A last piece of less than eight goes one by one: loads that may
-// be whole or not fill the instruction cache with both (333×1111×777, rank 9, 20 us
-// of 27).
-template <bool BF16, int TJ, class EIGHT, class ONE>
-__device__ __forceinline__ void add_eight(const Product &p, const uint16_t *B, int col0, int k, floatx4 (&acc)[TJ],
-                                          EIGHT &&eight, ONE &&one)
+// acc[j][e] += Σ t[q]·B(col0 + 16j + e, k + q), eight of the rank from k on: a lane's
+// columns of one row, whose adapter's B is B.  (This runs a few times in a wave, so
+// that its length counts too: a last piece of the rank that is not whole goes through
+// add_singly; with masks or shifts here 333×1111×777, rank 9, took 24 us for 21.
+// At ranks that are not a multiple of 8 the loads' odd addresses cost more than
+// either: 207×64×128 of 17 adapters, rank 24 18 us, 27 31.)
+template <bool BF16, int TJ>
+__device__ __forceinline__ void add_eight(const Adapters &a, const uint16_t *B, int col0, int cols, int k, const float (&t)[8],
+                                          floatx4 *acc)
 {
-    const Adapters &a = p.ad;
-    if (k + 8 <= a.rank) {
-        u32x4 b[TJ][4];
+    u32x4 b[TJ][4];
 #pragma unroll
-        for (int j = 0; j < TJ; ++j)
+    for (int j = 0; j < TJ; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                b[j][e] = *reinterpret_cast<const u32x4_any *>(B + min(col0 + 16 * j + e, p.N - 1) * a.ldb + k);
-        float t[8];
-        eight(t);
+        for (int e = 0; e < 4; ++e)
+            b[j][e] = *reinterpret_cast<const u32x4_any *>(B + min(col0 + 16 * j + e, cols - 1) * a.ldb + k);
 #pragma unroll
-        for (int j = 0; j < TJ; ++j)
+    for (int j = 0; j < TJ; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const u32x4 w = b[j][e];
+        for (int e = 0; e < 4; ++e) {
+            const u32x4 w = b[j][e];
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    acc[j][e] = __builtin_fmaf(t[q], widen<BF16>((uint16_t)(w[q >> 1] >> (16 * (q & 1)))), acc[j][e]);
-            }
-    } else {
-#pragma clang loop unroll(disable)
-        for (int r = k; r < a.rank; ++r) {
-            const float t = one(r);
-#pragma unroll
-            for (int j = 0; j < TJ; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[j][e] = __builtin_fmaf(t, widen<BF16>(B[min(col0 + 16 * j + e, p.N - 1) * a.ldb + r]), acc[j][e]);
+            for (int q = 0; q < 8; ++q)
+                acc[j][e] = __builtin_fmaf(t[q], widen<BF16>((uint16_t)(w[q >> 1] >> (16 * (q & 1)))), acc[j][e]);
         }
-    }
+}
+// The same for one of the rank.
+template <bool BF16, int TJ>
+__device__ __forceinline__ void add_singly(const Adapters &a, const uint16_t *B, int col0, int cols, int r, float t,
+                                           floatx4 *acc)
+{
+    uint16_t b[TJ][4];
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            b[j][e] = B[min(col0 + 16 * j + e, cols - 1) * a.ldb + r];
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc[j][e] = __builtin_fmaf(t, widen<BF16>(b[j][e]), acc[j][e]);
 }
 // The least of the lanes' values, the same in all of them, where lanes 16 apart
 // hold the same.
@@ -934,23 +937,33 @@ __device__ __forceinline__ void add_by_rows(const Product &p, const int (&mine)[
 {
     const Adapters &a = p.ad;
     const int frow = lane & 15, fhi = lane >> 4, up = (a.rank + 7) / 8 * 8;
-    for (int k = 0; k < a.rank; k += 8) {
+    const uint16_t *T = static_cast<const uint16_t *>(a.T) + (row0 + frow) * a.ldt;
+    int k = 0;
+    for (; k + 8 <= a.rank; k += 8) {
 #pragma unroll
         for (int i = 0; i < TI; ++i) {
             if (mine[i] < 0)
                 continue;
-            const uint16_t *T = static_cast<const uint16_t *>(a.T) + (row0 + 16 * i + frow) * a.ldt;
-            add_eight<BF16>(
-                p, a.B + mine[i] * a.stride, col0 + 4 * fhi, k, acc[i],
-                [&](float (&t)[8]) __attribute__((always_inline)) {
-                    float low[8];
-                    load8<BF16>(T + k, 8, t);
-                    load8<BF16>(T + up + k, 8, low);
+            float t[8], low[8];
+            load8<BF16>(T + 16 * i * a.ldt + k, 8, t);
+            load8<BF16>(T + 16 * i * a.ldt + up + k, 8, low);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        t[q] += low[q];
-                },
-                [&](int r) __attribute__((always_inline)) { return widen<BF16>(T[r]) + widen<BF16>(T[up + r]); });
+            for (int q = 0; q < 8; ++q)
+                t[q] += low[q];
+#pragma unroll
+            for (int j = 0; j < TJ; j += 2)
+                add_eight<BF16, 2>(a, a.B + mine[i] * a.stride, col0 + 4 * fhi + 16 * j, p.N, k, t, acc[i] + j);
+        }
+    }
+#pragma clang loop unroll(disable)
+    for (; k < a.rank; ++k) {
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+            if (mine[i] < 0)
+                continue;
+            const uint16_t *t = T + 16 * i * a.ldt + k;
+            add_singly<BF16, TJ>(a, a.B + mine[i] * a.stride, col0 + 4 * fhi, p.N, k, widen<BF16>(t[0]) + widen<BF16>(t[up]),
+                                 acc[i]);
         }
     }
 }

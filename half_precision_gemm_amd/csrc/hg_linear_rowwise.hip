@@ -80,16 +80,16 @@ __device__ __forceinline__ void begin_sums(const Product &p, floatx4 (&acc)[MB][
             if ((i & (split - 1)) != (wave & (split - 1)) || mine[i] < 0)
                 continue;
             const float *T = static_cast<const float *>(a.T) + (16 * i + frow) * a.ldt;
-            add_eight<BF16>(
-                p, a.B + mine[i] * a.stride, n0 + 4 * fhi, k, acc[i],
-                [&](float (&t)[8]) __attribute__((always_inline)) {
-                    const floatx4 lo = *reinterpret_cast<const floatx4 *>(T + k);
-                    const floatx4 hi = *reinterpret_cast<const floatx4 *>(T + k + 4);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        t[q] = q < 4 ? lo[q] : hi[q - 4];
-                },
-                [&](int r) __attribute__((always_inline)) { return T[r]; });
+            const uint16_t *B = a.B + mine[i] * a.stride;
+            if (k + 8 <= a.rank) {
+                const floatx4 lo = *reinterpret_cast<const floatx4 *>(T + k), hi = *reinterpret_cast<const floatx4 *>(T + k + 4);
+                const float t[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                add_eight<BF16, NB>(a, B, n0 + 4 * fhi, p.N, k, t, acc[i]);
+            } else {
+#pragma clang loop unroll(disable)
+                for (int r = k; r < a.rank; ++r)
+                    add_singly<BF16, NB>(a, B, n0 + 4 * fhi, p.N, r, T[r], acc[i]);
+            }
         }
     }
 }
@@ -179,14 +179,19 @@ struct OwnSums {
                 w += scratch[i * kOwnRank + r];
             return s * w;
         };
-        add_eight<BF16>(
-            p, p.ad.B + g * p.ad.stride, n0 + 4 * (lane >> 4), k, acc[0],
-            [&](float (&v)[8]) __attribute__((always_inline)) {
+        const uint16_t *B = p.ad.B + g * p.ad.stride;
+        const int col0 = n0 + 4 * (lane >> 4);
+        if (k + 8 <= p.ad.rank) {
+            float v[8];
 #pragma unroll
-                for (int h = 0; h < 8; ++h)
-                    v[h] = one(k + h);
-            },
-            one);
+            for (int h = 0; h < 8; ++h)
+                v[h] = one(k + h);
+            add_eight<BF16, NB>(p.ad, B, col0, p.N, k, v, acc[0]);
+        } else {
+#pragma clang loop unroll(disable)
+            for (int r = k; r < p.ad.rank; ++r)
+                add_singly<BF16, NB>(p.ad, B, col0, p.N, r, one(r), acc[0]);
+        }
     }
 };
 

@@ -222,13 +222,16 @@ __global__ void __launch_bounds__(TT) shrink_tile_kernel(const Shrink q, const P
 constexpr int SK = 256;                                           // k per stage
 template <int RB>
 constexpr int kShrinkSlot = 16 * (1 + RB) * SK * 2;
-template <int RB>
-constexpr int kShrinkSlots = 80 * 1024 / kShrinkSlot<RB> < 3 ? 3 : 80 * 1024 / kShrinkSlot<RB>;
+// Two workgroups to a CU, or, DEEP, one with all of its LDS: where there are no more
+// than CUs, more of each one's stages in flight (87×64×15424, rank 63, with 16 of the
+// rank in a workgroup instead of 64: 47 -> 32 us for the whole layer).
+template <int RB, bool DEEP>
+constexpr int kShrinkSlots = DEEP ? 10 : 80 * 1024 / kShrinkSlot<RB> < 3 ? 3 : 80 * 1024 / kShrinkSlot<RB>;
 
-template <int RB, bool BF16>
+template <int RB, bool DEEP, bool BF16>
 __global__ void __launch_bounds__(TT) shrink_stream_kernel(const Shrink q, const Place w)
 {
-    constexpr int NS = kShrinkSlots<RB>, SLOT = kShrinkSlot<RB>;
+    constexpr int NS = kShrinkSlots<RB, DEEP>, SLOT = kShrinkSlot<RB>;
     constexpr int ROW = SK * 2, CH = ROW / 16, RPI = 64 / CH, L = 1 + RB;     // bytes and chunks per row, rows per load
     static_assert(SK == TW * 32 && TW * RPI == 16 && NS >= 3 && (NS - 2) * L <= 63 && TW * RB * 1024 <= NS * SLOT, "");
     __shared__ __attribute__((aligned(1024))) unsigned char smem[NS * SLOT];
@@ -311,9 +314,11 @@ hipError_t shrink(const Shrink &q, hipStream_t s)
     if (q.M <= kFewRows)
         return start(shrink_rows_kernel<BF16>, (int64_t)q.M * parts, RT, s, q, parts);
     const int64_t blocks = ((int64_t)q.M + 15) / 16, grid = blocks < (1 << 17) ? blocks : 1 << 17;
-    const int rb = (q.rank + 15) / 16, per = rb > 2 ? 4 : rb, ranks = (rb + per - 1) / per;
-    // four workgroups per CU, at most one per row of a block
-    int64_t slots = 4 * (int64_t)cu_count() / (blocks * ranks);
+    const int rb = (q.rank + 15) / 16;
+    const bool deep = blocks * rb <= cu_count();
+    const int per = deep ? 1 : rb > 2 ? 4 : rb, ranks = (rb + per - 1) / per;
+    // one or four workgroups per CU, at most one per row of a block
+    int64_t slots = (deep ? 1 : 4) * (int64_t)cu_count() / (blocks * ranks);
     slots = slots < 1 ? 1 : slots > 16 ? 16 : slots;
     const Place w{(int)blocks, (int)slots};
     auto go = [&](auto kernel) {
@@ -322,9 +327,10 @@ hipError_t shrink(const Shrink &q, hipStream_t s)
                                dim3((unsigned)grid, (unsigned)ranks, (unsigned)slots), dim3(TT), args, 0, s);
     };
     if (q.direct)
-        return per == 1   ? go(shrink_stream_kernel<1, BF16>)
-               : per == 2 ? go(shrink_stream_kernel<2, BF16>)
-                          : go(shrink_stream_kernel<4, BF16>);
+        return deep       ? go(shrink_stream_kernel<1, true, BF16>)
+               : per == 1 ? go(shrink_stream_kernel<1, false, BF16>)
+               : per == 2 ? go(shrink_stream_kernel<2, false, BF16>)
+                          : go(shrink_stream_kernel<4, false, BF16>);
     return per == 1 ? go(shrink_tile_kernel<1, BF16>) : per == 2 ? go(shrink_tile_kernel<2, BF16>) : go(shrink_tile_kernel<4, BF16>);
 }
 
