@@ -259,3 +259,59 @@ def test_training_an_adapter_with_the_layer(hg):
     ref.check(dt, *gt["dX"], "dT")
     ref.check(db, *gt["dW"], "dB")
     ref.check(da, *ref.grads(dt.cpu(), A[0], X, torch.zeros(300, 16), "none")["dW"], "dA")
+
+
+def test_one_a_for_all(hg):
+    """A broadcast over the adapters, B their own."""
+    M, N, K, rank = 70, 96, 128, 16
+    X, W, A, B, s, which = operands(M, N, K, rank, 4, BF16, "single")
+    A = A[:1].expand(4, rank, K)
+    Y = torch.empty(M, N, dtype=BF16, device=DEV)
+    hg.linear_adapters(X.to(DEV), W.to(DEV), Y, which.to(DEV), A[:1].to(DEV).expand(4, rank, K), B.to(DEV), scales=s.to(DEV))
+    y, _, ey, _ = expected(X, W, A, B, s, which, None, "none", None)
+    ref.check(Y, y, ey, "Y")
+
+
+@pytest.mark.parametrize("M", [1, 9])
+def test_a_decoding_step(hg, M):
+    """What a server runs for the next tokens: a projection with the requests' adapters onto the residual stream, the
+    head, the most probable tokens; captured, replayed with other requests."""
+    from test_gpu_logprobs import close, order
+    from test_gpu_logprobs import expected as distribution
+    K, V, rank, count, k = 256, 3001, 16, 5, 6
+    X, W, A, B, s, which = (x.to(DEV) for x in operands(M, K, K, rank, count, BF16, "single"))
+    g = torch.Generator().manual_seed(3)
+    head = (torch.randn(V, K, generator=g) / 8).to(BF16).to(DEV)
+    h, stream = (torch.randn(M, K, generator=g).to(BF16).to(DEV) for _ in range(2))
+    logits = torch.empty(M, V, dtype=F32, device=DEV)
+    entropy, top = torch.empty(M, device=DEV), (torch.empty(M, k, dtype=torch.int64, device=DEV), torch.empty(M, k, device=DEV))
+    work, hwork = hg.linear_adapters_workspace(X, W, A), hg.linear_workspace(h, head)
+    pwork = hg.logprobs_workspace(logits, k)
+
+    def step():
+        hg.linear_adapters(X, W, h, which, A, B, scales=s, residual=stream, work=work)
+        hg.linear(h, head, logits, work=hwork)
+        hg.logprobs(logits, entropy=entropy, top=top, work=pwork)
+
+    with torch.cuda.stream(torch.cuda.Stream()):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(3):
+        x = torch.randn(M, K, generator=g).to(BF16)
+        w = torch.randint(-1, count, (M,), generator=g)
+        X.copy_(x)
+        which.copy_(w)
+        graph.replay()
+        torch.cuda.synchronize()
+        y, _, ey, _ = expected(x, W.cpu(), A.cpu(), B.cpu(), s.cpu(), w, None, "none", stream.cpu())
+        ref.check(h, y, ey, "h")
+        z, _, ez, _ = ref.linear(h.cpu(), head.cpu())
+        ref.check(logits, z, ez, "logits")
+        v, b = distribution(logits.cpu(), 1.0)
+        ids = order(logits.cpu(), k)
+        assert torch.equal(top[0].cpu(), ids)
+        close(top[1], v["logp"].gather(1, ids), b["logp"].gather(1, ids), "top")
+        close(entropy, v["entropy"][:, 0], b["entropy"][:, 0], "entropy")

@@ -358,3 +358,24 @@ def test_two_calls_at_once(hg):
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1]) and torch.equal(g[3][0], w[3][0])
+
+
+def test_more_rows_than_a_launch_has_workgroups(hg):
+    """Workgroups that go on to further rows, of one part and of several."""
+    for M, V, k in (((1 << 22) + 77, 9, 3), ((1 << 20) + 7, 4100, 1)):
+        g = torch.Generator(device=DEV).manual_seed(M)
+        x = (3 * torch.randn(M, V, generator=g, device=DEV)).to(BF16)
+        tokens = torch.randint(0, V, (M,), generator=g, device=DEV)
+        logp, stats = torch.full((M,), 9.0, device=DEV), torch.empty(M, 2, device=DEV)
+        ids = torch.full((M, k), -5, dtype=torch.int64, device=DEV)
+        hg.logprobs(x, tokens, logp=logp, stats=stats, top=(ids, None))
+        rows = torch.cat((torch.arange(50), torch.randint(0, M, (200,), generator=torch.Generator().manual_seed(1)),
+                          torch.arange(M - 100, M)))
+        some, tok = x[rows.to(DEV)].cpu(), tokens[rows.to(DEV)].cpu()
+        v, b = expected(some, 1.0)
+        close(logp[rows.to(DEV)], v["logp"].gather(1, tok[:, None])[:, 0], b["logp"].gather(1, tok[:, None])[:, 0], "logp")
+        assert torch.equal(ids[rows.to(DEV)].cpu(), order(some, k))
+        assert (logp <= 1e-4).all() and (ids >= 0).all()                     # every row was written
+        hg.logprobs_grad(x, tokens, stats, x, dlogp=torch.ones(M, device=DEV))
+        want, err = gradient(some, tok, 1.0, torch.ones(len(rows)), None, v, b)
+        ref.check(x[rows.to(DEV)], want, err, "dX")
