@@ -20,16 +20,28 @@ namespace adamw = hg::adamw;
 bool is_float(int type) { return type == HG_F16 || type == HG_BF16 || type == HG_F32; }
 bool good(const void *p, int64_t size) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(size - 1)) == 0; }
 
-// A tensor's arrays: what is written, then the gradient.
+// A tensor's arrays that are there: what is written, then the gradient.
 struct Arrays {
     Span a[7];
+    int count = 0;
+    void add(const void *p, int64_t bytes)
+    {
+        if (p != nullptr && bytes > 0)
+            a[count++] = span_of(p, bytes);
+    }
 };
 Arrays arrays_of(const hg_adamw_tensor &t)
 {
     const int64_t n = t.n, s = t.state_type == HG_E4M3 ? blocks8(n) : 0, e = esize(t.state_type);
-    return {{span_of(t.param, n * esize(t.param_type)), span_of(t.master, t.master != nullptr ? n * 4 : 0),
-             span_of(t.m, n * e), span_of(t.v, n * e), span_of(t.m_scales, s), span_of(t.v_scales, s),
-             span_of(t.grad, n * esize(t.grad_type))}};
+    Arrays x;
+    x.add(t.param, n * esize(t.param_type));
+    x.add(t.master, n * 4);
+    x.add(t.m, n * e);
+    x.add(t.v, n * e);
+    x.add(t.m_scales, s);
+    x.add(t.v_scales, s);
+    x.add(t.grad, n * esize(t.grad_type));
+    return x;
 }
 bool valid(const hg_adamw_tensor &t)
 {
@@ -44,8 +56,8 @@ bool valid(const hg_adamw_tensor &t)
     if (t.state_type == HG_E4M3 && (t.m_scales == nullptr || t.v_scales == nullptr))
         return false;
     const Arrays x = arrays_of(t);
-    for (int i = 0; i < 6; ++i)
-        for (int j = i + 1; j < 7; ++j)
+    for (int i = 0; i < x.count; ++i)
+        for (int j = i + 1; j < x.count; ++j)
             if (meet(x.a[i], x.a[j]))
                 return false;
     return true;
@@ -81,9 +93,8 @@ int hg_adamw_check(int64_t count, const hg_adamw_tensor *tensors)
         all.reserve((size_t)count * 7);
         for (int64_t i = 0; i < count; ++i) {
             const Arrays x = arrays_of(tensors[i]);
-            for (int j = 0; j < 7; ++j)
-                if (x.a[j].lo < x.a[j].hi)
-                    all.push_back({x.a[j], j < 6});
+            for (int j = 0; j < x.count; ++j)
+                all.push_back({x.a[j], j + 1 < x.count});
         }
         std::sort(all.begin(), all.end(), [](const Edge &a, const Edge &b) { return a.s.lo < b.s.lo; });
         uintptr_t any = 0, written = 0;           // the ends so far
@@ -122,9 +133,9 @@ int hg_adamw(int64_t count, const hg_adamw_tensor *tensors, int64_t step, const 
     if ((reinterpret_cast<uintptr_t>(factors) & 3) != 0)
         return -10;
     const Span st = span_of(device_step, 8), f = span_of(factors, 8);
-    for (int64_t i = 0; i < count; ++i) {
+    for (int64_t i = 0; i < count && (device_step != nullptr || factors != nullptr); ++i) {
         const Arrays x = arrays_of(tensors[i]);
-        for (int j = 0; j < 6; ++j) {
+        for (int j = 0; j + 1 < x.count; ++j) {
             if (meet(x.a[j], st))
                 return -4;
             if (meet(x.a[j], f))
@@ -132,7 +143,7 @@ int hg_adamw(int64_t count, const hg_adamw_tensor *tensors, int64_t step, const 
         }
     }
     adamw::Batch b;
-    b.count = b.pieces = 0;
+    b.count = b.pieces = b.used = 0;
     b.beta1 = (float)beta1;
     b.rest1 = (float)(1.0 - beta1);
     b.beta2 = (float)beta2;
@@ -157,14 +168,30 @@ int hg_adamw(int64_t count, const hg_adamw_tensor *tensors, int64_t step, const 
         if (t.n == 0)
             continue;
         const int64_t n = (t.n + adamw::piece_of(b.each) - 1) / adamw::piece_of(b.each);
-        if (b.count == adamw::kMost || b.pieces + n > hg::lin::kMostBlocks) {
+        const bool state8 = t.state_type == HG_E4M3;
+        const int words = adamw::kFewest + (t.master != nullptr ? 1 : 0) + (state8 ? 2 : 0);
+        if (b.count == adamw::kMost || b.used + words > adamw::kWords || b.pieces + n > hg::lin::kMostBlocks) {
             if (const hipError_t e = adamw::launch(b, s))
                 return status_of(e);
-            b.count = b.pieces = 0;
+            b.count = b.pieces = b.used = 0;
         }
-        b.first[b.count] = b.pieces;
-        b.t[b.count++] = {t.param, t.master, t.grad, t.m, t.m_scales, t.v, t.v_scales, t.n, (int32_t)i,
-                          (int8_t)t.param_type, (int8_t)t.grad_type, (int8_t)(t.state_type == HG_E4M3)};
+        b.place[b.count++] = {b.pieces, b.used};
+        const uint64_t numbers = (uint64_t)t.n | (uint64_t)i << adamw::kPlace | (uint64_t)t.param_type << adamw::kParam |
+                                 (uint64_t)t.grad_type << adamw::kGrad |
+                                 (uint64_t)(t.master != nullptr) << adamw::kMaster | (uint64_t)state8 << adamw::kState8;
+        void **w = b.words + b.used;
+        b.used += words;
+        *w++ = t.param;
+        *w++ = const_cast<void *>(t.grad);
+        *w++ = t.m;
+        *w++ = t.v;
+        *w++ = reinterpret_cast<void *>(numbers);
+        if (t.master != nullptr)
+            *w++ = t.master;
+        if (state8) {
+            *w++ = t.m_scales;
+            *w++ = t.v_scales;
+        }
         b.pieces += (int32_t)n;
     }
     return b.count > 0 ? status_of(adamw::launch(b, s)) : HG_OK;

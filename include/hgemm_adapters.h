@@ -8,7 +8,8 @@
  *
  * Conventions as in hgemm_linear.h.  Two launches (three or four where hg_linear
  * takes two or three): X·A_gᵀ, then the layer's product, whose kernels add the
- * second half to their sums before anything is rounded.
+ * second half to their sums before anything is rounded.  One row with adapters
+ * of a small rank takes one launch.
  *
  * An adapter is trained with what is there for any layer: T = X·Aᵀ and T·Bᵀ are
  * two hg_linear calls, their gradients two of hg_linear_grad.
@@ -57,9 +58,10 @@ typedef struct hg_adapters {
  * kept in fp32 (few rows) or as the sum of two numbers of X's type, off by at
  * most 2^-16 (HG_BF16) or 2^-22 (HG_F16, and 2^-25 where that is more) of it;
  * in HG_F16 a value past 65504 is infinite there.  Rows whose adapter's B_g holds
- * an infinity or NaN may come out NaN in any column.  A row's result does not
- * depend on the other rows: what is not finite in one request's row or adapter
- * stays in that request's rows.
+ * an infinity or NaN may come out NaN in any column.  Nothing of another row
+ * enters a row's result (its last bits may differ with the rows beside it, which
+ * choose the order of its sums): what is not finite in one request's row or
+ * adapter stays in that request's rows.
  */
 int hg_linear_adapters(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W,
                        const float *bias, const hg_matrix *R, const hg_matrix *Y, const hg_matrix *Z,

@@ -151,7 +151,7 @@ class Buffers:
             if self.bits == 32:
                 self.m[sl], self.v[sl] = torch.from_numpy(m), torch.from_numpy(v)
             else:
-                r = bits(seed, t, i + place0, 0, n)
+                r = bits(seed, t, place0(i) if callable(place0) else i + place0, 0, n)
                 for x, y, q, keep in ((self.m, m, r & np.uint32(0xffff), False), (self.v, v, r >> np.uint32(16), True)):
                     c, e = rounded(y, q, keep)
                     x[0][sl], x[1][bl] = torch.from_numpy(c), torch.from_numpy(e)
@@ -361,3 +361,23 @@ def test_a_training_step(hg):
     ref.check(master.flatten(), want, err, "master")
     r = bits(5, 1, 0, 0, V * K)
     assert np.array_equal(m[0].cpu().flatten().numpy(), rounded(nm, r & np.uint32(0xffff), False)[0])
+
+
+@pytest.mark.parametrize("t,bits,master,most", [(F32, 32, False, 83), (BF16, 32, True, 69), (BF16, 8, False, 59), (F16, 8, True, 51)])
+@pytest.mark.parametrize("more", [-1, 0, 1])
+def test_as_many_as_a_launch_takes(hg, t, bits, master, most, more):
+    """Of each kind of tensor, and one less and one more."""
+    b = Buffers([1 + 37 * i % 101 for i in range(most + more)], t, bits, master)
+    hg.adamw(b.tensors(hg), 4, LR, (B1, B2), EPS, DECAY, seed=6)
+    b.check(4, 6)
+
+
+def test_kinds_in_turn(hg):
+    """Tensors of all kinds in one call, in an order in which none follows its like."""
+    kinds = [(F32, 32, False), (BF16, 8, True), (F16, 8, False), (BF16, 32, True), (F16, 32, False), (F32, 8, False)]
+    bs = [Buffers([1 + (i * 53 + k * 7) % 90 for i in range(20)], *kind, seed=k) for k, kind in enumerate(kinds)]
+    lists = {key: [b.parts(key) or [None] * 20 for b in bs] for key in "pgmvw"}
+    turn = {key: [x[i] for i in range(20) for x in xs] for key, xs in lists.items()}
+    hg.adamw(hg.adamw_tensors(*(turn[k] for k in "pgmv"), masters=turn["w"]), 3, LR, (B1, B2), EPS, DECAY, seed=8)
+    for k, b in enumerate(bs):
+        b.check(3, 8, place0=lambda i: len(kinds) * i + k)
