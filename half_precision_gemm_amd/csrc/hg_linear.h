@@ -147,7 +147,7 @@ hipError_t launch_prepare(const Slope &g, const Copy &x, const Copy &w, bool bf1
 // T of Adapters from X (M×K, any address) and the adapters' A (adapter g: rank×K
 // at A + g·stride), with the adapters' scales (null: 1); rows without an adapter
 // are left alone.  wide: fp32, else two 16-bit numbers.  direct: rows of X and A are
-// whole 16-byte pieces at 16-byte addresses, 32-bit offsets reach 64 of them.
+// whole 16-byte pieces at 16-byte addresses, 32-bit offsets reach 256 of X's.
 struct Shrink {
     const uint16_t *X, *A;
     const int64_t *which;

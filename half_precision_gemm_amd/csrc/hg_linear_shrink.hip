@@ -8,12 +8,13 @@
 //  * Few rows (shrink_rows_kernel): a workgroup per row and four values of T;
 //    each row reads its adapter whatever the others' are, from L2 where they
 //    share it.
-//  * More: 16 rows of X and 16 to 64 of the rank per workgroup on the matrix
-//    cores, the sum split over its eight waves; one turn for every adapter among
-//    the 16 rows, of which each row keeps its own's.  Where rows are few enough to
-//    leave CUs idle, several workgroups share a block's adapters (slots): most of
-//    them end at once where prompts lie one after the other, and rows of different
-//    adapters side by side are taken in parallel.
+//  * More: 16 rows of X that share an adapter and 16 to 64 of the rank per
+//    workgroup on the matrix cores, the sum split over its eight waves.  The rows
+//    are gathered from a block of 256, so an adapter is read once or twice for all of
+//    a block's rows that have it: with 16 neighbours and a turn for every adapter
+//    among them, rows in no order read the adapters several times as often
+//    (8192×4096, 64 adapters of rank 16 in no order: 206 us for 46; one adapter
+//    to 128 neighbours on average: 22 for 18).
 //    shrink_stream_kernel takes X and A through a ring in LDS, 512 bytes of a row
 //    per load, shrink_tile_kernel straight into registers, at any address.
 #include "hg_linear.h"
@@ -108,47 +109,112 @@ __global__ void __launch_bounds__(RT) shrink_rows_kernel(const Shrink q, int par
 
 constexpr int TW = 8, TT = TW * 64;                               // waves and threads of a block's workgroup
 
-// A workgroup's place: blocks of 16 rows, 16·RB of the rank, one of `slots` among
-// the block's workgroups.
+// A workgroup's place: blocks of kRows rows, 16·RB of the rank, one of `slots` among
+// the block's workgroups, each of which takes every slots-th piece.
+constexpr int kRows = 256;
 struct Place {
     int blocks, slots;
 };
-// f(adapter) for this workgroup's adapters of a block, in ascending order; `mine`:
-// the adapter of the lane's row.
-template <class F>
-__device__ __forceinline__ void for_adapters(int mine, int slot, int slots, F &&f)
+// A piece: up to 16 rows of a block with the same adapter, in their order.
+// Thread t < kRows knows row t's adapter, how many rows before it have the same one,
+// and, of a piece's first row, its number (others: -1); count: the block's pieces.
+struct Pieces {
+    int g, before, number, count;
+};
+// Rows with the same adapter are found bit by bit of its number, 64 at a time: a
+// ballot says which rows have the bit (comparing with each of the rows took 1 us
+// more).
+__device__ __forceinline__ Pieces pieces_of(const Shrink &q, int row0, int lane, int wave, int *lds)
 {
-    int n = 0;
-    for (int g = -1;; ++n) {
-        g = least_of_rows(mine > g ? mine : 0x7fffffff);
-        if (g == 0x7fffffff)
-            return;
-        if (n % slots == slot)
-            f(g);
+    constexpr int SETS = kRows / 64;
+    static_assert(TW >= SETS, "");
+    int *const firsts = lds + 32;                                 // (behind what rows_of writes)
+    Pieces m{-1, 0, -1, 0};
+    uint64_t marks = 0;
+    if (wave < SETS) {
+        const Adapters who{q.which, nullptr, nullptr, 0, 0, 0, q.count, q.rank};
+        int v[SETS];
+        uint64_t same[SETS];
+#pragma unroll
+        for (int j = 0; j < SETS; ++j)
+            v[j] = adapter_of(who, row0 + 64 * j + lane, q.M);
+#pragma unroll
+        for (int j = 0; j < SETS; ++j) {
+            same[j] = __ballot(v[j] >= 0);
+            m.g = j == wave ? v[j] : m.g;
+        }
+        for (int bit = 0; q.count >> bit > 0; ++bit) {
+            const uint64_t mine = (m.g >> bit & 1) != 0 ? 0 : ~(uint64_t)0;
+#pragma unroll
+            for (int j = 0; j < SETS; ++j)
+                same[j] &= __ballot((v[j] >> bit & 1) != 0) ^ mine;
+        }
+#pragma unroll
+        for (int j = 0; j < SETS; ++j)
+            m.before += j < wave    ? __builtin_popcountll(same[j])
+                        : j == wave ? __builtin_popcountll(same[j] & (((uint64_t)1 << lane) - 1))
+                                    : 0;
+        const bool first = m.g >= 0 && m.before % 16 == 0;
+        marks = __ballot(first);
+        m.number = first ? __builtin_popcountll(marks & (((uint64_t)1 << lane) - 1)) : -1;
+        if (lane == 0)
+            firsts[wave] = __builtin_popcountll(marks);
     }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < SETS; ++w) {
+        m.number += w < wave && m.number >= 0 ? firsts[w] : 0;
+        m.count += firsts[w];
+    }
+    m.count = __builtin_amdgcn_readfirstlane(m.count);
+    return m;
 }
-// The waves' sums of a block's values of T, added in order and stored in the rows
-// that have adapter g.
+// Piece c's adapter, and in lanes l, l + 16, ... its row l within the block (-1: none).
+__device__ __forceinline__ int rows_of(const Pieces &m, int c, int *lds, int &g)
+{
+    if (threadIdx.x < 16)
+        lds[threadIdx.x] = -1;
+    if (m.number == c) {
+        lds[16] = m.g;
+        lds[17] = m.before;
+    }
+    __syncthreads();
+    g = __builtin_amdgcn_readfirstlane(lds[16]);
+    const unsigned i = (unsigned)(m.before - lds[17]);
+    if (m.g == g && i < 16)
+        lds[i] = threadIdx.x;
+    __syncthreads();
+    const int row = lds[threadIdx.x & 15];
+    __syncthreads();
+    return row;
+}
+// The waves' sums of a piece's values of T, added in order and stored.
 template <int RB, bool BF16>
-__device__ __forceinline__ void end_turn(const Shrink &q, float (*part)[16][RB * 16], const floatx4 (&acc)[RB], int row0,
-                                         int r0, int g, int wave, int lane)
+__device__ __forceinline__ void end_piece(const Shrink &q, float (*part)[16][RB * 16], const floatx4 (&acc)[RB], int row0,
+                                          int row, int r0, int g, int wave, int lane)
 {
     const int frow = lane & 15, fhi = lane >> 4;
-    const Adapters who{q.which, nullptr, nullptr, 0, 0, 0, q.count, q.rank};
     // (a lane holds values 4·fhi .. +3 of 16 of row frow)
 #pragma unroll
     for (int j = 0; j < RB; ++j)
         *reinterpret_cast<floatx4 *>(&part[wave][frow][16 * j + 4 * fhi]) = acc[j];
     __syncthreads();
+    // (whole waves take part or none of them)
     for (int i = threadIdx.x; i < 16 * RB * 16; i += TT) {
-        const int r = i / (RB * 16), k = i % (RB * 16);
+        const int r = i / (RB * 16), k = i % (RB * 16), to = __shfl(row, r);
         float t = 0.0f;
 #pragma unroll
         for (int w = 0; w < TW; ++w)
             t += part[w][r][k];
-        if (r0 + k < q.rank && adapter_of(who, row0 + r, q.M) == g)
-            store_t<BF16>(q, row0 + r, r0 + k, q.scales ? q.scales[g] * t : t);
+        if (r0 + k < q.rank && to >= 0)
+            store_t<BF16>(q, row0 + to, r0 + k, q.scales ? q.scales[g] * t : t);
     }
+    if (r0 == 0)
+        for (int r = wave; r < 16; r += TW) {
+            const int to = __builtin_amdgcn_readlane(row, r);
+            if (to >= 0)
+                store_zeros(q, row0 + to, lane, 64);
+        }
     __syncthreads();
 }
 
@@ -160,11 +226,14 @@ __global__ void __launch_bounds__(TT) shrink_tile_kernel(const Shrink q, const P
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int frow = lane & 15, fhi = lane >> 4;
     const int r0 = blockIdx.y * (RB * 16);
-    const Adapters who{q.which, nullptr, nullptr, 0, 0, 0, q.count, q.rank};
+    int *const lds = reinterpret_cast<int *>(part);
     for (int block = blockIdx.x; block < w.blocks; block += gridDim.x) {
-        const int row0 = block * 16, mine = adapter_of(who, row0 + frow, q.M);
-        const uint16_t *x = q.X + min(row0 + frow, q.M - 1) * q.ldx + 8 * fhi;
-        for_adapters(mine, blockIdx.z, w.slots, [&](int g) __attribute__((always_inline)) {
+        const int row0 = block * kRows;
+        const Pieces m = pieces_of(q, row0, lane, wave, lds);
+        for (int c = blockIdx.z; c < m.count; c += w.slots) {
+            int g;
+            const int row = rows_of(m, c, lds, g);
+            const uint16_t *x = q.X + (row0 + max(row, 0)) * q.ldx + 8 * fhi;
             const uint16_t *a[RB];
 #pragma unroll
             for (int j = 0; j < RB; ++j)
@@ -207,12 +276,9 @@ __global__ void __launch_bounds__(TT) shrink_tile_kernel(const Shrink q, const P
                 step(piece, plain);
             if (q.K % 64 != 0 && whole % TW == wave)
                 step(whole, [](const uint16_t *p, int n) __attribute__((always_inline)) { return load16x8(p, n); });
-            end_turn<RB, BF16>(q, part, acc, row0, r0, g, wave, lane);
-        });
-        if (blockIdx.y == 0 && blockIdx.z == 0)
-            for (int r = wave; r < 16; r += TW)
-                if (row0 + r < q.M)
-                    store_zeros(q, row0 + r, lane, 64);
+            end_piece<RB, BF16>(q, part, acc, row0, row, r0, g, wave, lane);
+        }
+        __syncthreads();                  // (the next block's pieces_of writes what this one's reads)
     }
 }
 
@@ -241,17 +307,20 @@ __global__ void __launch_bounds__(TT) shrink_stream_kernel(const Shrink q, const
     const int r0 = blockIdx.y * (RB * 16), ranks = min(q.rank - r0, RB * 16);
     const uint32_t lds_base = (uint32_t)reinterpret_cast<uintptr_t>(smem);
     const int nk = (K + SK - 1) / SK;
-    const Adapters who{q.which, nullptr, nullptr, 0, 0, 0, q.count, q.rank};
+    int *const lds = reinterpret_cast<int *>(smem);
     const int r = wave * RPI + lane / CH, ck = ((lane % CH) ^ (r & 15)) * 8;      // this lane's row of 16 and first k
     for (int block = blockIdx.x; block < w.blocks; block += gridDim.x) {
-        const int row0 = block * 16, rows = min(q.M - row0, 16), mine = adapter_of(who, row0 + frow, q.M);
+        const int row0 = block * kRows, rows = min(q.M - row0, kRows);
         const i32x4 rx = buffer_of(reinterpret_cast<uint64_t>(q.X) + (uint64_t)(row0 * q.ldx) * 2,
                                    (uint32_t)(rows - 1) * (uint32_t)q.ldx * 2 + (uint32_t)K * 2);
-        const uint32_t ox = r < rows ? (uint32_t)r * (uint32_t)q.ldx * 2 + ck * 2 : kOutside;
-        for_adapters(mine, blockIdx.z, w.slots, [&](int g) __attribute__((always_inline)) {
+        const Pieces m = pieces_of(q, row0, lane, wave, lds);
+        for (int c = blockIdx.z; c < m.count; c += w.slots) {
+            int g;
+            const int row = rows_of(m, c, lds, g), from = __shfl(row, r);
+            const uint32_t ox = from >= 0 ? (uint32_t)from * (uint32_t)q.ldx * 2 + ck * 2 : kOutside;
             const i32x4 ra = buffer_of(reinterpret_cast<uint64_t>(q.A) + (uint64_t)(g * q.stride + r0 * q.lda) * 2,
                                        (uint32_t)(ranks - 1) * (uint32_t)q.lda * 2 + (uint32_t)K * 2);
-            int at = (int)(((block >> 3) + (block & 7) * (unsigned)nk / 8) % (unsigned)nk);
+            int at = (int)(((c >> 3) + (c & 7) * (unsigned)nk / 8) % (unsigned)nk);
             auto issue = [&](int kt) __attribute__((always_inline)) {
                 const uint32_t slot = lds_base + (kt % NS) * SLOT + wave * 1024;
                 const int k0 = at * SK;
@@ -299,11 +368,9 @@ __global__ void __launch_bounds__(TT) shrink_stream_kernel(const Shrink q, const
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
             __atomic_signal_fence(__ATOMIC_SEQ_CST);
-            end_turn<RB, BF16>(q, reinterpret_cast<float(*)[16][RB * 16]>(smem), acc, row0, r0, g, wave, lane);
-        });
-        if (blockIdx.y == 0 && blockIdx.z == 0)
-            for (int i = wave; i < rows; i += TW)
-                store_zeros(q, row0 + i, lane, 64);
+            end_piece<RB, BF16>(q, reinterpret_cast<float(*)[16][RB * 16]>(smem), acc, row0, row, r0, g, wave, lane);
+        }
+        __syncthreads();                  // (the next block's pieces_of writes what this one's reads)
     }
 }
 
@@ -313,13 +380,16 @@ hipError_t shrink(const Shrink &q, hipStream_t s)
     const int parts = (q.rank + PER - 1) / PER;
     if (q.M <= kFewRows)
         return start(shrink_rows_kernel<BF16>, (int64_t)q.M * parts, RT, s, q, parts);
-    const int64_t blocks = ((int64_t)q.M + 15) / 16, grid = blocks < (1 << 17) ? blocks : 1 << 17;
+    const int64_t blocks = ((int64_t)q.M + kRows - 1) / kRows, grid = blocks < (1 << 17) ? blocks : 1 << 17;
+    // a block's pieces at most: an adapter has one that is not whole
+    const int rows = q.M < kRows ? q.M : kRows, most = (rows + 15) / 16 + (q.count < rows ? q.count : rows);
     const int rb = (q.rank + 15) / 16;
-    const bool deep = blocks * rb <= cu_count();
+    const bool deep = blocks * most * rb <= cu_count();
     const int per = deep ? 1 : rb > 2 ? 4 : rb, ranks = (rb + per - 1) / per;
-    // one or four workgroups per CU, at most one per row of a block
-    int64_t slots = (deep ? 1 : 4) * (int64_t)cu_count() / (blocks * ranks);
-    slots = slots < 1 ? 1 : slots > 16 ? 16 : slots;
+    // all pieces at once, or two workgroups per CU (8192 rows of 16 prompts: with four,
+    // of which half find nothing, 2 us more)
+    int64_t slots = deep ? most : 2 * (int64_t)cu_count() / (blocks * ranks);
+    slots = slots < 1 ? 1 : slots > most ? most : slots;
     const Place w{(int)blocks, (int)slots};
     auto go = [&](auto kernel) {
         void *args[] = {const_cast<Shrink *>(&q), const_cast<Place *>(&w)};

@@ -315,3 +315,46 @@ def test_a_decoding_step(hg, M):
         assert torch.equal(top[0].cpu(), ids)
         close(top[1], v["logp"].gather(1, ids), b["logp"].gather(1, ids), "top")
         close(entropy, v["entropy"][:, 0], b["entropy"][:, 0], "entropy")
+
+
+# rows of one adapter gathered from 256: fewer and more adapters than rows, more than 16 rows of one, blocks that end early
+@pytest.mark.parametrize("K", [72, 75])
+@pytest.mark.parametrize("M,rank,count", [(777, 16, 1), (777, 16, 2), (256, 33, 16), (257, 16, 255), (511, 5, 256), (512, 16, 257),
+                                          (777, 64, 1000), (1025, 16, 70000)])
+def test_rows_in_no_order(hg, M, rank, count, K):
+    case(hg, M, 64, K, rank, count, BF16, "single")
+
+
+def test_every_place_in_a_block(hg):
+    """A lone adapter's row at every place of 256, the others' without one or of another."""
+    M, N, K, rank = 256, 16, 64, 8
+    X, W, A, B, s, _ = operands(M, N, K, rank, 3, F16, "single")
+    dev = [x.to(DEV) for x in (X, W, A, B, s)]
+    for other in (-1, 1):
+        which = [torch.full((M,), other).index_fill(0, torch.tensor([i]), 2) for i in range(0, M, 5)]
+        for w in which:
+            Y = torch.empty(M, N, dtype=F16, device=DEV)
+            hg.linear_adapters(dev[0], dev[1], Y, w.to(DEV), dev[2], dev[3], scales=dev[4])
+            y, _, ey, _ = expected(X, W, A, B, s, w, None, "none", None)
+            ref.check(Y, y, ey, "Y")
+
+
+def test_more_blocks_than_a_launch_takes(hg):
+    """2^25 rows and some, blocks without an adapter among them: integers, exact."""
+    M, K, N, count = (1 << 25) + 300, 8, 8, 3
+    g = torch.Generator(device=DEV).manual_seed(3)
+    few = lambda *shape: torch.randint(-1, 2, shape, generator=g, device=DEV).to(BF16)  # noqa: E731
+    X, W, A, B = few(M, K), few(N, K), few(count, 1, K), few(count, N, 1)
+    at = torch.arange(M, device=DEV)
+    which = at * 2654435761 % 1000003 % 5 - 1
+    which[at // 256 % 3 == 1] = -1
+    Y = hg.linear_adapters(X, W, torch.empty(M, N, dtype=BF16, device=DEV), which, A, B)
+    torch.cuda.synchronize()
+    step = 1 << 23
+    for i in range(0, M, step):
+        x, w = X[i:i + step].float(), which[i:i + step]
+        y = sum(x[:, k, None] * W[:, k].float() for k in range(K))
+        for a in range(count):
+            t = (x * A[a, 0].float()).sum(1) * (w == a)
+            y += t[:, None] * B[a, :, 0].float()
+        assert torch.equal(Y[i:i + step].float(), y)
