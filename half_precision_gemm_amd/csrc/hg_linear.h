@@ -926,11 +926,13 @@ __device__ __forceinline__ int least_of_rows(int v)
 // time.  A block whose rows all have this adapter takes the products as they are;
 // one with other rows among them keeps those rows' sums (a choice by lane, not
 // zeros in T: an infinity or NaN of one request's adapter stays in its rows).
-// Rows past the last are not stored and may get anything.  A turn is one wait of
-// memory; from kTurns adapters on, which rows of different requests side by side
-// bring, a lane takes the rows and columns whose sums it holds, each with its own
-// row's B, and no turns are taken (add_by_rows).
+// Rows past the last are not stored and may get anything.  A turn is a wait of
+// memory and takes all rows; from kTurns adapters on, which rows of different
+// requests side by side bring, a lane takes the rows and columns whose sums it holds,
+// each with its own row's B, and no turns are taken (add_by_rows), or rows are
+// gathered (add_gathered).
 constexpr int kTurns = 4;
+
 template <bool BF16, int TI, int TJ>
 __device__ __forceinline__ void add_by_rows(const Product &p, const int (&mine)[TI], int row0, int col0, int lane,
                                             floatx4 (&acc)[TI][TJ])
@@ -967,8 +969,115 @@ __device__ __forceinline__ void add_by_rows(const Product &p, const int (&mine)[
         }
     }
 }
+
+// Waits until the matrix cores have written these sums.  (Where a branch follows a
+// matrix instruction, the compiler has been seen to read its result on the other
+// side at once.)
+__device__ __forceinline__ void settled(floatx4 (&v)[2]) { __asm__ volatile("s_nop 15" : "+v"(v[0]), "+v"(v[1])); }
+__device__ __forceinline__ void settled(floatx4 (&v)[4])
+{
+    __asm__ volatile("s_nop 15" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]));
+}
+
+// The same for large ranks: up to 16 of the wave's rows that share an adapter at a
+// time, on the matrix cores, four steps of 32 terms requested ahead, whatever adapter
+// they are of.  The sums go through `lds`, the wave's own, to the lanes that hold the
+// rows.  From kGatherFrom on, where row by row a lane's loads, from 64 places each,
+// take longer than one adapter after the other (us, the layer, rows in no order):
+// 1000×4096×4096, 64 adapters, 64 rows a wave: rank 16 69 for 64, 32 85 for 95, 64 147
+// for 337; 300×1024×4096, 32 rows a wave: rank 48 49 for 45, 64 55 for 59; 333×1111×777,
+// 5 adapters: rank 64 25 for 32.  Ranks that are not a multiple of 8 go row by row: B's
+// last piece would be waited for (300×1024×4096, rank 60: 110 for 70).
+constexpr int kGatherFrom = 128;                    // rank times blocks of 16 rows
+template <int TI, int TJ>
+constexpr int kGatherBytes = TI * TJ * 1024;
 template <bool BF16, int TI, int TJ>
-__device__ __forceinline__ void add_adapters(const Product &p, int row0, int col0, int lane, floatx4 (&acc)[TI][TJ])
+__device__ __forceinline__ void add_gathered(const Product &p, int row0, int col0, int lane, unsigned char *lds,
+                                             floatx4 (&acc)[TI][TJ])
+{
+    constexpr int AHEAD = 4, PIECES = 4 * TJ;
+    const Adapters &a = p.ad;
+    const int frow = lane & 15, fhi = lane >> 4;
+    const int chunks = (a.rank + 7) / 8, steps = (2 * chunks + 3) / 4;
+    const int mine = lane < 16 * TI ? adapter_of(a, row0 + lane, p.M) : -1;
+    const uint64_t below = ((uint64_t)1 << lane) - 1;
+    auto place = [&](int row, int j) __attribute__((always_inline)) {
+        return reinterpret_cast<floatx4 *>(lds + (row * PIECES + ((4 * j + fhi) ^ (row & (PIECES - 1)))) * 16);
+    };
+    uint64_t left = __builtin_amdgcn_ballot_w64(mine >= 0);
+    // What is requested next: step s of the rows `row` (lane: frow's) of adapter g.
+    int g = 0, row = -1, s = steps;
+    enum { NONE, SOME, LAST };
+    struct Unit {
+        u32x4 b[TJ], t;
+        int row, kind;
+    } ring[AHEAD];
+    // (straight code: a load that a branch goes round is waited for where its ways
+    // meet; behind the last piece the same is loaded again)
+    auto request = [&](Unit &u) __attribute__((always_inline)) {
+        if (s == steps && left != 0) {
+            g = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+            const bool same = mine == g && (left >> lane & 1) != 0;
+            const int nth = __builtin_popcountll(__builtin_amdgcn_ballot_w64(same) & below);
+            const bool take = same && nth < 16;
+            left &= ~__builtin_amdgcn_ballot_w64(take);
+            // (lanes that nothing is sent to get 0)
+            const int list = __builtin_amdgcn_ds_permute((take ? nth : 63) * 4, lane + 1);
+            row = __builtin_amdgcn_ds_bpermute(frow * 4, list) - 1;
+            s = 0;
+        }
+        u.kind = s == steps ? NONE : s + 1 == steps ? LAST : SOME;
+        const int c = 4 * min(s, steps - 1) + fhi, cb = c < chunks ? c : c < 2 * chunks ? c - chunks : 0;
+        const uint16_t *B = a.B + g * a.stride;
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+            u.b[j] = *reinterpret_cast<const u32x4_any *>(B + min(col0 + 16 * j + frow, p.N - 1) * a.ldb + 8 * cb);
+        u.t = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.T) + (row0 + max(row, 0)) * a.ldt + 8 * c);
+        u.row = row;
+        s = min(s + 1, steps);
+    };
+    static_for<AHEAD>([&](auto d) __attribute__((always_inline)) { request(ring[decltype(d)::value]); });
+    floatx4 sum[TJ];
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+        sum[j] = floatx4{0, 0, 0, 0};
+    while (ring[0].kind != NONE) {
+        static_for<AHEAD>([&](auto d) __attribute__((always_inline)) {
+            Unit &u = ring[decltype(d)::value];
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+                sum[j] = mfma_16x16x32<BF16>(__builtin_bit_cast(half8, u.b[j]), __builtin_bit_cast(half8, u.t), sum[j]);
+            settled(sum);
+            if (u.kind == LAST) {
+#pragma unroll
+                for (int j = 0; j < TJ; ++j) {
+                    if (u.row >= 0)
+                        *place(u.row, j) = sum[j];
+                    sum[j] = floatx4{0, 0, 0, 0};
+                }
+            }
+            request(u);
+        });
+    }
+    // a wave's LDS accesses execute in order; the fence keeps the compiler from
+    // moving them across
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+        const bool me = __builtin_amdgcn_ds_bpermute((16 * i + frow) * 4, mine) >= 0;
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+            const floatx4 more = *place(16 * i + frow, j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[i][j][e] = me ? acc[i][j][e] + more[e] : acc[i][j][e];
+        }
+    }
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+template <bool BF16, int TI, int TJ>
+__device__ __forceinline__ void add_adapters(const Product &p, int row0, int col0, int lane, unsigned char *lds,
+                                             floatx4 (&acc)[TI][TJ])
 {
     const Adapters &a = p.ad;
     const int frow = lane & 15, fhi = lane >> 4;
@@ -989,7 +1098,10 @@ __device__ __forceinline__ void add_adapters(const Product &p, int row0, int col
     for (int g = after(-1); g != NONE_LEFT && many < kTurns; g = after(g))
         ++many;
     if (many == kTurns) {
-        add_by_rows<BF16>(p, mine, row0, col0, lane, acc);
+        if (a.rank % 8 == 0 && a.rank * TI >= kGatherFrom)
+            add_gathered<BF16>(p, row0, col0, lane, lds, acc);
+        else
+            add_by_rows<BF16>(p, mine, row0, col0, lane, acc);
         return;
     }
     for (int g = after(-1); g != NONE_LEFT; g = after(g)) {
@@ -1026,6 +1138,9 @@ __device__ __forceinline__ void add_adapters(const Product &p, int row0, int col
             }
         }
     }
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+        settled(acc[i]);
 }
 
 // ---- Wave-private staging of a 16×W block of sums (fp32) in LDS, from the

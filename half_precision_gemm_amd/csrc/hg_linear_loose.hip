@@ -135,14 +135,15 @@ __global__ void __launch_bounds__(THREADS, 2) linear_loose_kernel(const Product 
             }
         }
     }
-    if constexpr (ADAPT) {
-        if (t.kt0 == 0)
-            add_adapters<BF16>(p, t.m0 + wm * WT, t.n0 + wn * WT, lane, acc);
-    }
     meet();
 
     unsigned char *stg = smem + wave * (16 * WT * 4);
     const int row0 = t.m0 + wm * WT;
+    if constexpr (ADAPT) {
+        static_assert(4 * (16 * WT * 4 + kGatherBytes<T, T>) <= sizeof smem, "");
+        if (t.kt0 == 0)
+            add_adapters<BF16>(p, row0, t.n0 + wn * WT, lane, smem + 4 * (16 * WT * 4) + wave * kGatherBytes<T, T>, acc);
+    }
     Drain<EDGE, WT, BF16> out(p, t, stg, lane, t.n0 + wn * WT);
     out.request(row0);
     settle(out.bias);

@@ -140,10 +140,6 @@ __device__ __forceinline__ void ring_tile(const Product &p, const Spread &w, int
         if (kt + 1 < nk)
             step(kt + 1, f1, f0);
     }
-    if constexpr (ADAPT) {
-        if (kt0 == 0)
-            add_adapters<BF16>(p, m0 + wm * WT, n0 + wn * WT, lane, acc);
-    }
     // The ring's last loads (zero fills) and everyone's reads are done before
     // the slots are used for the staging of the results.
     wait_vmcnt<0>();
@@ -152,6 +148,11 @@ __device__ __forceinline__ void ring_tile(const Product &p, const Spread &w, int
 
     unsigned char *stg = smem + wave * (16 * WT * 4);
     const int row0 = m0 + wm * WT;
+    if constexpr (ADAPT) {
+        static_assert(4 * (16 * WT * 4 + kGatherBytes<T, T>) <= kLds<EDGE>, "");
+        if (kt0 == 0)
+            add_adapters<BF16>(p, row0, n0 + wn * WT, lane, smem + 4 * (16 * WT * 4) + wave * kGatherBytes<T, T>, acc);
+    }
     Drain<EDGE, WT, BF16> out(p, t, stg, lane, n0 + wn * WT);
     out.request(row0);
     settle(out.bias);

@@ -8,7 +8,7 @@
 //  * Few rows (shrink_rows_kernel): a workgroup per row and four values of T;
 //    each row reads its adapter whatever the others' are, from L2 where they
 //    share it.
-//  * More: 16 rows of X that share an adapter and 16 to 64 of the rank per
+//  * More: 16 rows of X that share an adapter and 16 or 32 of the rank per
 //    workgroup on the matrix cores, the sum split over its eight waves.  The rows
 //    are gathered from a block of 256, so an adapter is read once or twice for all of
 //    a block's rows that have it: with 16 neighbours and a turn for every adapter
@@ -292,7 +292,7 @@ constexpr int kShrinkSlot = 16 * (1 + RB) * SK * 2;
 // than CUs, more of each one's stages in flight (87×64×15424, rank 63, with 16 of the
 // rank in a workgroup instead of 64: 47 -> 32 us for the whole layer).
 template <int RB, bool DEEP>
-constexpr int kShrinkSlots = DEEP ? 10 : 80 * 1024 / kShrinkSlot<RB> < 3 ? 3 : 80 * 1024 / kShrinkSlot<RB>;
+constexpr int kShrinkSlots = (DEEP ? 160 : 80) * 1024 / kShrinkSlot<RB>;
 
 template <int RB, bool DEEP, bool BF16>
 __global__ void __launch_bounds__(TT) shrink_stream_kernel(const Shrink q, const Place w)
@@ -385,7 +385,9 @@ hipError_t shrink(const Shrink &q, hipStream_t s)
     const int rows = q.M < kRows ? q.M : kRows, most = (rows + 15) / 16 + (q.count < rows ? q.count : rows);
     const int rb = (q.rank + 15) / 16;
     const bool deep = blocks * most * rb <= cu_count();
-    const int per = deep ? 1 : rb > 2 ? 4 : rb, ranks = (rb + per - 1) / per;
+    // (more of the rank in a workgroup leaves one to a CU: 8192×1024, rank 64, 83 us for 79
+    // of the layer)
+    const int per = deep || rb == 1 ? 1 : 2, ranks = (rb + per - 1) / per;
     // all pieces at once, or two workgroups per CU (8192 rows of 16 prompts: with four,
     // of which half find nothing, 2 us more)
     int64_t slots = deep ? most : 2 * (int64_t)cu_count() / (blocks * ranks);
@@ -399,9 +401,8 @@ hipError_t shrink(const Shrink &q, hipStream_t s)
     if (q.direct)
         return deep       ? go(shrink_stream_kernel<1, true, BF16>)
                : per == 1 ? go(shrink_stream_kernel<1, false, BF16>)
-               : per == 2 ? go(shrink_stream_kernel<2, false, BF16>)
-                          : go(shrink_stream_kernel<4, false, BF16>);
-    return per == 1 ? go(shrink_tile_kernel<1, BF16>) : per == 2 ? go(shrink_tile_kernel<2, BF16>) : go(shrink_tile_kernel<4, BF16>);
+                          : go(shrink_stream_kernel<2, false, BF16>);
+    return per == 1 ? go(shrink_tile_kernel<1, BF16>) : go(shrink_tile_kernel<2, BF16>);
 }
 
 }  // namespace

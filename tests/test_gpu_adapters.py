@@ -358,3 +358,28 @@ def test_more_blocks_than_a_launch_takes(hg):
             t = (x * A[a, 0].float()).sum(1) * (w == a)
             y += t[:, None] * B[a, :, 0].float()
         assert torch.equal(Y[i:i + step].float(), y)
+
+
+# rows of many adapters in 128×128 tiles: rows of one that are more than 16 of a wave's, ranks of several steps, edges
+@pytest.mark.parametrize("t", [F16, BF16])
+@pytest.mark.parametrize("M,N,K,rank,count", [(1000, 4096, 256, 64, 64), (1000, 4096, 264, 20, 5), (901, 4001, 128, 100, 7),
+                                              (1024, 2048, 1024, 8, 4), (700, 5000, 64, 3, 1000), (901, 4001, 128, 32, 7),
+                                              (300, 200, 64, 72, 40), (1100, 2500, 128, 200, 9), (333, 111, 77, 256, 33)])
+def test_many_adapters_in_a_tile(hg, t, M, N, K, rank, count):
+    case(hg, M, N, K, rank, count, t, "single")
+
+
+def test_infinities_stay_in_their_rows_among_many(hg):
+    """What is not finite in some adapters' B and in some rows of X, rows of many adapters side by side."""
+    for M, N, rank in ((300, 200, 16), (1000, 4096, 16), (300, 200, 64), (1000, 4096, 64)):
+        X, W, A, B, s, which = operands(M, N, 64, rank, 12, BF16, "single")
+        Y = []
+        for bad in (False, True):
+            x, b = X.clone(), B.clone()
+            if bad:
+                b[3, 5, 2], b[7, 100, 0], x[17, 3] = float("inf"), float("nan"), float("-inf")
+            y = torch.empty(M, N, dtype=BF16, device=DEV)
+            Y.append(hg.linear_adapters(x.to(DEV), W.to(DEV), y, which.to(DEV), A.to(DEV), b.to(DEV), scales=s.to(DEV)).cpu())
+        touched = (which == 3) | (which == 7) | (torch.arange(M) == 17)
+        assert torch.equal(Y[0][~touched], Y[1][~touched])
+        assert not Y[1][which == 3][:, 5].isfinite().any() and Y[1][which == 7][:, 100].isnan().all()
