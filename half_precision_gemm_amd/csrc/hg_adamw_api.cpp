@@ -126,7 +126,7 @@ int hg_adamw(int64_t count, const hg_adamw_tensor *tensors, int64_t step, const 
         return -6;
     if (!part(beta2))
         return -7;
-    if (!amount(eps))
+    if (!amount(eps) || (eps != 0.0 && (eps < HG_ADAMW_LEAST_EPS || eps > 1.0 / HG_ADAMW_LEAST_EPS)))
         return -8;
     if (!amount(decay))
         return -9;

@@ -129,8 +129,8 @@ def adamw(tensors, step, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8
 
     step: its number, 1 the first: an int, or an int64 device tensor of one element
     for calls that are captured (below 1: nothing is changed).  factors: a float32
-    device tensor of two, what lr and every gradient are multiplied by.  seed: of
-    the random rounding of 8-bit moments (mod 2^64)."""
+    device tensor of two, what lr and every gradient are multiplied by.  eps: 0, or
+    1e-30 to 1e30.  seed: of the random rounding of 8-bit moments (mod 2^64)."""
     if not isinstance(tensors, AdamWTensors):
         raise TypeError("tensors must be an AdamWTensors (adamw_tensors)")
     dev = tensors.device

@@ -18,9 +18,10 @@
 extern "C" {
 #endif
 
-/* Largest number of elements of a tensor, and of tensors in a call. */
+/* Largest number of elements of a tensor, and of tensors in a call; least eps that is not 0. */
 #define HG_ADAMW_MAX_ELEMENTS ((int64_t)1 << 36)
 #define HG_ADAMW_MAX_TENSORS (1 << 20)
+#define HG_ADAMW_LEAST_EPS 1e-30
 
 /*
  * One tensor: n elements one after the other in each array.
@@ -61,7 +62,7 @@ typedef struct hg_adamw_tensor {
  *                  1 nothing is changed (a step that is to be left out).
  *  5 lr, 9 decay : finite, not negative.
  *  6, 7          : beta1, beta2 in [0, 1).
- *  8 eps         : finite, not negative.
+ *  8 eps         : 0, or HG_ADAMW_LEAST_EPS to 1 / HG_ADAMW_LEAST_EPS.
  * 10 factors     : two DEVICE fp32 values, or NULL: what lr and every gradient are
  *                  multiplied by (a schedule; clipping, a loss scale).
  * 11 seed        : of the random rounding of 8-bit moments; a call's with the same

@@ -43,7 +43,7 @@ def test_header_and_exports_agree(api, hg):
     (dict(count=-1), -1), (dict(count=(1 << 20) + 1), -1), (dict(tensors=False, count=1), -2), (dict(t=0), -3), (dict(t=-5), -3),
     (dict(dt=P[9] + 4), -4), (dict(lr=-1.0), -5), (dict(lr=NAN), -5), (dict(lr=INF), -5), (dict(lr=1e39), -5),
     (dict(b1=1.0), -6), (dict(b1=-0.1), -6), (dict(b1=NAN), -6), (dict(b2=1.0), -7), (dict(b2=NAN), -7), (dict(eps=-1.0), -8),
-    (dict(eps=INF), -8), (dict(decay=-1.0), -9), (dict(decay=NAN), -9), (dict(factors=P[9] + 2), -10),
+    (dict(eps=INF), -8), (dict(eps=9e-31), -8), (dict(eps=1.1e30), -8), (dict(eps=NAN), -8), (dict(decay=-1.0), -9), (dict(decay=NAN), -9), (dict(factors=P[9] + 2), -10),
     (dict(count=-1, t=0), -1), (dict(), 0), (dict(t=0, dt=P[9]), 0), (dict(tensors=[]), 0),
 ])
 def test_refusals(api, kw, code):

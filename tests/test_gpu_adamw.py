@@ -5,10 +5,11 @@ moments, and the codes and scales of 8-bit ones, are known to the bit: the
 reference forms them in fp32 on the CPU and rounds at random by the same bits.
 
 The weight, from these moments, is in 64 bits; bound: u = 2^-24.  1 - beta^t is
-off by 5u of itself (its exponent by u, expm1 by 4u), the quotient of the two
-moments by 5u for either, half of that in the root, three roundings and the sum
-with eps: under 16u; times lr and with decay·w four more roundings of either
-term, the subtraction one of the result, and factors one of lr.
+off by 5u of itself (its exponent by u, expm1 by 4u), its reciprocal and its
+product with either moment by 7u, half of that in the root, the card's root and
+reciprocal by 2u each (a step), the sum with eps and the quotient one rounding
+each: under 17u; times lr and with decay·w four more roundings of either term, the
+subtraction one of the result, and factors one of lr.
 """
 import numpy as np
 import pytest
@@ -381,3 +382,20 @@ def test_kinds_in_turn(hg):
     hg.adamw(hg.adamw_tensors(*(turn[k] for k in "pgmv"), masters=turn["w"]), 3, LR, (B1, B2), EPS, DECAY, seed=8)
     for k, b in enumerate(bs):
         b.check(3, 8, place0=lambda i: len(kinds) * i + k)
+
+
+@pytest.mark.parametrize("size", [1e-15, 1e-18, 3e-19, 1e-19, 1e-20, 3e-21])
+def test_second_moments_below_the_least_normal_number(hg, size):
+    """With eps = 0 the quotient still is that of the moments, however small they are."""
+    n, f = 97, np.float32
+    g = (size * np.linspace(0.5, 2.0, n)).astype(f)
+    p, m, v = (torch.zeros(n, device=DEV) for _ in range(3))
+    hg.adamw(hg.adamw_tensors([p], [torch.from_numpy(g).to(DEV)], [m], [v]), 1, 0.5, (B1, B2), 0.0, 0.0)
+    zero = np.zeros(n, f)
+    M, V, new, err = step_of(g, zero, zero, zero, 1, 0.5, eps=0.0, decay=0.0)
+    assert torch.equal(m.cpu(), torch.from_numpy(M)) and torch.equal(v.cpu(), torch.from_numpy(V))
+    # (v times its factor, below the least normal number, is off by half of the least step)
+    q = V.astype(np.float64) / (1 - B2)
+    err = err + torch.from_numpy(np.where(q > 0, 0.5 * 2.0 ** -149 / np.maximum(q, 2.0 ** -149), 0)) * new.abs()
+    some = torch.from_numpy(V > 0)
+    ref.check(p.cpu()[some], new[some], err[some], "weight")
