@@ -986,12 +986,12 @@ __device__ __forceinline__ void settled(floatx4 (&v)[4])
 // take longer than one adapter after the other (us, the layer, rows in no order):
 // 1000×4096×4096, 64 adapters, 64 rows a wave: rank 16 69 for 64, 32 85 for 95, 64 147
 // for 337; 300×1024×4096, 32 rows a wave: rank 48 49 for 45, 64 55 for 59; 333×1111×777,
-// 5 adapters: rank 64 25 for 32.  Ranks that are not a multiple of 8 go row by row: B's
-// last piece would be waited for (300×1024×4096, rank 60: 110 for 70).
-constexpr int kGatherFrom = 128;                    // rank times blocks of 16 rows
+// 5 adapters: rank 64 25 for 32; 383×9792×128, 45 adapters: rank 42 74 for 132.  Not
+// where rows of B lie at odd elements (1000×4096×4096, rank 33: 174 for 149).
+constexpr int kGatherFrom = 112;                    // rank times blocks of 16 rows
 template <int TI, int TJ>
 constexpr int kGatherBytes = TI * TJ * 1024;
-template <bool BF16, int TI, int TJ>
+template <bool CUT, bool BF16, int TI, int TJ>
 __device__ __forceinline__ void add_gathered(const Product &p, int row0, int col0, int lane, unsigned char *lds,
                                              floatx4 (&acc)[TI][TJ])
 {
@@ -1010,7 +1010,7 @@ __device__ __forceinline__ void add_gathered(const Product &p, int row0, int col
     enum { NONE, SOME, LAST };
     struct Unit {
         u32x4 b[TJ], t;
-        int row, kind;
+        int row, kind, valid;             // valid: of the eight from the rank's piece on
     } ring[AHEAD];
     // (straight code: a load that a branch goes round is waited for where its ways
     // meet; behind the last piece the same is loaded again)
@@ -1034,6 +1034,7 @@ __device__ __forceinline__ void add_gathered(const Product &p, int row0, int col
             u.b[j] = *reinterpret_cast<const u32x4_any *>(B + min(col0 + 16 * j + frow, p.N - 1) * a.ldb + 8 * cb);
         u.t = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.T) + (row0 + max(row, 0)) * a.ldt + 8 * c);
         u.row = row;
+        u.valid = a.rank - 8 * cb;
         s = min(s + 1, steps);
     };
     static_for<AHEAD>([&](auto d) __attribute__((always_inline)) { request(ring[decltype(d)::value]); });
@@ -1044,6 +1045,15 @@ __device__ __forceinline__ void add_gathered(const Product &p, int row0, int col
     while (ring[0].kind != NONE) {
         static_for<AHEAD>([&](auto d) __attribute__((always_inline)) {
             Unit &u = ring[decltype(d)::value];
+            if constexpr (CUT) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t keep = u.valid >= 2 * e + 2 ? ~0u : u.valid == 2 * e + 1 ? 0xffffu : 0u;
+#pragma unroll
+                    for (int j = 0; j < TJ; ++j)
+                        u.b[j][e] &= keep;
+                }
+            }
 #pragma unroll
             for (int j = 0; j < TJ; ++j)
                 sum[j] = mfma_16x16x32<BF16>(__builtin_bit_cast(half8, u.b[j]), __builtin_bit_cast(half8, u.t), sum[j]);
@@ -1098,8 +1108,12 @@ __device__ __forceinline__ void add_adapters(const Product &p, int row0, int col
     for (int g = after(-1); g != NONE_LEFT && many < kTurns; g = after(g))
         ++many;
     if (many == kTurns) {
-        if (a.rank % 8 == 0 && a.rank * TI >= kGatherFrom)
-            add_gathered<BF16>(p, row0, col0, lane, lds, acc);
+        // (what follows a row in memory is loaded with it and cut off; columns that
+        // less than eight elements may follow go row by row)
+        if (a.rank * TI >= kGatherFrom && a.rank % 8 == 0)
+            add_gathered<false, BF16>(p, row0, col0, lane, lds, acc);
+        else if (a.rank * TI >= kGatherFrom && a.ldb % 2 == 0 && col0 + 16 * TJ + 8 <= p.N)
+            add_gathered<true, BF16>(p, row0, col0, lane, lds, acc);
         else
             add_by_rows<BF16>(p, mine, row0, col0, lane, acc);
         return;
