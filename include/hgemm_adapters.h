@@ -29,9 +29,10 @@ extern "C" {
 #define HG_ADAPTERS_MAX_STRIDE ((int64_t)1 << 40)
 
 /*
- * Adapters of one rank (pad shorter ones with zeros).  Adapter g: A_g rank×K at
- * A + g·stride_a elements, rows lda apart; B_g N×rank at B + g·stride_b, rows
- * ldb apart (any alignment of 2 bytes; multiples of 8 elements are fastest).
+ * Adapters of one rank (pad shorter ones with zeros; ranks that are a multiple of
+ * 8 are fastest).  Adapter g: A_g rank×K at A + g·stride_a elements, rows lda
+ * apart; B_g N×rank at B + g·stride_b, rows ldb apart (any alignment of 2 bytes;
+ * multiples of 8 elements are fastest).
  */
 typedef struct hg_adapters {
     const int64_t *which; /* M values: row i's adapter; outside 0 .. count-1: none */
