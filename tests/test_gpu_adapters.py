@@ -383,3 +383,10 @@ def test_infinities_stay_in_their_rows_among_many(hg):
         touched = (which == 3) | (which == 7) | (torch.arange(M) == 17)
         assert torch.equal(Y[0][~touched], Y[1][~touched])
         assert not Y[1][which == 3][:, 5].isfinite().any() and Y[1][which == 7][:, 100].isnan().all()
+
+
+@pytest.mark.parametrize("M,N,rank,count,apad", [(300, 300, 60, 40, 0), (300, 300, 58, 40, 2), (1000, 4096, 30, 16, 4), (900, 4100, 100, 9, 6),
+                                                 (1000, 4096, 33, 16, 1), (300, 300, 57, 9, 3)])
+def test_ranks_cut_from_padded_rows(hg, M, N, rank, count, apad):
+    """What lies between B's rows (NaN) is loaded with them in places and must not count."""
+    case(hg, M, N, 64, rank, count, BF16, "single", apad=apad)
