@@ -122,8 +122,8 @@ __device__ __forceinline__ int encode(const float (&v)[8], const uint32_t (&r)[8
         const uint32_t add = (SHIFT ? r[e] >> 12 & 0xffff0u : r[e] << 4 & 0xffff0u) | 8u;
         float c = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, z) + add) & 0xfff00000u);
         c = low ? c - 0x1p-6f : c;
-        if (KEEP)
-            c = c == 0.0f && y > 0.0f ? 0x1p-9f : c;
+        if (KEEP)                         // (y itself may have left fp32)
+            c = c == 0.0f && v[e] > 0.0f ? 0x1p-9f : c;
         c = y <= lim ? c : __builtin_fabsf(v[e]) < __builtin_inff() ? lim : __builtin_nanf("");
         q[e] = __builtin_copysignf(c, v[e]);
     }

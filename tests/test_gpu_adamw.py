@@ -399,3 +399,20 @@ def test_second_moments_below_the_least_normal_number(hg, size):
     err = err + torch.from_numpy(np.where(q > 0, 0.5 * 2.0 ** -149 / np.maximum(q, 2.0 ** -149), 0)) * new.abs()
     some = torch.from_numpy(V > 0)
     ref.check(p.cpu()[some], new[some], err[some], "weight")
+
+
+@pytest.mark.parametrize("small", [1e-15, 1e-17, 1e-10])
+def test_a_tiny_second_moment_beside_a_huge_one(hg, small):
+    """In one block of 32, a second moment above 0 never becomes 0, however far below the block's largest it is: the
+    quotient 1e-33 / 2^102 itself leaves fp32."""
+    n = 64
+    g = torch.zeros(n)
+    g[0], g[1:20], g[32:50] = 1e18, small, small
+    p = torch.zeros(n, device=DEV)
+    m, v = hg.adamw_state(p, 8)
+    tensors = hg.adamw_tensors([p], [g.to(DEV)], [m], [v])
+    for t in range(1, 4):
+        hg.adamw(tensors, t, LR, (B1, B2), EPS, DECAY, seed=t)
+        codes = v[0].cpu()
+        assert codes[0] > 0x70 and (codes[1:20] == 1).all(), codes[:32]        # the least code, 2^-9 of the scale
+        assert (codes[32:50] > 1).all() and not codes[20:32].any() and not codes[50:].any()
