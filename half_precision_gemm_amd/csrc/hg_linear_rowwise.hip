@@ -125,7 +125,7 @@ struct OwnSums {
     {
         const uint16_t *A = p.own + max(g, 0) * p.own_stride;
         const int k = k0 + threadIdx.x * 8, at = min(k, p.K - 8);
-        xs = *reinterpret_cast<const u32x4 *>(p.A + at) & (k < p.K ? ~0u : 0u);
+        xs = *reinterpret_cast<const u32x4 *>(p.A + at);
 #pragma unroll
         for (int r = 0; r < kOwnRank; ++r)
             as[r] = *reinterpret_cast<const u32x4_any *>(A + min(r, p.ad.rank - 1) * p.own_ld + at);
@@ -134,15 +134,19 @@ struct OwnSums {
     __device__ __forceinline__ float sum()
     {
         for (int k0 = 0;;) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                x[e] = widen<BF16>((uint16_t)(xs[e >> 1] >> (16 * (e & 1))));
-#pragma unroll
-            for (int r = 0; r < kOwnRank; ++r)
+            // (lanes past K hold the last eight again: left out, as zeros in X would make
+            // a NaN of an infinity in A)
+            if (k0 + (int)threadIdx.x * 8 < p.K) {
+                float x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    v[r] = __builtin_fmaf(widen<BF16>((uint16_t)(as[r][e >> 1] >> (16 * (e & 1)))), x[e], v[r]);
+                    x[e] = widen<BF16>((uint16_t)(xs[e >> 1] >> (16 * (e & 1))));
+#pragma unroll
+                for (int r = 0; r < kOwnRank; ++r)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[r] = __builtin_fmaf(widen<BF16>((uint16_t)(as[r][e >> 1] >> (16 * (e & 1)))), x[e], v[r]);
+            }
             k0 += THREADS * 8;
             if (k0 >= p.K)
                 break;

@@ -390,3 +390,19 @@ def test_infinities_stay_in_their_rows_among_many(hg):
 def test_ranks_cut_from_padded_rows(hg, M, N, rank, count, apad):
     """What lies between B's rows (NaN) is loaded with them in places and must not count."""
     case(hg, M, N, 64, rank, count, BF16, "single", apad=apad)
+
+
+@pytest.mark.parametrize("t", [F16, BF16])
+@pytest.mark.parametrize("K", [8, 128, 512, 4096, 4104, 6000])
+def test_an_infinite_a_of_one_row(hg, t, K):
+    """One row, one launch: an infinity at either end of a row of A gives infinities as in the formula, no NaN."""
+    N, rank, count = 64, 9, 2
+    X, W, A, B, _, which = operands(1, N, K, rank, count, t, "one", scales=False)
+    X, B = X.abs() + 0.5, torch.where(B.abs() < 0.1, 0.1, B).to(t)
+    X = X.to(t)
+    for k in (K - 1, 0):
+        a = A.clone()
+        a[1, 3, k] = float("inf")
+        Y = torch.empty(1, N, dtype=F32, device=DEV)
+        hg.linear_adapters(X.to(DEV), W.to(DEV), Y, which.to(DEV), a.to(DEV), B.to(DEV))
+        assert torch.equal(Y[0].cpu(), torch.where(B[1, :, 3] > 0, float("inf"), -float("inf")).float()), k
