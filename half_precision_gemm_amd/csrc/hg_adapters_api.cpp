@@ -67,7 +67,7 @@ struct Beside {
     {
         return meets(y) || meets(z) || meets(zs) ? -11 : HG_OK;
     }
-    int most_tile() const { return most_tile_of(l->rank); }
+    int most_tile() const { return any() ? most_tile_of(l->rank) : 256; }
     void *room(Arena &a) const { return a.take(any() ? M * width_of(l->rank) * 2 : 0); }
     hipError_t begin(lin::Product &p, Arena &a, const LinearPlan &q, bool bf16, hipStream_t s) const
     {
@@ -101,9 +101,11 @@ extern "C" {
 int64_t hg_linear_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, const hg_matrix *X,
                                           const hg_matrix *W)
 {
-    const int64_t need = linear_room(M, N, K, X, W, most_tile_of(rank));
+    int64_t need = linear_room(M, N, K, X, W, most_tile_of(rank));
     if (need < 0 && need > -4)
         return need;
+    // (a call may have no adapters, whatever their rank)
+    need = std::max(need, linear_room(M, N, K, X, W));
     if (rank < 0 || rank > HG_ADAPTERS_MAX_RANK)
         return -4;
     if (need < 0)

@@ -83,3 +83,17 @@ def test_workspace_size_refusals(lib):
     assert size(-1, 8, 64, 999, None, None) == -1 and size(4, -1, 64, 999, x, w) == -2 and size(4, 8, -1, 9, x, w) == -3
     assert size(4, 8, 64, 257, x, w) == -4 and size(4, 8, 64, -1, x, w) == -4
     assert size(4, 8, 64, 16, None, w) == -5 and size(4, 8, 64, 16, x, mat(1, 64, F16)) == -6
+
+
+@pytest.mark.parametrize("M,N,K", [(8192, 4096, 4096), (7840, 2816, 5560), (3001, 3026, 148), (64, 8224, 512)])
+@pytest.mark.parametrize("kw", [dict(rank=17, count=0), dict(rank=16, count=0), dict(rank=0, count=4)])
+def test_without_adapters_the_layer_is_cut_alike(lib, M, N, K, kw):
+    """Whatever the rank of adapters that there are none of, and in the workspace that the rank asks for."""
+    X, W, Y = mat(0, K), mat(1, K), mat(2, N)
+    assert lib.hg_linear(4, M, N, K, X, W, None, None, Y, None, 9 * SPACE, lib.hg_linear_workspace_size(M, N, K, X, W), None) == 0
+    alone = lib.plan_launches()
+    X, W = mat(0, K), mat(1, K)
+    L = adapters.Adapters(5 * SPACE, None, 6 * SPACE, K, 0, 7 * SPACE, max(1, kw["rank"]), 0, kw["count"], kw["rank"], BF16)
+    work = lib.hg_linear_adapters_workspace_size(M, N, K, kw["rank"], X, W)
+    assert lib.hg_linear_adapters(4, M, N, K, X, W, None, None, Y, None, L, 9 * SPACE, work, None) == 0
+    assert lib.plan_launches() == alone
