@@ -15,9 +15,15 @@ namespace {
 
 namespace lin = hg::lin;
 
-// 16-bit numbers, or half as many fp32 ones, that a row of T takes: high and low
-// halves up to the matrix cores' 32 (lin::Adapters).
-int64_t width_of(int64_t rank) { return (2 * up8(rank) + 31) / 32 * 32; }
+// Numbers of X's type for one of T (lin::Adapters).
+int parts_of(int type, bool out32) { return type == HG_BF16 && out32 ? 3 : 2; }
+// Numbers that a row of T takes: fp32 ones up to a whole eight where it goes row by
+// row (`few`), else `parts` 16-bit ones for each, up to the matrix cores' 32.
+int64_t width_of(int64_t rank, bool few, int parts) { return few ? up8(rank) : (parts * up8(rank) + 31) / 32 * 32; }
+void *room_of(Arena &a, int64_t M, int64_t rank, bool few, int parts)
+{
+    return a.take(M * width_of(rank, few, parts) * (few ? 4 : 2));
+}
 
 // The largest tiles that may be taken: 256×256 ones add the terms of whole
 // eights only.
@@ -25,7 +31,7 @@ int most_tile_of(int64_t rank) { return rank % 8 == 0 ? 256 : 128; }
 
 struct Beside {
     const hg_adapters *l;
-    const hg_matrix *X;
+    const hg_matrix *X, *Y;
     int64_t M, N, K;
 
     bool any() const { return l->count > 0 && l->rank > 0; }
@@ -68,28 +74,32 @@ struct Beside {
         return meets(y) || meets(z) || meets(zs) ? -11 : HG_OK;
     }
     int most_tile() const { return any() ? most_tile_of(l->rank) : 256; }
-    void *room(Arena &a) const { return a.take(any() ? M * width_of(l->rank) * 2 : 0); }
+    int parts() const { return parts_of(X->type, Y->type == HG_F32); }
+    void *room(Arena &a, const LinearPlan &q) const
+    {
+        return any() ? room_of(a, M, l->rank, q.cut.tile == 0, parts()) : nullptr;
+    }
     hipError_t begin(lin::Product &p, Arena &a, const LinearPlan &q, bool bf16, hipStream_t s) const
     {
         if (!any())
             return hipSuccess;
-        void *T = room(a);
+        void *T = room(a, q);
         const bool few = q.cut.tile == 0;
         // (see OwnSums of hg_linear_rowwise.hip)
         if (few && q.direct && lin::weight_blocks(N, p.f.save == lin::kSave8) == 1 && M == 1 && l->rank <= lin::kOwnRank &&
             (N + 15) / 16 <= hg::cu_count()) {
-            p.ad = {l->which, static_cast<const uint16_t *>(l->B), nullptr, l->stride_b, l->ldb, 0, (int32_t)l->count, l->rank};
+            p.ad = {l->which, static_cast<const uint16_t *>(l->B), nullptr, l->stride_b, l->ldb, 0, (int32_t)l->count, l->rank, 2};
             p.own = static_cast<const uint16_t *>(l->A);
             p.own_scales = l->scales;
             p.own_stride = l->stride_a;
             p.own_ld = l->lda;
             return hipSuccess;
         }
-        const int64_t ldt = few ? up8(l->rank) : width_of(l->rank);
-        p.ad = {l->which, static_cast<const uint16_t *>(l->B), T, l->stride_b, l->ldb, ldt, (int32_t)l->count, l->rank};
+        const int64_t ldt = width_of(l->rank, few, parts());
+        p.ad = {l->which, static_cast<const uint16_t *>(l->B), T, l->stride_b, l->ldb, ldt, (int32_t)l->count, l->rank, parts()};
         return lin::launch_shrink({static_cast<const uint16_t *>(X->data), static_cast<const uint16_t *>(l->A), l->which,
                                    l->scales, T, X->ld, l->lda, l->stride_a, ldt, (int32_t)M, (int32_t)K,
-                                   (int32_t)l->count, l->rank, few, direct_rows()},
+                                   (int32_t)l->count, l->rank, parts(), few, direct_rows()},
                                   bf16, s);
     }
 };
@@ -101,27 +111,24 @@ extern "C" {
 int64_t hg_linear_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, const hg_matrix *X,
                                           const hg_matrix *W)
 {
-    int64_t need = linear_room(M, N, K, X, W, most_tile_of(rank));
-    if (need < 0 && need > -4)
-        return need;
-    // (a call may have no adapters, whatever their rank)
-    need = std::max(need, linear_room(M, N, K, X, W));
+    // A call may have no adapters, whatever their rank, and Y of either type.
+    const int64_t alone = linear_room(M, N, K, X, W);
+    if (alone < 0 && alone > -4)
+        return alone;
     if (rank < 0 || rank > HG_ADAPTERS_MAX_RANK)
         return -4;
-    if (need < 0)
-        return need - 1;
-    if (M == 0 || N == 0 || K == 0)
-        return 0;
-    Arena a{nullptr};
-    a.take(M * width_of(rank) * 2);
-    return need + a.used;
+    if (alone < 0)
+        return alone - 1;
+    return std::max(alone, linear_room(M, N, K, X, W, most_tile_of(rank), [&](Arena &a, const LinearPlan &q) {
+                        room_of(a, M, rank, q.cut.tile == 0, parts_of(X->type, true));
+                    }));
 }
 
 int hg_linear_adapters(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W,
                        const float *bias, const hg_matrix *R, const hg_matrix *Y, const hg_matrix *Z,
                        const hg_adapters *adapters, void *work, int64_t work_bytes, void *stream)
 {
-    return linear_call<-12>(act, M, N, K, X, W, bias, R, Y, Z, Beside{adapters, X, M, N, K}, work, work_bytes, stream);
+    return linear_call<-12>(act, M, N, K, X, W, bias, R, Y, Z, Beside{adapters, X, Y, M, N, K}, work, work_bytes, stream);
 }
 
 }  // extern "C"

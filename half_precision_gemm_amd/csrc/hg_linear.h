@@ -51,13 +51,15 @@ constexpr int kFewRows = 64;      // rows that the forms for few rows take
 // two 16-bit numbers whose sum it is, up8 high ones and up8 low ones, with zeros
 // up to a multiple of 32.  The rest of such a number is 2^-16 (bf16) or 2^-22
 // of it, and the sums take it as 2·up8 more terms of the matrix cores' 32 at
-// once: at rank 16 as many instructions as one 16-bit number would take.
+// once: at rank 16 as many instructions as one 16-bit number would take.  A bf16
+// product whose result is fp32, where 2^-16 would show, has a third number, up8
+// more behind the low ones: all 24 bits.
 struct Adapters {
     const int64_t *which;         // M values
     const uint16_t *B;            // adapter g: cols×rank at B + g·stride, null: no adapters
     const void *T;
     int64_t stride, ldb, ldt;
-    int32_t count, rank;
+    int32_t count, rank, parts;   // parts: numbers of X's type for one of T, 2 or 3
 };
 
 // One product: C[rows×cols] = Σ_k A(i, k)·B(j, k).  An operand is stored
@@ -146,7 +148,7 @@ hipError_t launch_prepare(const Slope &g, const Copy &x, const Copy &w, bool bf1
 
 // T of Adapters from X (M×K, any address) and the adapters' A (adapter g: rank×K
 // at A + g·stride), with the adapters' scales (null: 1); rows without an adapter
-// are left alone.  wide: fp32, else two 16-bit numbers.  direct: rows of X and A are
+// are left alone.  wide: fp32, else `parts` 16-bit numbers.  direct: rows of X and A are
 // whole 16-byte pieces at 16-byte addresses, 32-bit offsets reach 256 of X's.
 struct Shrink {
     const uint16_t *X, *A;
@@ -154,7 +156,7 @@ struct Shrink {
     const float *scales;
     void *T;
     int64_t ldx, lda, stride, ldt;
-    int32_t M, K, count, rank;
+    int32_t M, K, count, rank, parts;
     bool wide, direct;
 };
 hipError_t launch_shrink(const Shrink &q, bool bf16, hipStream_t s);
@@ -838,6 +840,14 @@ __device__ __forceinline__ int adapter_of(const Adapters &a, int row, int rows)
     const int64_t g = row < rows ? a.which[row] : -1;
     return g >= 0 && g < a.count ? (int)g : -1;
 }
+// Which eight of an adapter's B the c-th eight of a row of T meets: high, low and
+// third numbers the same, the zeros behind them any.
+__device__ __forceinline__ int eight_of_b(int c, int chunks)
+{
+    c -= c >= chunks ? chunks : 0;
+    c -= c >= chunks ? chunks : 0;
+    return c < chunks ? c : 0;
+}
 // Elements k .. k + 7 of row `row` of an adapter's B (cols rows of `rank`), zeros
 // behind the rank.  What follows a row in memory is loaded with it and cut off, but
 // for the last rows, behind which nothing may be: those element by element.
@@ -933,7 +943,9 @@ __device__ __forceinline__ int least_of_rows(int v)
 // gathered (add_gathered).
 constexpr int kTurns = 4;
 
-template <bool BF16, int TI, int TJ>
+// (PARTS a template argument: a branch in the last loop cost 333×1111×777, rank 9, 0.7
+// of 21.5 us.)
+template <bool BF16, int PARTS, int TI, int TJ>
 __device__ __forceinline__ void add_by_rows(const Product &p, const int (&mine)[TI], int row0, int col0, int lane,
                                             floatx4 (&acc)[TI][TJ])
 {
@@ -952,6 +964,12 @@ __device__ __forceinline__ void add_by_rows(const Product &p, const int (&mine)[
 #pragma unroll
             for (int q = 0; q < 8; ++q)
                 t[q] += low[q];
+            if constexpr (PARTS > 2) {
+                load8<BF16>(T + 16 * i * a.ldt + 2 * up + k, 8, low);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    t[q] += low[q];
+            }
 #pragma unroll
             for (int j = 0; j < TJ; j += 2)
                 add_eight<BF16, 2>(a, a.B + mine[i] * a.stride, col0 + 4 * fhi + 16 * j, p.N, k, t, acc[i] + j);
@@ -964,8 +982,10 @@ __device__ __forceinline__ void add_by_rows(const Product &p, const int (&mine)[
             if (mine[i] < 0)
                 continue;
             const uint16_t *t = T + 16 * i * a.ldt + k;
-            add_singly<BF16, TJ>(a, a.B + mine[i] * a.stride, col0 + 4 * fhi, p.N, k, widen<BF16>(t[0]) + widen<BF16>(t[up]),
-                                 acc[i]);
+            float v = widen<BF16>(t[0]) + widen<BF16>(t[up]);
+            if constexpr (PARTS > 2)
+                v += widen<BF16>(t[2 * up]);
+            add_singly<BF16, TJ>(a, a.B + mine[i] * a.stride, col0 + 4 * fhi, p.N, k, v, acc[i]);
         }
     }
 }
@@ -998,7 +1018,7 @@ __device__ __forceinline__ void add_gathered(const Product &p, int row0, int col
     constexpr int AHEAD = 4, PIECES = 4 * TJ;
     const Adapters &a = p.ad;
     const int frow = lane & 15, fhi = lane >> 4;
-    const int chunks = (a.rank + 7) / 8, steps = (2 * chunks + 3) / 4;
+    const int chunks = (a.rank + 7) / 8, steps = (a.parts * chunks + 3) / 4;
     const int mine = lane < 16 * TI ? adapter_of(a, row0 + lane, p.M) : -1;
     const uint64_t below = ((uint64_t)1 << lane) - 1;
     auto place = [&](int row, int j) __attribute__((always_inline)) {
@@ -1027,7 +1047,7 @@ __device__ __forceinline__ void add_gathered(const Product &p, int row0, int col
             s = 0;
         }
         u.kind = s == steps ? NONE : s + 1 == steps ? LAST : SOME;
-        const int c = 4 * min(s, steps - 1) + fhi, cb = c < chunks ? c : c < 2 * chunks ? c - chunks : 0;
+        const int c = 4 * min(s, steps - 1) + fhi, cb = eight_of_b(c, chunks);
         const uint16_t *B = a.B + g * a.stride;
 #pragma unroll
         for (int j = 0; j < TJ; ++j)
@@ -1091,7 +1111,7 @@ __device__ __forceinline__ void add_adapters(const Product &p, int row0, int col
 {
     const Adapters &a = p.ad;
     const int frow = lane & 15, fhi = lane >> 4;
-    const int chunks = (a.rank + 7) / 8, steps = (2 * chunks + 3) / 4;
+    const int chunks = (a.rank + 7) / 8, steps = (a.parts * chunks + 3) / 4;
     int mine[TI];
 #pragma unroll
     for (int i = 0; i < TI; ++i)
@@ -1114,15 +1134,16 @@ __device__ __forceinline__ void add_adapters(const Product &p, int row0, int col
             add_gathered<false, BF16>(p, row0, col0, lane, lds, acc);
         else if (a.rank * TI >= kGatherFrom && a.ldb % 2 == 0 && col0 + 16 * TJ + 8 <= p.N)
             add_gathered<true, BF16>(p, row0, col0, lane, lds, acc);
+        else if (BF16 && a.parts > 2)
+            add_by_rows<BF16, 3>(p, mine, row0, col0, lane, acc);
         else
-            add_by_rows<BF16>(p, mine, row0, col0, lane, acc);
+            add_by_rows<BF16, 2>(p, mine, row0, col0, lane, acc);
         return;
     }
     for (int g = after(-1); g != NONE_LEFT; g = after(g)) {
         const uint16_t *B = a.B + g * a.stride;
         for (int s = 0; s < steps; ++s) {
-            // low halves meet the same B, the zeros behind them its first eight
-            const int c = 4 * s + fhi, cb = c < chunks ? c : c < 2 * chunks ? c - chunks : 0;
+            const int c = 4 * s + fhi, cb = eight_of_b(c, chunks);
             half8 b[TJ], t[TI];
 #pragma unroll
             for (int j = 0; j < TJ; ++j)

@@ -365,8 +365,10 @@ inline LinearRoom room_linear(Arena &a, const LinearPlan &q, int64_t M, int64_t 
     return r;
 }
 
-// Workspace of the forward product, whatever Y and Z.
-inline int64_t linear_room(int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W, int most = 256)
+// Workspace of the forward product, whatever Y and Z, and of what goes beside it:
+// beside(arena, plan).
+template <class Beside>
+int64_t linear_room(int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W, int most, Beside beside)
 {
     if (const int e = check_sizes(M, N, K, 1))
         return e;
@@ -377,10 +379,19 @@ inline int64_t linear_room(int64_t M, int64_t N, int64_t K, const hg_matrix *X, 
     if (M == 0 || N == 0 || K == 0)
         return 0;
     // A call that saves Z in 8 bits may take another kernel.
-    Arena a{nullptr}, b{nullptr};
-    room_linear(a, plan_linear(M, N, K, X, W, false, most), M, N, K);
-    room_linear(b, plan_linear(M, N, K, X, W, true, most), M, N, K);
-    return std::max(a.used, b.used);
+    int64_t need = 0;
+    for (const bool save8 : {false, true}) {
+        const LinearPlan q = plan_linear(M, N, K, X, W, save8, most);
+        Arena a{nullptr};
+        room_linear(a, q, M, N, K);
+        beside(a, q);
+        need = std::max(need, a.used);
+    }
+    return need;
+}
+inline int64_t linear_room(int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W)
+{
+    return linear_room(M, N, K, X, W, 256, [](Arena &, const LinearPlan &) {});
 }
 
 // The forward product: hg_linear's arguments 1 to 10 as they are numbered there
@@ -390,7 +401,7 @@ struct Nothing {
     int valid() const { return HG_OK; }                                     // its own arguments
     int check(const Span &, const Span &, const Span &) const { return HG_OK; }   // against Y, Z and Z's scales
     int most_tile() const { return 256; }
-    void room(Arena &) const {}                                             // its part of the workspace
+    void room(Arena &, const LinearPlan &) const {}                         // its part of the workspace
     bool meets(const Span &) const { return false; }
     // What is launched first.
     hipError_t begin(lin::Product &, Arena &, const LinearPlan &, bool, hipStream_t) const { return hipSuccess; }
@@ -434,7 +445,7 @@ int linear_call(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, co
     Arena count{nullptr};
     if (K > 0) {
         room_linear(count, q, M, N, K);
-        beside.room(count);
+        beside.room(count, q);
     }
     const Span wk = span_of(work, count.used);
     if (bad_work(work, count.used) || any_meet({wk}, {sx, sw, sb, sr, sy, sz, ss}) || beside.meets(wk))

@@ -35,12 +35,16 @@ __device__ __forceinline__ void store_t(const Shrink &q, int64_t row, int k, flo
         static_cast<float *>(q.T)[row * q.ldt + k] = v;
         return;
     }
+    const int up = (q.rank + 7) / 8 * 8;
     uint16_t *t = static_cast<uint16_t *>(q.T) + row * q.ldt + k;
     const uint16_t high = narrow<BF16>(v);
-    const float rest = v - widen<BF16>(high);
-    t[0] = high;
     // (of an infinity or NaN there is no rest)
-    t[(q.rank + 7) / 8 * 8] = __builtin_fabsf(widen<BF16>(high)) < __builtin_inff() ? narrow<BF16>(rest) : (uint16_t)0;
+    const float rest = __builtin_fabsf(widen<BF16>(high)) < __builtin_inff() ? v - widen<BF16>(high) : 0.0f;
+    const uint16_t low = narrow<BF16>(rest);
+    t[0] = high;
+    t[up] = low;
+    if (q.parts > 2)
+        t[2 * up] = narrow<BF16>(rest - widen<BF16>(low));
 }
 // Zeros behind the rank, thread `t` of `n`.
 __device__ __forceinline__ void store_zeros(const Shrink &q, int64_t row, int t, int n)
@@ -53,7 +57,7 @@ __device__ __forceinline__ void store_zeros(const Shrink &q, int64_t row, int t,
     }
     uint16_t *r = static_cast<uint16_t *>(q.T) + row * q.ldt;
     for (int k = q.rank + t; k < q.ldt; k += n)
-        if (k < up || k >= up + q.rank)
+        if (k >= q.parts * up || k - (k >= 2 * up ? 2 * up : k >= up ? up : 0) >= q.rank)
             r[k] = 0;
 }
 
@@ -132,7 +136,7 @@ __device__ __forceinline__ Pieces pieces_of(const Shrink &q, int row0, int lane,
     Pieces m{-1, 0, -1, 0};
     uint64_t marks = 0;
     if (wave < SETS) {
-        const Adapters who{q.which, nullptr, nullptr, 0, 0, 0, q.count, q.rank};
+        const Adapters who{q.which, nullptr, nullptr, 0, 0, 0, q.count, q.rank, q.parts};
         int v[SETS];
         uint64_t same[SETS];
 #pragma unroll

@@ -125,7 +125,7 @@ __device__ __forceinline__ void add_adapters_straight(const Product &p, int row0
 {
     const Adapters &a = p.ad;
     const int frow = lane & 15, fhi = lane >> 4;
-    const int chunks = a.rank / 8, steps = (2 * chunks + 3) / 4;
+    const int chunks = a.rank / 8, steps = (a.parts * chunks + 3) / 4;
     int mine[T];
 #pragma unroll
     for (int i = 0; i < T; ++i)
@@ -142,7 +142,7 @@ __device__ __forceinline__ void add_adapters_straight(const Product &p, int row0
     if (first == NONE_LEFT)
         return;
     for (int s = 0; s < steps; ++s) {
-        const int c = 4 * s + fhi, cb = c < chunks ? c : c < 2 * chunks ? c - chunks : 0;
+        const int c = 4 * s + fhi, cb = eight_of_b(c, chunks);
         u32x4 b[T], ahead[T], t[T];
         auto request = [&](int g) __attribute__((always_inline)) {
             const uint16_t *B = a.B + g * a.stride + 8 * cb;

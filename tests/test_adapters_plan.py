@@ -97,3 +97,18 @@ def test_without_adapters_the_layer_is_cut_alike(lib, M, N, K, kw):
     work = lib.hg_linear_adapters_workspace_size(M, N, K, kw["rank"], X, W)
     assert lib.hg_linear_adapters(4, M, N, K, X, W, None, None, Y, None, L, 9 * SPACE, work, None) == 0
     assert lib.plan_launches() == alone
+
+
+@pytest.mark.parametrize("M,N,K", [(100, 512, 512), (1000, 4096, 256), (8192, 4096, 4096), (32, 7412, 11584), (3, 512, 512), (300, 260, 4000)])
+@pytest.mark.parametrize("rank", [1, 8, 11, 16, 24, 64, 256])
+def test_three_numbers_for_an_fp32_result(lib, M, N, K, rank):
+    """Rows of T for bf16 products with Y in fp32, in the workspace that is the same for any Y."""
+    X, W = mat(0, K), mat(1, K)
+    L = adapters.Adapters(5 * SPACE, None, 6 * SPACE, K, rank * K, 7 * SPACE, rank, N * rank, 4, rank, BF16)
+    work = lib.hg_linear_adapters_workspace_size(M, N, K, rank, X, W)
+    up = -(-rank // 8) * 8
+    for type, parts in ((F32, 3), (BF16, 2)):
+        assert lib.hg_linear_adapters(0, M, N, K, X, W, None, None, mat(2, N, type), None, L, 9 * SPACE, work, None) == 0
+        kernel, edge = lib.plan_launches().decode().split()[:2]
+        if kernel != "rowwise":
+            assert edge == "edge=%d" % (up if kernel == "shrink_wide" else -(-parts * up // 32) * 32)

@@ -406,3 +406,37 @@ def test_an_infinite_a_of_one_row(hg, t, K):
         Y = torch.empty(1, N, dtype=F32, device=DEV)
         hg.linear_adapters(X.to(DEV), W.to(DEV), Y, which.to(DEV), a.to(DEV), B.to(DEV))
         assert torch.equal(Y[0].cpu(), torch.where(B[1, :, 3] > 0, float("inf"), -float("inf")).float()), k
+
+
+# W is zero, and A and B have one value a value of T and a column: T comes out alone, with nothing that a sum could hide.
+# 64×64 tiles at any address, 64×64, 128×128, 256×256, slices of each, few rows in tiles.
+PLANS = [(333, 111, 777), (100, 512, 512), (1000, 4096, 256), (4096, 4096, 64), (300, 260, 4000), (32, 7412, 11584)]
+
+
+def alone(M, N, K, rank, count, t, order, a=1.0, b=1.0, spread=False):
+    """(X, W, A, B, s, which, T in fp32 by column); a: A's values, b: B's; spread: rows of very different size."""
+    X, _, _, _, s, which = operands(M, N, K, rank, count, t, order)
+    g = torch.Generator().manual_seed(M + N + K + rank)
+    if spread:
+        X = (X * torch.exp2(torch.randint(-9, 6, (M, 1), generator=g).float())).to(t)
+    A, B = torch.zeros(count, rank, K, dtype=t), torch.zeros(count, N, rank, dtype=t)
+    at = torch.randint(0, K, (count, rank), generator=g)
+    value = (a * torch.randn(count, rank, generator=g).clamp(-2, 2)).to(t)
+    A.scatter_(2, at[:, :, None], value[:, :, None])
+    B[:, torch.arange(N), torch.arange(N) % rank] = b
+    T = torch.zeros(M, rank)
+    for c in range(count):
+        rows = which == c
+        T[rows] = X[rows][:, at[c]].float() * value[c].float() * s[c]
+    return X, torch.zeros(N, K, dtype=t), A, B, s, which, T[:, torch.arange(N) % rank]
+
+
+@pytest.mark.parametrize("M,N,K", PLANS)
+@pytest.mark.parametrize("rank", [1, 8, 16, 33, 64])
+@pytest.mark.parametrize("order,count", [("single", 40), ("runs", 3)])
+def test_t_is_as_exact_as_an_fp32_result(hg, M, N, K, rank, order, count):
+    """bf16 with Y in fp32: T as a sum of bf16 numbers loses nothing of its 24 bits."""
+    X, W, A, B, s, which, T = alone(M, N, K, rank, count, BF16, order)
+    Y = torch.empty(M, N, dtype=F32, device=DEV)
+    hg.linear_adapters(X.to(DEV), W.to(DEV), Y, which.to(DEV), A.to(DEV), B.to(DEV), scales=s.to(DEV))
+    assert torch.equal(Y.cpu(), T)
