@@ -20,9 +20,15 @@ int parts_of(int type, bool out32) { return type == HG_BF16 && out32 ? 3 : 2; }
 // Numbers that a row of T takes: fp32 ones up to a whole eight where it goes row by
 // row (`few`), else `parts` 16-bit ones for each, up to the matrix cores' 32.
 int64_t width_of(int64_t rank, bool few, int parts) { return few ? up8(rank) : (parts * up8(rank) + 31) / 32 * 32; }
-void *room_of(Arena &a, int64_t M, int64_t rank, bool few, int parts)
+struct Room {
+    void *T, *far;
+};
+Room room_of(Arena &a, int64_t M, int64_t rank, int type, bool few, int parts)
 {
-    return a.take(M * width_of(rank, few, parts) * (few ? 4 : 2));
+    Room r;
+    r.T = a.take(M * width_of(rank, few, parts) * (few ? 4 : 2));
+    r.far = type == HG_F16 && !few ? a.take(M * up8(rank) * 4) : nullptr;
+    return r;
 }
 
 // The largest tiles that may be taken: 256×256 ones add the terms of whole
@@ -75,20 +81,20 @@ struct Beside {
     }
     int most_tile() const { return any() ? most_tile_of(l->rank) : 256; }
     int parts() const { return parts_of(X->type, Y->type == HG_F32); }
-    void *room(Arena &a, const LinearPlan &q) const
+    Room room(Arena &a, const LinearPlan &q) const
     {
-        return any() ? room_of(a, M, l->rank, q.cut.tile == 0, parts()) : nullptr;
+        return any() ? room_of(a, M, l->rank, X->type, q.cut.tile == 0, parts()) : Room{nullptr, nullptr};
     }
     hipError_t begin(lin::Product &p, Arena &a, const LinearPlan &q, bool bf16, hipStream_t s) const
     {
         if (!any())
             return hipSuccess;
-        void *T = room(a, q);
+        const Room to = room(a, q);
         const bool few = q.cut.tile == 0;
         // (see OwnSums of hg_linear_rowwise.hip)
         if (few && q.direct && lin::weight_blocks(N, p.f.save == lin::kSave8) == 1 && M == 1 && l->rank <= lin::kOwnRank &&
             (N + 15) / 16 <= hg::cu_count()) {
-            p.ad = {l->which, static_cast<const uint16_t *>(l->B), nullptr, l->stride_b, l->ldb, 0, (int32_t)l->count, l->rank, 2};
+            p.ad = {l->which, static_cast<const uint16_t *>(l->B), nullptr, nullptr, l->stride_b, l->ldb, 0, (int32_t)l->count, l->rank, 2};
             p.own = static_cast<const uint16_t *>(l->A);
             p.own_scales = l->scales;
             p.own_stride = l->stride_a;
@@ -96,9 +102,11 @@ struct Beside {
             return hipSuccess;
         }
         const int64_t ldt = width_of(l->rank, few, parts());
-        p.ad = {l->which, static_cast<const uint16_t *>(l->B), T, l->stride_b, l->ldb, ldt, (int32_t)l->count, l->rank, parts()};
+        float *const far = static_cast<float *>(to.far);
+        p.ad = {l->which, static_cast<const uint16_t *>(l->B), to.T, far, l->stride_b, l->ldb, ldt, (int32_t)l->count, l->rank,
+                parts()};
         return lin::launch_shrink({static_cast<const uint16_t *>(X->data), static_cast<const uint16_t *>(l->A), l->which,
-                                   l->scales, T, X->ld, l->lda, l->stride_a, ldt, (int32_t)M, (int32_t)K,
+                                   l->scales, to.T, far, X->ld, l->lda, l->stride_a, ldt, (int32_t)M, (int32_t)K,
                                    (int32_t)l->count, l->rank, parts(), few, direct_rows()},
                                   bf16, s);
     }
@@ -120,7 +128,7 @@ int64_t hg_linear_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64
     if (alone < 0)
         return alone - 1;
     return std::max(alone, linear_room(M, N, K, X, W, most_tile_of(rank), [&](Arena &a, const LinearPlan &q) {
-                        room_of(a, M, rank, q.cut.tile == 0, parts_of(X->type, true));
+                        room_of(a, M, rank, X->type, q.cut.tile == 0, parts_of(X->type, true));
                     }));
 }
 

@@ -53,11 +53,14 @@ constexpr int kFewRows = 64;      // rows that the forms for few rows take
 // of it, and the sums take it as 2·up8 more terms of the matrix cores' 32 at
 // once: at rank 16 as many instructions as one 16-bit number would take.  A bf16
 // product whose result is fp32, where 2^-16 would show, has a third number, up8
-// more behind the low ones: all 24 bits.
+// more behind the low ones: all 24 bits.  What fp16 does not reach is infinite in
+// such a T and stands in `far` in fp32; the matrix cores get zeros for it, and it is
+// added by itself, which costs nothing where there is none (add_far).
 struct Adapters {
     const int64_t *which;         // M values
     const uint16_t *B;            // adapter g: cols×rank at B + g·stride, null: no adapters
     const void *T;
+    const float *far;             // rows of up8; fp16 in tiles, else null
     int64_t stride, ldb, ldt;
     int32_t count, rank, parts;   // parts: numbers of X's type for one of T, 2 or 3
 };
@@ -148,13 +151,14 @@ hipError_t launch_prepare(const Slope &g, const Copy &x, const Copy &w, bool bf1
 
 // T of Adapters from X (M×K, any address) and the adapters' A (adapter g: rank×K
 // at A + g·stride), with the adapters' scales (null: 1); rows without an adapter
-// are left alone.  wide: fp32, else `parts` 16-bit numbers.  direct: rows of X and A are
+// are left alone.  wide: fp32, else `parts` 16-bit numbers (and far: of fp16).  direct: rows of X and A are
 // whole 16-byte pieces at 16-byte addresses, 32-bit offsets reach 256 of X's.
 struct Shrink {
     const uint16_t *X, *A;
     const int64_t *which;
     const float *scales;
     void *T;
+    float *far;
     int64_t ldx, lda, stride, ldt;
     int32_t M, K, count, rank, parts;
     bool wide, direct;
@@ -917,6 +921,31 @@ __device__ __forceinline__ void add_singly(const Adapters &a, const uint16_t *B,
         for (int e = 0; e < 4; ++e)
             acc[j][e] = __builtin_fmaf(t, widen<BF16>(b[j][e]), acc[j][e]);
 }
+// Of eight fp16 numbers those that are infinite or NaN, as bits 15 and 31 of their
+// words (an exponent of all ones and its last place carry to the sign), and the
+// eight with zeros for these.
+__device__ __forceinline__ u32x4 past_fp16(const u32x4 &t) { return ((t & 0x7fff7fffu) + 0x04000400u) & 0x80008000u; }
+__device__ __forceinline__ u32x4 within_fp16(const u32x4 &t, const u32x4 &past) { return t & ~((past << 1) - (past >> 15)); }
+// Sets to zero what of eights of T is not finite; whether a row with an adapter has
+// such a number, the same in all lanes.
+template <bool BF16, int N>
+__device__ __forceinline__ bool hold_back(u32x4 (&t)[N], const int (&mine)[N])
+{
+    if constexpr (BF16)
+        return false;
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const u32x4 past = past_fp16(t[i]);
+        any |= mine[i] >= 0 ? past[0] | past[1] | past[2] | past[3] : 0u;
+    }
+    if (__builtin_amdgcn_ballot_w64(any != 0) == 0)
+        return false;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        t[i] = within_fp16(t[i], past_fp16(t[i]));
+    return true;
+}
 // The least of the lanes' values, the same in all of them, where lanes 16 apart
 // hold the same.
 __device__ __forceinline__ int least_of_rows(int v)
@@ -946,12 +975,19 @@ constexpr int kTurns = 4;
 // (PARTS a template argument: a branch in the last loop cost 333×1111×777, rank 9, 0.7
 // of 21.5 us.)
 template <bool BF16, int PARTS, int TI, int TJ>
-__device__ __forceinline__ void add_by_rows(const Product &p, const int (&mine)[TI], int row0, int col0, int lane,
+__device__ __forceinline__ bool add_by_rows(const Product &p, const int (&mine)[TI], int row0, int col0, int lane,
                                             floatx4 (&acc)[TI][TJ])
 {
     const Adapters &a = p.ad;
     const int frow = lane & 15, fhi = lane >> 4, up = (a.rank + 7) / 8 * 8;
     const uint16_t *T = static_cast<const uint16_t *>(a.T) + (row0 + frow) * a.ldt;
+    bool far = false;
+    // (the other numbers of one that is not finite are 0)
+    auto held_back = [&](float t) __attribute__((always_inline)) {
+        const bool in = BF16 || __builtin_fabsf(t) < __builtin_inff();
+        far |= !in;
+        return in ? t : 0.0f;
+    };
     int k = 0;
     for (; k + 8 <= a.rank; k += 8) {
 #pragma unroll
@@ -963,7 +999,7 @@ __device__ __forceinline__ void add_by_rows(const Product &p, const int (&mine)[
             load8<BF16>(T + 16 * i * a.ldt + up + k, 8, low);
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                t[q] += low[q];
+                t[q] = held_back(t[q]) + low[q];
             if constexpr (PARTS > 2) {
                 load8<BF16>(T + 16 * i * a.ldt + 2 * up + k, 8, low);
 #pragma unroll
@@ -982,12 +1018,13 @@ __device__ __forceinline__ void add_by_rows(const Product &p, const int (&mine)[
             if (mine[i] < 0)
                 continue;
             const uint16_t *t = T + 16 * i * a.ldt + k;
-            float v = widen<BF16>(t[0]) + widen<BF16>(t[up]);
+            float v = held_back(widen<BF16>(t[0])) + widen<BF16>(t[up]);
             if constexpr (PARTS > 2)
                 v += widen<BF16>(t[2 * up]);
             add_singly<BF16, TJ>(a, a.B + mine[i] * a.stride, col0 + 4 * fhi, p.N, k, v, acc[i]);
         }
     }
+    return !BF16 && __builtin_amdgcn_ballot_w64(far) != 0;
 }
 
 // Waits until the matrix cores have written these sums.  (Where a branch follows a
@@ -1012,7 +1049,7 @@ constexpr int kGatherFrom = 112;                    // rank times blocks of 16 r
 template <int TI, int TJ>
 constexpr int kGatherBytes = TI * TJ * 1024;
 template <bool CUT, bool BF16, int TI, int TJ>
-__device__ __forceinline__ void add_gathered(const Product &p, int row0, int col0, int lane, unsigned char *lds,
+__device__ __forceinline__ bool add_gathered(const Product &p, int row0, int col0, int lane, unsigned char *lds,
                                              floatx4 (&acc)[TI][TJ])
 {
     constexpr int AHEAD = 4, PIECES = 4 * TJ;
@@ -1062,6 +1099,7 @@ __device__ __forceinline__ void add_gathered(const Product &p, int row0, int col
 #pragma unroll
     for (int j = 0; j < TJ; ++j)
         sum[j] = floatx4{0, 0, 0, 0};
+    uint32_t far = 0;
     while (ring[0].kind != NONE) {
         static_for<AHEAD>([&](auto d) __attribute__((always_inline)) {
             Unit &u = ring[decltype(d)::value];
@@ -1073,6 +1111,11 @@ __device__ __forceinline__ void add_gathered(const Product &p, int row0, int col
                     for (int j = 0; j < TJ; ++j)
                         u.b[j][e] &= keep;
                 }
+            }
+            if constexpr (!BF16) {
+                const u32x4 past = past_fp16(u.t);
+                far |= u.row >= 0 ? past[0] | past[1] | past[2] | past[3] : 0u;
+                u.t = within_fp16(u.t, past);
             }
 #pragma unroll
             for (int j = 0; j < TJ; ++j)
@@ -1104,9 +1147,11 @@ __device__ __forceinline__ void add_gathered(const Product &p, int row0, int col
         }
     }
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    return !BF16 && __builtin_amdgcn_ballot_w64(far != 0) != 0;
 }
+// (Returns whether T has numbers for add_far in these rows.)
 template <bool BF16, int TI, int TJ>
-__device__ __forceinline__ void add_adapters(const Product &p, int row0, int col0, int lane, unsigned char *lds,
+__device__ __forceinline__ bool add_adapters(const Product &p, int row0, int col0, int lane, unsigned char *lds,
                                              floatx4 (&acc)[TI][TJ])
 {
     const Adapters &a = p.ad;
@@ -1131,27 +1176,30 @@ __device__ __forceinline__ void add_adapters(const Product &p, int row0, int col
         // (what follows a row in memory is loaded with it and cut off; columns that
         // less than eight elements may follow go row by row)
         if (a.rank * TI >= kGatherFrom && a.rank % 8 == 0)
-            add_gathered<false, BF16>(p, row0, col0, lane, lds, acc);
-        else if (a.rank * TI >= kGatherFrom && a.ldb % 2 == 0 && col0 + 16 * TJ + 8 <= p.N)
-            add_gathered<true, BF16>(p, row0, col0, lane, lds, acc);
-        else if (BF16 && a.parts > 2)
-            add_by_rows<BF16, 3>(p, mine, row0, col0, lane, acc);
-        else
-            add_by_rows<BF16, 2>(p, mine, row0, col0, lane, acc);
-        return;
+            return add_gathered<false, BF16>(p, row0, col0, lane, lds, acc);
+        if (a.rank * TI >= kGatherFrom && a.ldb % 2 == 0 && col0 + 16 * TJ + 8 <= p.N)
+            return add_gathered<true, BF16>(p, row0, col0, lane, lds, acc);
+        if constexpr (BF16) {
+            if (a.parts > 2)
+                return add_by_rows<BF16, 3>(p, mine, row0, col0, lane, acc);
+        }
+        return add_by_rows<BF16, 2>(p, mine, row0, col0, lane, acc);
     }
+    bool far = false;
     for (int g = after(-1); g != NONE_LEFT; g = after(g)) {
         const uint16_t *B = a.B + g * a.stride;
         for (int s = 0; s < steps; ++s) {
             const int c = 4 * s + fhi, cb = eight_of_b(c, chunks);
-            half8 b[TJ], t[TI];
+            half8 b[TJ];
+            u32x4 t[TI];
 #pragma unroll
             for (int j = 0; j < TJ; ++j)
                 b[j] = __builtin_bit_cast(half8, load_b(a, B, min(col0 + 16 * j + frow, p.N - 1), p.N, 8 * cb));
 #pragma unroll
             for (int i = 0; i < TI; ++i)
-                t[i] = *reinterpret_cast<const half8 *>(static_cast<const uint16_t *>(a.T) +
+                t[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.T) +
                                                         min(row0 + 16 * i + frow, p.M - 1) * a.ldt + 8 * c);
+            far |= hold_back<BF16>(t, mine);
 #pragma unroll
             for (int i = 0; i < TI; ++i) {
                 const bool me = mine[i] == g;
@@ -1160,11 +1208,11 @@ __device__ __forceinline__ void add_adapters(const Product &p, int row0, int col
                 if (__builtin_amdgcn_ballot_w64(!me && row0 + 16 * i + frow < p.M) == 0) {
 #pragma unroll
                     for (int j = 0; j < TJ; ++j)
-                        acc[i][j] = mfma_16x16x32<BF16>(b[j], t[i], acc[i][j]);
+                        acc[i][j] = mfma_16x16x32<BF16>(b[j], __builtin_bit_cast(half8, t[i]), acc[i][j]);
                 } else {
 #pragma unroll
                     for (int j = 0; j < TJ; ++j) {
-                        const floatx4 sum = mfma_16x16x32<BF16>(b[j], t[i], acc[i][j]);
+                        const floatx4 sum = mfma_16x16x32<BF16>(b[j], __builtin_bit_cast(half8, t[i]), acc[i][j]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             acc[i][j][e] = me ? sum[e] : acc[i][j][e];
@@ -1176,6 +1224,7 @@ __device__ __forceinline__ void add_adapters(const Product &p, int row0, int col
 #pragma unroll
     for (int i = 0; i < TI; ++i)
         settled(acc[i]);
+    return far;
 }
 
 // ---- Wave-private staging of a 16×W block of sums (fp32) in LDS, from the
@@ -1206,6 +1255,36 @@ __device__ __forceinline__ void stage_get(const unsigned char *s, int row, int u
     for (int e = 0; e < 4; ++e) {
         v[e] = lo[e];
         v[4 + e] = hi[e];
+    }
+}
+
+// Adds what of T fp16 does not reach to a wave's staged 16×W block at (row0, col0):
+// its terms one by one, in the rows that have some, where the wave has met one.  Slow
+// and rare: 8192×4096×4096, rank 16, 273 us without such a value (as before there
+// was this), 335 with one such row, 553 with 64.
+template <int W>
+__device__ __forceinline__ void add_far(const Product &p, int row0, int col0, int lane, unsigned char *stg)
+{
+    const Adapters &a = p.ad;
+    const int row = row0 + (lane & 15), fhi = lane >> 4, g = adapter_of(a, row, p.M);
+    if (g < 0)
+        return;
+    const uint16_t *T = static_cast<const uint16_t *>(a.T) + row * a.ldt, *B = a.B + g * a.stride;
+    const float *far = a.far + (int64_t)row * ((a.rank + 7) / 8 * 8);
+#pragma clang loop unroll(disable)
+    for (int k = 0; k < a.rank; ++k) {
+        if (__builtin_fabsf(widen<false>(T[k])) < __builtin_inff())
+            continue;
+        const float t = far[k];
+#pragma clang loop unroll(disable)
+        for (int j = 0; j < W / 16; ++j) {
+            floatx4 *v = reinterpret_cast<floatx4 *>(stg + stage_at<W>(lane & 15, 4 * j + fhi));
+            floatx4 sum = *v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sum[e] = __builtin_fmaf(t, widen<false>(B[min(col0 + 16 * j + 4 * fhi + e, p.N - 1) * a.ldb + k]), sum[e]);
+            *v = sum;
+        }
     }
 }
 

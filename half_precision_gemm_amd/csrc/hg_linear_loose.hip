@@ -139,10 +139,11 @@ __global__ void __launch_bounds__(THREADS, 2) linear_loose_kernel(const Product 
 
     unsigned char *stg = smem + wave * (16 * WT * 4);
     const int row0 = t.m0 + wm * WT;
+    bool far = false;
     if constexpr (ADAPT) {
         static_assert(4 * (16 * WT * 4 + kGatherBytes<T, T>) <= sizeof smem, "");
         if (t.kt0 == 0)
-            add_adapters<BF16>(p, row0, t.n0 + wn * WT, lane, smem + 4 * (16 * WT * 4) + wave * kGatherBytes<T, T>, acc);
+            far = add_adapters<BF16>(p, row0, t.n0 + wn * WT, lane, smem + 4 * (16 * WT * 4) + wave * kGatherBytes<T, T>, acc);
     }
     Drain<EDGE, WT, BF16> out(p, t, stg, lane, t.n0 + wn * WT);
     out.request(row0);
@@ -151,6 +152,11 @@ __global__ void __launch_bounds__(THREADS, 2) linear_loose_kernel(const Product 
     for (int i = 0; i < T; ++i) {
         stage_put<WT>(stg, lane, acc[i]);
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        if constexpr (ADAPT && !BF16) {
+            if (far)
+                add_far<WT>(p, row0 + 16 * i, t.n0 + wn * WT, lane, stg);
+            __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        }
         out.block(row0 + 16 * i, i == T - 1);
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
     }

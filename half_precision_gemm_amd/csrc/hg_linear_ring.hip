@@ -148,10 +148,11 @@ __device__ __forceinline__ void ring_tile(const Product &p, const Spread &w, int
 
     unsigned char *stg = smem + wave * (16 * WT * 4);
     const int row0 = m0 + wm * WT;
+    bool far = false;
     if constexpr (ADAPT) {
         static_assert(4 * (16 * WT * 4 + kGatherBytes<T, T>) <= kLds<EDGE>, "");
         if (kt0 == 0)
-            add_adapters<BF16>(p, row0, n0 + wn * WT, lane, smem + 4 * (16 * WT * 4) + wave * kGatherBytes<T, T>, acc);
+            far = add_adapters<BF16>(p, row0, n0 + wn * WT, lane, smem + 4 * (16 * WT * 4) + wave * kGatherBytes<T, T>, acc);
     }
     Drain<EDGE, WT, BF16> out(p, t, stg, lane, n0 + wn * WT);
     out.request(row0);
@@ -162,6 +163,11 @@ __device__ __forceinline__ void ring_tile(const Product &p, const Spread &w, int
         // a wave's LDS accesses execute in order; the fences keep the compiler
         // from moving them across
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        if constexpr (ADAPT && !BF16) {
+            if (far)
+                add_far<WT>(p, row0 + 16 * i, n0 + wn * WT, lane, stg);
+            __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        }
         out.block(row0 + 16 * i, i == T - 1);
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
     }

@@ -39,10 +39,13 @@ __device__ __forceinline__ void store_t(const Shrink &q, int64_t row, int k, flo
     uint16_t *t = static_cast<uint16_t *>(q.T) + row * q.ldt + k;
     const uint16_t high = narrow<BF16>(v);
     // (of an infinity or NaN there is no rest)
-    const float rest = __builtin_fabsf(widen<BF16>(high)) < __builtin_inff() ? v - widen<BF16>(high) : 0.0f;
+    const bool in = __builtin_fabsf(widen<BF16>(high)) < __builtin_inff();
+    const float rest = in ? v - widen<BF16>(high) : 0.0f;
     const uint16_t low = narrow<BF16>(rest);
     t[0] = high;
     t[up] = low;
+    if (!BF16 && !in)
+        q.far[row * up + k] = v;
     if (q.parts > 2)
         t[2 * up] = narrow<BF16>(rest - widen<BF16>(low));
 }
@@ -136,7 +139,7 @@ __device__ __forceinline__ Pieces pieces_of(const Shrink &q, int row0, int lane,
     Pieces m{-1, 0, -1, 0};
     uint64_t marks = 0;
     if (wave < SETS) {
-        const Adapters who{q.which, nullptr, nullptr, 0, 0, 0, q.count, q.rank, q.parts};
+        const Adapters who{q.which, nullptr, nullptr, nullptr, 0, 0, 0, q.count, q.rank, q.parts};
         int v[SETS];
         uint64_t same[SETS];
 #pragma unroll

@@ -120,8 +120,9 @@ __device__ __forceinline__ void multiply_in_place(const half8 &a, const half8 &b
 // that zero times an infinity or NaN of this adapter's B does not reach those rows,
 // eight numbers with one among them count as zeros, and the adapter's own rows get
 // a NaN from T instead.
+// (Returns whether T has numbers for add_far in these rows.)
 template <bool BF16>
-__device__ __forceinline__ void add_adapters_straight(const Product &p, int row0, int col0, int lane, floatx4 (&acc)[T][T])
+__device__ __forceinline__ bool add_adapters_straight(const Product &p, int row0, int col0, int lane, floatx4 (&acc)[T][T])
 {
     const Adapters &a = p.ad;
     const int frow = lane & 15, fhi = lane >> 4;
@@ -140,7 +141,8 @@ __device__ __forceinline__ void add_adapters_straight(const Product &p, int row0
     };
     const int first = after(-1);
     if (first == NONE_LEFT)
-        return;
+        return false;
+    bool far = false;
     for (int s = 0; s < steps; ++s) {
         const int c = 4 * s + fhi, cb = eight_of_b(c, chunks);
         u32x4 b[T], ahead[T], t[T];
@@ -155,6 +157,7 @@ __device__ __forceinline__ void add_adapters_straight(const Product &p, int row0
         for (int i = 0; i < T; ++i)
             t[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.T) +
                                                     min(row0 + 16 * i + frow, p.M - 1) * a.ldt + 8 * c);
+        far |= hold_back<BF16>(t, mine);
         int g = first, next;
         do {
             bool bad = false;
@@ -179,6 +182,7 @@ __device__ __forceinline__ void add_adapters_straight(const Product &p, int row0
             g = next;
         } while (g != NONE_LEFT);
     }
+    return far;
 }
 
 template <bool TA, bool TB, bool KCHK, bool BF16, bool ADAPT = false>
@@ -312,11 +316,12 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
             as = an;
             bs = bn;
         }
+        bool far = false;
         if constexpr (ADAPT) {
             // the K loop's last results are in their registers
             __asm__ volatile("s_nop 15\n\ts_nop 15");
             if (t.kt0 == 0)
-                add_adapters_straight<BF16>(p, t.m0 + wm * WT, t.n0 + wn * WT, lane, acc);
+                far = add_adapters_straight<BF16>(p, t.m0 + wm * WT, t.n0 + wn * WT, lane, acc);
         }
         // the ring's last loads (zero fills) and everyone's reads are done:
         // the slots are free
@@ -329,10 +334,10 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
         // put() are not seen by the compiler's check for that)
         __asm__ volatile("s_nop 15\n\ts_nop 15");
 
-        const int row0 = t.m0 + wm * WT;
+        const int row0 = t.m0 + wm * WT, col0 = t.n0 + wn * WT;
         const int stg = 2 * SLOT + wave * (16 * WT * 4);
         prev = t.m0 + EDGE <= p.M && t.n0 + EDGE <= p.N ? 1 : 2;
-        Drain<EDGE, WT, BF16> out(p, t, smem + stg, lane, t.n0 + wn * WT);
+        Drain<EDGE, WT, BF16> out(p, t, smem + stg, lane, col0);
         out.request(row0);
         __builtin_amdgcn_sched_barrier(0);
         id += gridDim.x;
@@ -351,6 +356,11 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
                     put(acc[b], lds_base + stg, lane);
             });
             __atomic_signal_fence(__ATOMIC_SEQ_CST);
+            if constexpr (ADAPT && !BF16) {
+                if (far)
+                    add_far<WT>(p, row0 + 16 * i, col0, lane, smem + stg);
+                __atomic_signal_fence(__ATOMIC_SEQ_CST);
+            }
             out.block(row0 + 16 * i, i == T - 1);
             __atomic_signal_fence(__ATOMIC_SEQ_CST);
         }

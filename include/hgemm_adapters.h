@@ -58,8 +58,9 @@ typedef struct hg_adapters {
  * X·A_gᵀ and its scaling are computed in fp32.  For the second product it is
  * kept in fp32 (few rows), as the sum of three HG_BF16 numbers if Y is HG_F32
  * (all of its 24 bits), or of two numbers of X's type, off by at most 2^-16
- * (HG_BF16) or 2^-22 (HG_F16, and 2^-25 where that is more) of it; in HG_F16 a
- * value past 65504 is infinite there.  Rows whose adapter's B_g holds
+ * (HG_BF16) or 2^-22 (HG_F16, and 2^-25 where that is more) of it.  In HG_F16 a
+ * value that rounds past 65504 is kept in fp32 in any case (which takes longer in
+ * the rows that have one).  Rows whose adapter's B_g holds
  * an infinity or NaN may come out NaN in any column.  Nothing of another row
  * enters a row's result (its last bits may differ with the rows beside it, which
  * choose the order of its sums): what is not finite in one request's row or

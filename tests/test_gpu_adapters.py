@@ -432,7 +432,7 @@ def alone(M, N, K, rank, count, t, order, a=1.0, b=1.0, spread=False):
 
 
 @pytest.mark.parametrize("M,N,K", PLANS)
-@pytest.mark.parametrize("rank", [1, 8, 16, 33, 64])
+@pytest.mark.parametrize("rank", [1, 8, 16, 33, 60, 64])
 @pytest.mark.parametrize("order,count", [("single", 40), ("runs", 3)])
 def test_t_is_as_exact_as_an_fp32_result(hg, M, N, K, rank, order, count):
     """bf16 with Y in fp32: T as a sum of bf16 numbers loses nothing of its 24 bits."""
@@ -440,3 +440,26 @@ def test_t_is_as_exact_as_an_fp32_result(hg, M, N, K, rank, order, count):
     Y = torch.empty(M, N, dtype=F32, device=DEV)
     hg.linear_adapters(X.to(DEV), W.to(DEV), Y, which.to(DEV), A.to(DEV), B.to(DEV), scales=s.to(DEV))
     assert torch.equal(Y.cpu(), T)
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 512, 512)] + PLANS)
+@pytest.mark.parametrize("rank", [1, 8, 16, 33, 60, 64])
+@pytest.mark.parametrize("order,count", [("single", 40), ("runs", 3)])
+def test_values_of_t_past_fp16(hg, M, N, K, rank, order, count):
+    """fp16: values of X·A_gᵀ past 65504, beside others of the same row within it, are finite as in the formula whatever
+    the number of rows; what is infinite stays that, in its rows."""
+    X, W, A, B, s, which, T = alone(M, N, K, rank, count, F16, order, a=30000.0, b=2.0 ** -14, spread=True)
+    # (a few rows in runs may have small values alone)
+    assert order == "runs" or ((T.abs() > 65520).any() and (T.abs() < 65504).any())
+    bad = int(which.max())
+    bad = bad if 0 < bad < count else -1
+    if bad >= 0:
+        A[bad, rank - 1, A[bad, rank - 1].float().abs().argmax()] = float("inf")
+    Y = torch.empty(M, N, dtype=F32, device=DEV)
+    hg.linear_adapters(X.to(DEV), W.to(DEV), Y, which.to(DEV), A.to(DEV), B.to(DEV), scales=s.to(DEV))
+    got, want = Y.cpu().double(), T.double() * 2.0 ** -14
+    mine = which == bad if bad >= 0 else torch.zeros(M, dtype=torch.bool)
+    assert not got[mine][:, rank - 1::rank].isfinite().any()
+    # two fp16 numbers are off by 2^-22 of T, or 2^-25; the product is exact, the sum an fp32 one
+    lim = want.abs() * (2.0 ** -22 + 2.0 ** -23) + 2.0 ** -39
+    assert ((got - want).abs() <= lim)[~mine].all()
