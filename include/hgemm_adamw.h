@@ -88,8 +88,11 @@ typedef struct hg_adamw_tensor {
  *         key = mix(key + w + 0x9E3779B9)
  *     bits = mix(element mod 2^32 ^ key)
  *
- * An infinite or NaN gradient makes its element's moments and weight NaN and no
- * other's.
+ * An infinite or NaN gradient makes its element's weight NaN and no other's; its
+ * moments are infinite or NaN then, as the sums say (8 bits: NaN).  A finite one
+ * whose square passes fp32's range (above 1.8e19, after factors) makes v
+ * infinite: with fp32 moments its weight decays and nothing else from that step
+ * on, with 8-bit ones v is NaN and so is the next step's weight.
  */
 int hg_adamw(int64_t count, const hg_adamw_tensor *tensors, int64_t step, const int64_t *device_step, double lr,
              double beta1, double beta2, double eps, double decay, const float *factors, uint64_t seed, void *stream);

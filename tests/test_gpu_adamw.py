@@ -416,3 +416,27 @@ def test_a_tiny_second_moment_beside_a_huge_one(hg, small):
         codes = v[0].cpu()
         assert codes[0] > 0x70 and (codes[1:20] == 1).all(), codes[:32]        # the least code, 2^-9 of the scale
         assert (codes[32:50] > 1).all() and not codes[20:32].any() and not codes[50:].any()
+
+
+@pytest.mark.parametrize("t,bits,master", [(F32, 32, False), (F32, 8, False), (BF16, 8, True), (BF16, 32, True)])
+def test_gradients_whose_square_leaves_fp32(hg, t, bits, master):
+    """What the header says of them, beside elements that go on as ever."""
+    b = Buffers([200], t, bits, master)
+    at, inf = [5, 40, 41, 199], 70
+    for x in (b.g, b.dev["g"]):
+        x[at], x[inf] = 2e19, -float("inf")
+    tensors = b.tensors(hg)
+    for step in (1, 2, 3):
+        hg.adamw(tensors, step, LR, (B1, B2), EPS, DECAY, seed=2)
+        before = (b.p if b.w is None else b.w)[at].float().numpy()
+        b.check(step, 2)
+        w = b.dev["p" if b.w is None else "w"].cpu().float()
+        v = b.v if bits == 32 else torch.from_numpy(values(b.v[0], b.v[1]))
+        assert w[inf].isnan() and w.isfinite().sum() == (199 if bits == 32 or step == 1 else 195)
+        if bits == 32:
+            assert v[at].isinf().all() and v[inf].isinf()
+            # (lr·decay and its product with the weight are rounded, and the result, to the param's type last)
+            want = torch.from_numpy(before * (1 - LR * DECAY))
+            assert ((w[at] - want).abs() <= 4 * U * want.abs() + (0 if t == F32 or master else ref.half(t) * want.abs())).all()
+        else:
+            assert v[at].isnan().all() and v[inf].isnan()
