@@ -463,3 +463,17 @@ def test_values_of_t_past_fp16(hg, M, N, K, rank, order, count):
     # two fp16 numbers are off by 2^-22 of T, or 2^-25; the product is exact, the sum an fp32 one
     lim = want.abs() * (2.0 ** -22 + 2.0 ** -23) + 2.0 ** -39
     assert ((got - want).abs() <= lim)[~mine].all()
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 256, 512), (300, 256, 512), (4096, 4096, 64)])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_a_row_in_two_places(hg, M, N, K, out):
+    """The same row beside other rows: both are the formula's within the bound (their last bits may differ)."""
+    X, W, A, B, s, which = operands(M, N, K, 16, 6, BF16, "single")
+    which[0] = 3
+    X[M - 1], which[M - 1] = X[0], which[0]
+    Y = hg.linear_adapters(*(x.to(DEV) for x in (X, W)), torch.empty(M, N, dtype=out, device=DEV),
+                           *(x.to(DEV) for x in (which, A, B)), scales=s.to(DEV))
+    two = [0, M - 1]
+    y, _, ey, _ = expected(X[two], W, A, B, s, which[two], None, "none", None)
+    ref.check(Y[two], y, ey, "Y")
