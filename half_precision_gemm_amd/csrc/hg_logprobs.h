@@ -11,7 +11,8 @@ namespace probs {
 
 constexpr int kThreads = 256;
 constexpr int kGroup = 8;                 // neighbouring logits that one lane loads together
-constexpr int kMostParts = 64;            // pieces of a row
+constexpr int kMostParts = 64;            // that rows are cut into to fill the GPU
+constexpr int kLongestParts = 65;         // of the longest parts in a row of 2^20 logits, wherever in a group it begins
 
 // A row's parts: `per` groups each, `groups` (1, 2, 4 or 8) for a lane of `waves` (1
 // or 4) waves.

@@ -35,7 +35,7 @@
 // logit, so in its page) counts as -inf.
 #include "hg_logprobs.h"
 
-#include "hgemm.h"
+#include "hgemm_logprobs.h"
 #include "hg_linear.h"
 
 namespace hg {
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(WAVES * 64, GR == 8 ? (TYPE == HG_F32 ? 4 : 5)
     }
 }
 
-// One wave joins a row's parts; E·64 keys at most.
+// One wave joins a row's parts, at most two to a lane; E·64 keys at most.
 template <int E, int TYPE>
 __global__ void __launch_bounds__(kThreads) join_kernel(const Forward f)
 {
@@ -696,7 +696,10 @@ hipError_t forward(const Forward &f, hipStream_t s)
     if (e != hipSuccess || f.parts.parts == 1)
         return e;
     const int keys = f.parts.parts * f.top;
-    if (f.parts.parts > 128 || keys > 33 * 64)
+    static_assert(kMostParts <= kLongestParts && kLongestParts <= 128 && kLongestParts * HG_LOGPROBS_MAX_TOP <= 33 * 64 &&
+                      (HG_LOGPROBS_MAX_VOCABULARY + 2 * kGroup - 2) / kGroup <= kLongestParts * 8 * kThreads,
+                  "");
+    if (f.parts.parts > kLongestParts)
         return hipErrorInvalidConfiguration;
     return start(keys <= 64    ? join_kernel<1, TYPE>
                  : keys <= 256 ? join_kernel<4, TYPE>

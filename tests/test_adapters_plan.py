@@ -112,3 +112,20 @@ def test_three_numbers_for_an_fp32_result(lib, M, N, K, rank):
         kernel, edge = lib.plan_launches().decode().split()[:2]
         if kernel != "rowwise":
             assert edge == "edge=%d" % (up if kernel == "shrink_wide" else -(-parts * up // 32) * 32)
+
+
+@pytest.mark.parametrize("M,N,K", [(100, 512, 512), (1000, 4096, 256), (8192, 4096, 4096), (8192, 4096, 4095), (3, 512, 512), (300, 260, 4000)])
+@pytest.mark.parametrize("rank", [1, 16, 33])
+def test_one_workspace_in_fp16(lib, M, N, K, rank):
+    """With room for what fp16 does not reach, for Y and Z of either type."""
+    X, W = mat(0, K, F16), mat(1, K, F16)
+    L = adapters.Adapters(5 * SPACE, None, 6 * SPACE, K, rank * K, 7 * SPACE, rank, N * rank, 4, rank, F16)
+    work = lib.hg_linear_adapters_workspace_size(M, N, K, rank, X, W)
+    up = -(-rank // 8) * 8
+    rows = M * up * 4 if M == 3 else M * up * 4 + M * -(-2 * up // 32) * 64
+    assert work >= rows
+    for y in (F16, F32):
+        for z in (None, F16, E4M3):
+            Z = None if z is None else mat(3, N, z)
+            assert lib.hg_linear_adapters(0, M, N, K, X, W, None, None, mat(2, N, y), Z, L, 9 * SPACE, work, None) == 0
+            assert lib.hg_linear_adapters(0, M, N, K, X, W, None, None, mat(2, N, y), Z, L, 9 * SPACE, rows - 256, None) == -13
