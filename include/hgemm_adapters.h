@@ -11,8 +11,12 @@
  * second half to their sums before anything is rounded.  One row with adapters
  * of a small rank takes one launch.
  *
- * An adapter is trained with what is there for any layer: T = X·Aᵀ and T·Bᵀ are
- * two hg_linear calls, their gradients two of hg_linear_grad.
+ * There is no backward entry point.  An adapter is trained with the layer's: T =
+ * X·Aᵀ and T·Bᵀ are two hg_linear calls on the rows that have it, their gradients
+ * two of hg_linear_grad (dB and dT = dz·B, then dA and dT·A, with dz times s_g as
+ * their dY).  What is the caller's then: rows of several adapters are taken apart
+ * first, and dX is the sum of two matrices of X's type, each rounded, dz·W (a third
+ * hg_linear_grad) and the adapters' dT·A.
  */
 #ifndef HGEMM_ADAPTERS_H
 #define HGEMM_ADAPTERS_H

@@ -477,3 +477,59 @@ def test_a_row_in_two_places(hg, M, N, K, out):
     two = [0, M - 1]
     y, _, ey, _ = expected(X[two], W, A, B, s, which[two], None, "none", None)
     ref.check(Y[two], y, ey, "Y")
+
+
+@pytest.mark.parametrize("t", [F16, BF16])
+def test_the_gradient_of_an_adapted_layer(hg, t):
+    """What the header says of a backward pass: rows of one adapter at a time, the layer's dX and the adapter's added by the
+    caller.  dX, dA and dB against the formula's and, in a direction each, against differences in 64 bits."""
+    M, N, K, rank, count = 200, 96, 160, 16, 3
+    X, W, A, B, _, which = operands(M, N, K, rank, count, t, "single", scales=False)
+    dY = torch.randn(M, N, generator=torch.Generator().manual_seed(4)).to(t)
+    new = lambda *shape, type=t: torch.empty(*shape, dtype=type, device=DEV)  # noqa: E731
+    dx = hg.linear_grad(dY.to(DEV), W.to(DEV), None, dX=new(M, K))[0].cpu()
+    dA, dB = torch.zeros(count, rank, K), torch.zeros(count, N, rank)
+    for c in range(count):
+        rows = (which == c).nonzero()[:, 0]
+        x, dy, a, b = X[rows].to(DEV), dY[rows].to(DEV), A[c].to(DEV), B[c].to(DEV)
+        T = hg.linear(x, a, new(len(rows), rank))
+        dT, db, _ = hg.linear_grad(dy, b, T, dX=new(len(rows), rank), dW=new(N, rank, type=F32))
+        more, da, _ = hg.linear_grad(dT, a, x, dX=new(len(rows), K), dW=new(rank, K, type=F32))
+        dx[rows] = (dx[rows].float() + more.cpu().float()).to(t)
+        dA[c], dB[c] = da.cpu(), db.cpu()
+
+    def z(x, a, b):
+        out = x @ W.double().t()
+        for c in range(count):
+            rows = which == c
+            out[rows] += x[rows] @ a[c].t() @ b[c].t()
+        return out
+
+    x, w, a, b, dy, h = X.double(), W.double(), A.double(), B.double(), dY.double(), ref.half(t) * 1.01
+    wx, ex = dy @ w, (N + 2) * U32 * (dy.abs() @ w.abs())
+    eA, eB = torch.zeros(count, rank, K).double(), torch.zeros(count, N, rank).double()
+    for c in range(count):
+        rows = which == c
+        xr, dr, T, dT = x[rows], dy[rows], x[rows] @ a[c].t(), dy[rows] @ b[c]
+        sT, sd = xr.abs() @ a[c].abs().t(), dr.abs() @ b[c].abs()
+        # T and dT: sums in fp32, rounded once (fp16: by 2^-25 at least)
+        eT, ed = (v.abs() * h + 1.01 * (n + 2) * U32 * s + ref.tiny(t) for v, n, s in ((T, K, sT), (dT, N, sd)))
+        eB[c] = dr.abs().t() @ eT + (M + 2) * U32 * (dr.abs().t() @ (T.abs() + eT))
+        eA[c] = ed.t() @ xr.abs() + (M + 2) * U32 * ((dT.abs() + ed).t() @ xr.abs())
+        ref.check(dB[c], dr.t() @ T, eB[c], "dB")
+        ref.check(dA[c], dT.t() @ xr, eA[c], "dA")
+        e = ed @ a[c].abs() + (rank + 2) * U32 * ((dT.abs() + ed) @ a[c].abs())
+        # two matrices rounded each
+        ex[rows] += e + h * (wx[rows].abs() + ex[rows] + (dT @ a[c]).abs() + e) + 2 * ref.tiny(t)
+        wx[rows] += dT @ a[c]
+    ref.check(dx, wx, ex, "dX")
+    g = torch.Generator().manual_seed(9)
+    # z is linear in each: differences are exact but for 64 bits' rounding
+    for got, at, err in ((dx, 0, ex), (dA, 1, eA), (dB, 2, eB)):
+        args = [x, a, b]
+        way = torch.randn(args[at].shape, generator=g, dtype=torch.float64)
+        up, down = list(args), list(args)
+        up[at], down[at] = args[at] + way, args[at] - way
+        change = ((z(*up) - z(*down)) / 2 * dy).sum()
+        last = ref.half(got.dtype) * (got.double().abs() + err) * 1.01 + ref.tiny(got.dtype)
+        assert ((got.double() * way).sum() - change).abs() <= ((err + last) * way.abs()).sum() + 1e-9
