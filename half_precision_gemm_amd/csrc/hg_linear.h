@@ -926,20 +926,28 @@ __device__ __forceinline__ void add_singly(const Adapters &a, const uint16_t *B,
 // eight with zeros for these.
 __device__ __forceinline__ u32x4 past_fp16(const u32x4 &t) { return ((t & 0x7fff7fffu) + 0x04000400u) & 0x80008000u; }
 __device__ __forceinline__ u32x4 within_fp16(const u32x4 &t, const u32x4 &past) { return t & ~((past << 1) - (past >> 15)); }
-// Sets to zero what of eights of T is not finite; whether a row with an adapter has
-// such a number, the same in all lanes.
+// Sets to zero what of the lanes' c-th eights of T is not finite; whether a row with an
+// adapter has such a number, the same in all lanes.  (Low numbers are finite, so steps
+// that hold them alone are not looked at; the largest magnitude says whether the rest
+// is needed: 2048×4096×4096 fp16, rank 64, 113.8 us without all this, 116 with the marks
+// of every eight, 114.8 as it is.)
 template <bool BF16, int N>
-__device__ __forceinline__ bool hold_back(u32x4 (&t)[N], const int (&mine)[N])
+__device__ __forceinline__ bool hold_back(u32x4 (&t)[N], const int (&mine)[N], int step, int chunks)
 {
-    if constexpr (BF16)
+    if (BF16 || 4 * step >= chunks)
         return false;
-    uint32_t any = 0;
+    using u16x2 = uint16_t __attribute__((ext_vector_type(2)));
+    u16x2 most = {0, 0};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const u32x4 past = past_fp16(t[i]);
-        any |= mine[i] >= 0 ? past[0] | past[1] | past[2] | past[3] : 0u;
+        u16x2 m = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, t[i][e] & 0x7fff7fffu));
+        const uint32_t own = mine[i] >= 0 ? __builtin_bit_cast(uint32_t, m) : 0u;
+        most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, own));
     }
-    if (__builtin_amdgcn_ballot_w64(any != 0) == 0)
+    if (__builtin_expect(__builtin_amdgcn_ballot_w64(most[0] >= 0x7c00 || most[1] >= 0x7c00) == 0, 1))
         return false;
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -1043,7 +1051,10 @@ __device__ __forceinline__ void settled(floatx4 (&v)[4])
 // take longer than one adapter after the other (us, the layer, rows in no order):
 // 1000×4096×4096, 64 adapters, 64 rows a wave: rank 16 69 for 64, 32 85 for 95, 64 147
 // for 337; 300×1024×4096, 32 rows a wave: rank 48 49 for 45, 64 55 for 59; 333×1111×777,
-// 5 adapters: rank 64 25 for 32; 383×9792×128, 45 adapters: rank 42 74 for 132.  Not
+// 5 adapters: rank 64 25 for 32; 383×9792×128, 45 adapters: rank 42 74 for 132.  Three
+// numbers a value (Y in fp32) leave the rule where it is: 64 rows a wave rank 24 96 for
+// 84, 32 96 for 102, 64 181 for 338; 32 rows a wave rank 48 61 for 45, 64 68 for 66, and
+// 333×1111×777 27 for 32.  Not
 // where rows of B lie at odd elements (1000×4096×4096, rank 33: 174 for 149).
 constexpr int kGatherFrom = 112;                    // rank times blocks of 16 rows
 template <int TI, int TJ>
@@ -1199,7 +1210,7 @@ __device__ __forceinline__ bool add_adapters(const Product &p, int row0, int col
             for (int i = 0; i < TI; ++i)
                 t[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.T) +
                                                         min(row0 + 16 * i + frow, p.M - 1) * a.ldt + 8 * c);
-            far |= hold_back<BF16>(t, mine);
+            far |= hold_back<BF16>(t, mine, s, chunks);
 #pragma unroll
             for (int i = 0; i < TI; ++i) {
                 const bool me = mine[i] == g;

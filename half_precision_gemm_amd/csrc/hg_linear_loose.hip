@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(THREADS, 2) linear_loose_kernel(const Product 
         stage_put<WT>(stg, lane, acc[i]);
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
         if constexpr (ADAPT && !BF16) {
-            if (far)
+            if (__builtin_expect(far, 0))
                 add_far<WT>(p, row0 + 16 * i, t.n0 + wn * WT, lane, stg);
             __atomic_signal_fence(__ATOMIC_SEQ_CST);
         }

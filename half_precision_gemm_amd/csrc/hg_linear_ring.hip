@@ -164,7 +164,7 @@ __device__ __forceinline__ void ring_tile(const Product &p, const Spread &w, int
         // from moving them across
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
         if constexpr (ADAPT && !BF16) {
-            if (far)
+            if (__builtin_expect(far, 0))
                 add_far<WT>(p, row0 + 16 * i, n0 + wn * WT, lane, stg);
             __atomic_signal_fence(__ATOMIC_SEQ_CST);
         }

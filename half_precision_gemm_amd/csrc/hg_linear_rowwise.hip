@@ -100,9 +100,14 @@ __device__ __forceinline__ void begin_sums(const Product &p, floatx4 (&acc)[MB][
 // `which` to A, T and B is 5 us of waits, so W's first loads are requested before
 // it, T's sums are formed behind the first stage, and what they give is added when
 // the sum over W is done.  The registers that this takes leave a CU one workgroup,
-// and every workgroup reads all of A: taken where there is one for each CU
-// (1×4096×4096 10.5 us, with the launch before 12.6; 1×16384×4096 30.9 and 29.6;
-// 2×4096×4096 in the matrix core's layout 17.2 and 12.7).
+// and every workgroup reads all of A: taken where there is one for each CU.  In
+// graphs, bf16, us, this / the launch before it, rank 8 and 16: 1×512×4096 8.0 / 9.3
+// and 8.3 / 9.6, 1×1024×1024 6.1 / 7.1 and 6.3 / 7.1, 1×2048×4096 8.3 / 10.5 and 8.6 /
+// 10.4, 1×4096×4096 8.6 / 10.6 and 9.0 / 10.6, 1×4096×14336 25.0 / 26.6 and 25.5 /
+// 26.7; with more than one workgroup for a CU 1×4608×4096 14.7 / 12.8 and 15.4 / 13.0,
+// 1×8128×4096 18.0 / 16.5 and 18.8 / 16.4.  2×4096×4096 in the matrix core's layout
+// takes 17.2 for 12.7.  Larger ranks have the launch before: 1×4096×4096 10.9 at rank
+// 32, 11.1 at 64, 1×16384×4096 26.1 at 16, 26.3 at 32, 26.7 at 64.
 struct NoSums {
     __device__ __forceinline__ NoSums(const Product &, int, int) {}
 };

@@ -152,12 +152,12 @@ __device__ __forceinline__ bool add_adapters_straight(const Product &p, int row0
             for (int j = 0; j < T; ++j)
                 ahead[j] = *reinterpret_cast<const u32x4_any *>(B + min(col0 + 16 * j + frow, p.N - 1) * a.ldb);
         };
-        request(first);
 #pragma unroll
         for (int i = 0; i < T; ++i)
             t[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.T) +
                                                     min(row0 + 16 * i + frow, p.M - 1) * a.ldt + 8 * c);
-        far |= hold_back<BF16>(t, mine);
+        request(first);
+        far |= hold_back<BF16>(t, mine, s, chunks);
         int g = first, next;
         do {
             bool bad = false;
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_tile_kernel(const Product p
             });
             __atomic_signal_fence(__ATOMIC_SEQ_CST);
             if constexpr (ADAPT && !BF16) {
-                if (far)
+                if (__builtin_expect(far, 0))
                     add_far<WT>(p, row0 + 16 * i, col0, lane, smem + stg);
                 __atomic_signal_fence(__ATOMIC_SEQ_CST);
             }
