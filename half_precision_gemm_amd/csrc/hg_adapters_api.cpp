@@ -119,17 +119,19 @@ extern "C" {
 int64_t hg_linear_adapters_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, const hg_matrix *X,
                                           const hg_matrix *W)
 {
-    // A call may have no adapters, whatever their rank, and Y of either type.
-    const int64_t alone = linear_room(M, N, K, X, W);
-    if (alone < 0 && alone > -4)
-        return alone;
+    // (for Y of either type)
+    const int most = most_tile_of(rank);
+    const int64_t need = linear_room(M, N, K, X, W, most, [&](Arena &a, const LinearPlan &q) {
+        room_of(a, M, rank, X->type, q.cut.tile == 0, parts_of(X->type, true));
+    });
+    if (need < 0 && need > -4)
+        return need;
     if (rank < 0 || rank > HG_ADAPTERS_MAX_RANK)
         return -4;
-    if (alone < 0)
-        return alone - 1;
-    return std::max(alone, linear_room(M, N, K, X, W, most_tile_of(rank), [&](Arena &a, const LinearPlan &q) {
-                        room_of(a, M, rank, X->type, q.cut.tile == 0, parts_of(X->type, true));
-                    }));
+    if (need < 0)
+        return need - 1;
+    // A call may have no adapters, whatever their rank; the layer's tiles may be larger then.
+    return most == 256 ? need : std::max(need, linear_room(M, N, K, X, W));
 }
 
 int hg_linear_adapters(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W,
