@@ -440,3 +440,36 @@ def test_gradients_whose_square_leaves_fp32(hg, t, bits, master):
             assert ((w[at] - want).abs() <= 4 * U * want.abs() + (0 if t == F32 or master else ref.half(t) * want.abs())).all()
         else:
             assert v[at].isnan().all() and v[inf].isnan()
+
+
+@pytest.mark.parametrize("t", [(1 << 32) + 5, (1 << 40) - 1])
+def test_steps_past_32_bits(hg, t):
+    """Both halves of the step's number go into the random bits; from the host and from the device."""
+    b = Buffers([3000, 65], BF16, 8, True)
+    tensors = b.tensors(hg)
+    hg.adamw(tensors, t, LR, (B1, B2), EPS, DECAY, seed=(1 << 64) - 3)
+    b.check(t, (1 << 64) - 3)
+    hg.adamw(tensors, torch.tensor([t + 1], device=DEV), LR, (B1, B2), EPS, DECAY, seed=-3)
+    b.check(t + 1, (1 << 64) - 3)
+
+
+def test_two_steps_at_once(hg):
+    """Of different tensors on two streams, over and over."""
+    bs = [Buffers([5000, 65, 33], BF16, 8, True, seed=i) for i in (0, 1)]
+    streams, tensors = [torch.cuda.Stream() for _ in bs], [b.tensors(hg) for b in bs]
+    torch.cuda.synchronize()
+    for t in range(1, 5):
+        for stream, x in zip(streams, tensors):
+            with torch.cuda.stream(stream):
+                hg.adamw(x, t, LR, (B1, B2), EPS, DECAY, seed=t)
+    torch.cuda.synchronize()
+    for b in bs:
+        dev = {k: b.dev[k] for k in "pwmv"}
+        again = Buffers([5000, 65, 33], BF16, 8, True, seed=bs.index(b))
+        x = again.tensors(hg)
+        for t in range(1, 5):
+            hg.adamw(x, t, LR, (B1, B2), EPS, DECAY, seed=t)
+            again.check(t, t)
+        for k, v in dev.items():
+            for p, q in zip(v if isinstance(v, tuple) else (v,), again.dev[k] if isinstance(v, tuple) else (again.dev[k],)):
+                assert torch.equal(p, q), k

@@ -62,3 +62,70 @@ def test_t_alone(hg, size, order, count, t):
     want = T.to(DEV).double() * (2.0 ** -14 if half else 1.0)
     lim = want.abs() * (2.0 ** -22 + 2.0 ** -23) + 2.0 ** -39 if half else 0.0
     assert ((Y.double() - want).abs() <= lim).all()
+
+
+@pytest.mark.parametrize("t,out", [(F16, F16), (BF16, F32)])
+@pytest.mark.parametrize("size", [(1, 256, 512), (33, 512, 512), (66, 100, 24), (79, 70, 2010), (4106, 71, 5056), (8294, 457, 16)])
+def test_residual_in_place(hg, size, t, out):
+    """R is Y itself."""
+    X, W, A, B, s, which = (x.to(DEV) for x in operands(*size, 16, 5, t, "single"))
+    r = torch.randn(size[:2], generator=torch.Generator().manual_seed(2)).to(out).to(DEV)
+    Y = r.clone()
+    hg.linear_adapters(X, W, Y, which, A, B, scales=s, act=hg.ACT_SILU, residual=Y)
+    y, _, ey, _ = expected(X, W, A, B, s, which, None, "silu", r)
+    ref.check(Y, y.cpu(), ey.cpu(), "Y")
+
+
+@pytest.mark.parametrize("size", [(1, 256, 512), (40, 512, 512), (300, 260, 4000), (4096, 4096, 64)])
+@pytest.mark.parametrize("t", [F16, BF16])
+def test_two_calls_at_once(hg, size, t):
+    """On two streams, a workspace each, over and over: each gets its own results."""
+    calls = []
+    for seed in (0, 1):
+        X, W, A, B, s, which = (x.to(DEV) for x in operands(*size, 16, 6, t, "single", seed=seed))
+        want = hg.linear_adapters(X, W, torch.empty(size[:2], dtype=t, device=DEV), which, A, B, scales=s)
+        calls.append((X, W, torch.empty_like(want), which, A, B, s, hg.linear_adapters_workspace(X, W, A), want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for X, W, Y, which, A, B, s, work, want, stream in calls:
+            with torch.cuda.stream(stream):
+                hg.linear_adapters(X, W, Y, which, A, B, scales=s, work=work)
+    torch.cuda.synchronize()
+    for c in calls:
+        assert torch.equal(c[2], c[8])
+
+
+@pytest.mark.parametrize("size", [(1, 256, 512), (40, 512, 512), (300, 260, 400), (4096, 4096, 64)])
+def test_numbers_that_are_no_adapter(hg, size):
+    """Any number outside 0 .. count-1, the largest and smallest of 64 bits and those that are an adapter's in their low
+    32 among them."""
+    M = size[0]
+    X, W, A, B, s, which = (x.to(DEV) for x in operands(*size, 16, 6, BF16, "single"))
+    which = which.clamp(0, 5)
+    none = torch.tensor([-1, 6, 1 << 32, (1 << 32) + 3, -(1 << 32), (1 << 63) - 1, -(1 << 63), 5 - (1 << 32), 1 << 31, -(1 << 31)],
+                        device=DEV)
+    at = torch.arange(0, M, 2, device=DEV)
+    which[at] = none[at // 2 % 10]
+    Y = torch.empty(size[:2], dtype=BF16, device=DEV)
+    hg.linear_adapters(X, W, Y, which, A, B, scales=s)
+    mine = torch.where((which >= 0) & (which < 6), which, -1)
+    y, _, ey, _ = expected(X, W, A, B, s, mine, None, "none", None)
+    ref.check(Y, y.cpu(), ey.cpu(), "Y")
+
+
+@pytest.mark.parametrize("t,out", [(F16, F16), (BF16, F32)])
+@pytest.mark.parametrize("size", [(3, 256, 512), (65, 512, 512), (333, 111, 777), (1000, 4096, 256), (4096, 4096, 64)])
+@pytest.mark.parametrize("order", ["single", "runs"])
+def test_the_largest_rank(hg, size, t, out, order):
+    run(hg, *size, 256, 5, t, order, out)
+
+
+@pytest.mark.parametrize("size", [(40, 512, 512), (300, 260, 400), (4096, 4096, 64)])
+def test_one_b_for_all(hg, size):
+    """B broadcast over the adapters, A their own, and the two together."""
+    X, W, A, B, s, which = (x.to(DEV) for x in operands(*size, 16, 6, BF16, "single"))
+    for a, b in ((A, B[:1].expand_as(B)), (A[:1].expand_as(A), B[:1].expand_as(B))):
+        Y = torch.empty(size[:2], dtype=BF16, device=DEV)
+        hg.linear_adapters(X, W, Y, which, a, b, scales=s)
+        y, _, ey, _ = expected(X, W, a, b, s, which, None, "none", None)
+        ref.check(Y, y.cpu(), ey.cpu(), "Y")
