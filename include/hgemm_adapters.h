@@ -64,11 +64,11 @@ typedef struct hg_adapters {
  * (all of its 24 bits), or of two numbers of X's type, off by at most 2^-16
  * (HG_BF16) or 2^-22 (HG_F16, and 2^-25 where that is more) of it.  In HG_F16 a
  * value that rounds past 65504 is kept in fp32 in any case (which takes longer in
- * the rows that have one).  Rows whose adapter's B_g holds
- * an infinity or NaN may come out NaN in any column.  Nothing of another row
- * enters a row's result (its last bits may differ with the rows beside it, which
- * choose the order of its sums): what is not finite in one request's row or
- * adapter stays in that request's rows.
+ * the rows that have one).  Rows whose adapter's B_g holds an infinity or NaN may
+ * come out NaN in any column.  Nothing of another row enters a row's result (its
+ * last bits may differ with the rows beside it, which choose the order of its
+ * sums): what is not finite in one request's row or adapter stays in that
+ * request's rows.
  */
 int hg_linear_adapters(int act, int64_t M, int64_t N, int64_t K, const hg_matrix *X, const hg_matrix *W,
                        const float *bias, const hg_matrix *R, const hg_matrix *Y, const hg_matrix *Z,
